@@ -79,6 +79,7 @@ extern "C" {
 #define PKV_DEVERR_CONTEXT_LEN  0x4   /* context_len < 0 or > max_blocks_per_seq * block_size */
 #define PKV_DEVERR_QUERY_LEN    0x8   /* q_len < 0 or q_len > context_len */
 #define PKV_DEVERR_TIMEOUT      0x10  /* a pipeline wait gave up (internal fault) */
+#define PKV_DEVERR_FREE_BLOCKS  0x20  /* a step needs more blocks than its free list holds */
 
 /* ---- dtypes --------------------------------------------------------------- */
 #define PKV_DTYPE_BF16 0
@@ -90,6 +91,9 @@ extern "C" {
 /* ---- ops for pkv_workspace_size ------------------------------------------- */
 #define PKV_OP_DECODE 0
 #define PKV_OP_VARLEN 1
+/* ---- ops for pkv_latent_workspace_size ------------------------------------- */
+#define PKV_OP_LATENT_ABSORBED 2
+#define PKV_OP_LATENT_EXPANDED 3
 
 /*
  * KV write ("reshape_and_cache").  [LPNH] §2.2 pool layout; [LESSON] "PagedAttention
@@ -297,6 +301,92 @@ int pkv_paged_attention_decode_static(void *out, const void *q, const void *k_ca
  */
 int pkv_copy_to_device(void *dst, const void *src, size_t bytes, void *stream);
 int pkv_copy_to_host(void *dst, const void *src, size_t bytes, void *stream);
+
+/*
+ * Step metadata on the device: what the host side of an iteration otherwise computes and
+ * copies (context lengths, query offsets, the growth of the block tables, the slot map),
+ * from the lengths of the requests, so that a step needs no host data and can be captured
+ * once and replayed.  All arguments but the sizes are device memory.
+ *   cached_lens [num_seqs]   tokens of each sequence already in the cache
+ *   new_lens    [num_seqs]   its new tokens in this step (0: it takes no part)
+ *   block_tables             entries of the blocks that hold the cached tokens on entry; the
+ *                            entries of blocks the new tokens open are written
+ *   free_blocks [num_free]   ids the step may take, from index free_begin[0] on
+ * Writes, with bs = block_size:
+ *   context_lens[s]    = cached_lens[s] + new_lens[s]
+ *   query_start_loc[s] = new_lens[0] + .. + new_lens[s - 1]            (num_seqs + 1 entries)
+ *   block_tables       a sequence gains ceil(context / bs) - ceil(cached / bs) blocks, taken
+ *                      from the free list in sequence order (deterministic)
+ *   slot_mapping[t]    the slot of new token t, as pkv_slot_mapping gives it; -1 for
+ *                      query_start_loc[num_seqs] <= t < num_slots
+ *   free_end[0]        = free_begin[0] + blocks taken
+ * context_lens may be cached_lens itself and free_end free_begin itself: every length is read
+ * before anything is written, so a replayed step advances its own state.  No other arrays may
+ * overlap.
+ * A sequence with a negative length, or whose tokens exceed max_blocks_per_seq * block_size,
+ * takes no part and is flagged (PKV_DEVERR_QUERY_LEN for new_lens < 0, else
+ * PKV_DEVERR_CONTEXT_LEN); its context_lens entry is its cached_lens entry.  A step with more
+ * than num_slots tokens (PKV_DEVERR_QUERY_LEN), or that needs more blocks than the list holds
+ * from free_begin on (PKV_DEVERR_FREE_BLOCKS), is refused whole: no block is taken, every
+ * offset is 0, every slot -1 and context_lens = cached_lens.  A block id outside
+ * [0, num_blocks) is flagged PKV_DEVERR_BLOCK_ID; a fresh one becomes the table entry -1, and
+ * tokens in such a block get slot -1.
+ * Supported: block_size 8, 16, 32 or 64, num_seqs <= 16384, num_slots, num_free, num_blocks
+ * and max_blocks_per_seq * block_size < 2^31.
+ */
+int pkv_step_metadata(int32_t *block_tables, int32_t *context_lens, int32_t *query_start_loc,
+                      int64_t *slot_mapping, int32_t *free_end, const int32_t *cached_lens,
+                      const int32_t *new_lens, const int32_t *free_blocks, const int32_t *free_begin,
+                      int num_seqs, int max_blocks_per_seq, int64_t num_slots, int64_t num_free,
+                      int64_t num_blocks, int block_size, void *stream);
+
+/*
+ * Latent attention: keys and values of all heads come from one shared row a token,
+ *   latent_cache [num_blocks, block_size, latent_dim + rope_dim]  bf16,
+ * the token's latent vector c (latent_dim values) followed by its rotary key part r (rope_dim
+ * values, position already applied).  Head h's key is [W_k[h] c ; r] and its value W_v[h] c.
+ * Block tables, context lengths, causal masking, workspaces and error flags are those of the
+ * paged calls above.
+ *
+ * pkv_latent_cache_write: for each token t with slot = slot_mapping[t] >= 0, the row of that
+ * slot becomes [latent[t] ; rope[t]] (latent [num_tokens, latent_dim], rope [num_tokens,
+ * rope_dim], bf16).  Bit-exact; negative slots are skipped, slots outside the pool skipped and
+ * flagged PKV_DEVERR_SLOT; two tokens with the same slot race.
+ * Supported: dtype PKV_DTYPE_BF16, latent_dim and rope_dim multiples of 8, at most 65536.
+ */
+int pkv_latent_cache_write(void *latent_cache, const void *latent, const void *rope,
+                           const int64_t *slot_mapping, int64_t num_tokens, int64_t num_blocks, int block_size,
+                           int latent_dim, int rope_dim, int dtype, void *stream);
+
+/*
+ * Absorbed form: the caller has folded W_k into the query (q_nope W_k[h], latent_dim columns,
+ * then the rotary columns) and applies W_v to the output, so a cached row serves as the key
+ * and, in its first latent_dim columns, as the value of every head:
+ *     out[i][h] = softmax_j(scale * q[i][h] . [c_j ; r_j]) c_j
+ *   q [total_q_tokens, num_heads, latent_dim + rope_dim], out [total_q_tokens, num_heads,
+ *   latent_dim], bf16.
+ * query_start_loc NULL: one query row per sequence (total_q_tokens = num_seqs), context_lens
+ * 0 gives a zero row.  Otherwise sequence s owns rows query_start_loc[s] ..
+ * query_start_loc[s + 1] - 1, its last q_len positions (verification of drafted tokens, short
+ * chunks), masked as in pkv_paged_attention_varlen; a sequence whose metadata is bad gets zero
+ * rows, and rows behind query_start_loc[num_seqs] are left as they were.  Cache rows at or past
+ * a context are never read as values.  The softmax weights are rounded to bf16 for the product
+ * with the latents; sums are fp32.
+ * Supported: dtype PKV_DTYPE_BF16, latent_dim 256 or 512, rope_dim 64, block_size 8, 16, 32 or
+ * 64, any num_heads with total_q_tokens * num_heads < 2^31 - 128, 0 < scale < infinity.
+ * Workspace: pkv_latent_workspace_size(PKV_OP_LATENT_ABSORBED, ...), 256-byte aligned.
+ */
+int pkv_latent_attention_absorbed(void *out, const void *q, const int32_t *query_start_loc,
+                                  const void *latent_cache, const int32_t *block_tables,
+                                  const int32_t *context_lens, int num_seqs, int total_q_tokens,
+                                  int max_blocks_per_seq, int num_heads, int latent_dim, int rope_dim,
+                                  int block_size, int64_t num_blocks, float scale, int causal, int dtype,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of a latent-attention call on the current device for these sizes (0 if
+ * they are unsupported).  total_context is used by PKV_OP_LATENT_EXPANDED only. */
+size_t pkv_latent_workspace_size(int op, int num_seqs, int total_q_tokens, int64_t total_context,
+                                 int num_heads, int latent_dim, int rope_dim);
 
 /*
  * Limit, in nanoseconds, of every pipeline wait inside the attention kernels launched

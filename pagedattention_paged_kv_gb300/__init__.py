@@ -9,7 +9,11 @@ Calls (names as in the C ABI, without the ``pkv_`` prefix):
   reshape_and_cache         KV write through a slot mapping
   paged_attention_decode    one query row per sequence
   paged_attention_varlen    ragged batch: prefill chunks and decodes in one call
+  step_metadata             a step's lengths, offsets, block tables and slot map, on the device
+  latent_cache_write        latent rows into the block-paged latent cache
+  latent_attention_absorbed attention over the latent cache, projections folded into q and out
   workspace_size            device scratch the attention calls need
+  latent_workspace_size     the same for the latent-attention calls
   get_device_error          flags the kernels raised on bad device metadata
   slot_mapping              host: slot of each new token from the block tables
   BlockManager              host: free-list allocator of physical block ids
@@ -24,6 +28,8 @@ import numpy as np
 BLOCK_SIZE = 16
 OP_DECODE = 0
 OP_VARLEN = 1
+OP_LATENT_ABSORBED = 2
+OP_LATENT_EXPANDED = 3
 DTYPE_BF16 = 0
 DTYPE_FP8_E4M3 = 1
 
@@ -36,6 +42,7 @@ DEVERR_BLOCK_ID = 0x2
 DEVERR_CONTEXT_LEN = 0x4
 DEVERR_QUERY_LEN = 0x8
 DEVERR_TIMEOUT = 0x10
+DEVERR_FREE_BLOCKS = 0x20
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpagedkv.so")
@@ -84,6 +91,11 @@ def lib() -> ctypes.CDLL:
         L.pkv_set_decode_split.restype = None
         L.pkv_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
         L.pkv_workspace_size.restype = sz
+        L.pkv_step_metadata.argtypes = [vp] * 9 + [i32, i32, i64, i64, i64, i32, vp]
+        L.pkv_latent_cache_write.argtypes = [vp, vp, vp, vp, i64, i64, i32, i32, i32, i32, vp]
+        L.pkv_latent_attention_absorbed.argtypes = [vp] * 6 + [i32] * 7 + [i64, f32, i32, i32, vp, sz, vp]
+        L.pkv_latent_workspace_size.argtypes = [i32, i32, i32, i64, i32, i32, i32]
+        L.pkv_latent_workspace_size.restype = sz
         L.pkv_status_string.argtypes = [i32]
         L.pkv_status_string.restype = ctypes.c_char_p
         L.pkv_get_device_error.argtypes = [vp]
@@ -101,7 +113,8 @@ def lib() -> ctypes.CDLL:
                      "pkv_block_manager_allocate", "pkv_block_manager_free", "pkv_copy_blocks",
                      "pkv_block_manager_share", "pkv_block_manager_ref_count",
                      "pkv_block_manager_copy_on_write", "pkv_paged_attention_decode_kvwrite",
-                     "pkv_paged_attention_decode_kvwrite_fp8", "pkv_copy_to_device", "pkv_copy_to_host"):
+                     "pkv_paged_attention_decode_kvwrite_fp8", "pkv_copy_to_device", "pkv_copy_to_host",
+                     "pkv_step_metadata", "pkv_latent_cache_write", "pkv_latent_attention_absorbed"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -315,6 +328,123 @@ def paged_attention_decode_kvwrite(out, q, k_new, v_new, k_cache, v_cache, block
                "paged_attention_decode_kvwrite_fp8")
     else:
         _check(lib().pkv_paged_attention_decode_kvwrite(*args, DTYPE_BF16, *tail), "paged_attention_decode_kvwrite")
+
+
+def _on_current_device(*tensors):
+    """The library launches on the current device: tensors of another one are refused."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _call_workspace(workspace, nbytes, like, stream):
+    """The caller's workspace (a contiguous CUDA buffer of enough bytes), or a fresh one that
+    stays alive until `stream` is past the call."""
+    import torch
+    if workspace is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        if stream is not None:
+            ws.record_stream(stream)
+        return ws
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    _on_current_device(workspace)
+    return _workspace(workspace, nbytes, like.device)
+
+
+def step_metadata(block_tables, context_lens, query_start_loc, slot_mapping, free_end, cached_lens, new_lens,
+                  free_blocks, free_begin, num_blocks: int, block_size: int = BLOCK_SIZE, stream=None) -> None:
+    """A step's metadata from its lengths, on the device: cached_lens/new_lens [S] int32,
+    free_blocks [F] int32 taken from index free_begin [1] int32 on -> context_lens [S],
+    query_start_loc [S + 1], free_end [1] int32, slot_mapping [room] int64 (-1 past the last
+    token), and the new entries of block_tables [S, MB] int32.  context_lens may be cached_lens
+    and free_end may be free_begin: a replayed call then advances its own state."""
+    import torch
+    i32 = torch.int32
+    _require(block_tables, i32, "block_tables", 2)
+    for t, n in ((context_lens, "context_lens"), (query_start_loc, "query_start_loc"), (free_end, "free_end"),
+                 (cached_lens, "cached_lens"), (new_lens, "new_lens"), (free_blocks, "free_blocks"),
+                 (free_begin, "free_begin")):
+        _require(t, i32, n, 1)
+    _require(slot_mapping, torch.int64, "slot_mapping", 1)
+    _on_current_device(block_tables, context_lens, query_start_loc, slot_mapping, free_end, cached_lens, new_lens,
+                       free_blocks, free_begin)
+    S = cached_lens.shape[0]
+    if new_lens.shape[0] != S or context_lens.shape[0] != S or block_tables.shape[0] != S \
+            or query_start_loc.shape[0] != S + 1 or free_end.shape[0] != 1 or free_begin.shape[0] != 1:
+        raise ValueError("shape mismatch")
+    _check(lib().pkv_step_metadata(
+        _ptr(block_tables), _ptr(context_lens), _ptr(query_start_loc), _ptr(slot_mapping), _ptr(free_end),
+        _ptr(cached_lens), _ptr(new_lens), _ptr(free_blocks), _ptr(free_begin), S, block_tables.shape[1],
+        slot_mapping.shape[0], free_blocks.shape[0], int(num_blocks), int(block_size), _stream_ptr(stream)),
+        "step_metadata")
+
+
+def latent_cache_write(latent_cache, latent, rope, slot_mapping, stream=None) -> None:
+    """latent_cache [NB, bs, R + P] bf16 <- rows [latent ; rope] (latent [T, R], rope [T, P] bf16)
+    at int64 slot_mapping [T]; negative slots are skipped."""
+    import torch
+    _require(latent_cache, torch.bfloat16, "latent_cache", 3)
+    _require(latent, torch.bfloat16, "latent", 2)
+    _require(rope, torch.bfloat16, "rope", 2)
+    _require(slot_mapping, torch.int64, "slot_mapping", 1)
+    _on_current_device(latent_cache, latent, rope, slot_mapping)
+    NB, bs, cols = latent_cache.shape
+    T, R = latent.shape
+    if rope.shape[0] != T or slot_mapping.shape[0] != T or R + rope.shape[1] != cols:
+        raise ValueError("shape mismatch")
+    _check(lib().pkv_latent_cache_write(_ptr(latent_cache), _ptr(latent), _ptr(rope), _ptr(slot_mapping), T, NB, bs,
+                                        R, rope.shape[1], DTYPE_BF16, _stream_ptr(stream)), "latent_cache_write")
+
+
+def latent_workspace_size(op: int, num_seqs: int, total_q_tokens: int, num_heads: int, latent_dim: int,
+                          rope_dim: int, total_context: int = 0) -> int:
+    n = lib().pkv_latent_workspace_size(op, num_seqs, total_q_tokens, int(total_context), num_heads, latent_dim,
+                                        rope_dim)
+    if n == 0:
+        raise PagedKVError(-2, "latent_workspace_size")
+    return int(n)
+
+
+def _latent_common(out, q, latent_cache, block_tables, context_lens, query_start_loc):
+    import torch
+    _require(out, torch.bfloat16, "out", 3)
+    _require(q, torch.bfloat16, "q", 3)
+    _require(latent_cache, torch.bfloat16, "latent_cache", 3)
+    _require(block_tables, torch.int32, "block_tables", 2)
+    _require(context_lens, torch.int32, "context_lens", 1)
+    if query_start_loc is not None:
+        _require(query_start_loc, torch.int32, "query_start_loc", 1)
+    _on_current_device(out, q, latent_cache, block_tables, context_lens, query_start_loc)
+    S = context_lens.shape[0]
+    if tuple(out.shape[:2]) != tuple(q.shape[:2]) or block_tables.shape[0] != S \
+            or (query_start_loc is not None and query_start_loc.shape[0] != S + 1) \
+            or (query_start_loc is None and q.shape[0] != S):
+        raise ValueError("shape mismatch")
+    return S
+
+
+def latent_attention_absorbed(out, q, latent_cache, block_tables, context_lens, scale: float, query_start_loc=None,
+                              causal: bool = True, workspace=None, stream=None) -> None:
+    """Latent attention with the projections absorbed: q [T, H, R + P] bf16 (q_nope W_k, then the
+    rotary part), out [T, H, R] bf16 (to be multiplied by W_v), latent_cache [NB, bs, R + P] bf16,
+    block_tables [S, MB] int32, context_lens [S] int32.  Without query_start_loc one row per
+    sequence; with it [S + 1] int32 (device), each sequence's last q_len positions."""
+    S = _latent_common(out, q, latent_cache, block_tables, context_lens, query_start_loc)
+    T, H, cols = q.shape
+    NB, bs, ccols = latent_cache.shape
+    R = out.shape[2]
+    if ccols != cols or cols <= R:
+        raise ValueError("shape mismatch")
+    n = latent_workspace_size(OP_LATENT_ABSORBED, S, T, H, R, cols - R)
+    ws = _call_workspace(workspace, n, q, stream)
+    _check(lib().pkv_latent_attention_absorbed(
+        _ptr(out), _ptr(q), _ptr(query_start_loc) if query_start_loc is not None else None, _ptr(latent_cache),
+        _ptr(block_tables), _ptr(context_lens), S, T, block_tables.shape[1], H, R, cols - R, bs, NB, float(scale),
+        int(bool(causal)), DTYPE_BF16, _ptr(ws), ws.numel() * ws.element_size(), _stream_ptr(stream)),
+        "latent_attention_absorbed")
 
 
 def copy_blocks(k_cache, v_cache, block_pairs, stream=None) -> None:

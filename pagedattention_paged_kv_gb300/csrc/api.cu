@@ -11,6 +11,7 @@
 #include <atomic>
 
 #include "../../include/pagedkv.h"
+#include "api_common.h"
 #include "paged_decode.cuh"
 #include "paged_prefill.cuh"
 #include "paged_varlen.cuh"
@@ -283,6 +284,34 @@ int run_decode(void *out, const void *q, const int32_t *query_start_loc, int tot
 }
 
 }  // namespace
+
+namespace pkv {
+
+int current_device(DeviceFacts *out) {
+    DeviceInfo *d = nullptr;
+    const int st = device_info(&d);
+    if (st == PKV_OK) *out = DeviceFacts{d->sms, d->smem_optin, d->err};
+    return st;
+}
+
+int encode_tiled(CUtensorMap *map, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
+                 const uint32_t *box) {
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], one[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base),
+                                d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
+}
+
+uint64_t wait_limit_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
+
+}  // namespace pkv
 
 extern "C" const char *pkv_status_string(int status) {
     switch (status) {

@@ -1,0 +1,185 @@
+// latent_api.cu -- the extern "C" entry points of the latent-attention operators and of the
+// step metadata (declared in include/pagedkv.h): argument checks, tensor maps, launches.
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/pagedkv.h"
+#include "api_common.h"
+#include "latent_absorbed.cuh"
+#include "step_metadata.cuh"
+
+namespace pkv {
+cudaError_t launch_latent_cache_write(void *cache, const void *latent, const void *rope,
+                                      const int64_t *slot_mapping, int64_t num_tokens, int64_t num_slots,
+                                      int latent_bytes, int rope_bytes, int num_sms, int *err,
+                                      cudaStream_t stream);
+}
+
+using pkv::aligned_to;
+using pkv::round_up_to;
+
+namespace {
+
+// log2 of a supported block size, or -1.
+int block_shift(int block_size) {
+    return block_size == 8 ? 3 : block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : -1;
+}
+
+int check_latent(int num_seqs, int total_q, int max_blocks_per_seq, int num_heads, int latent_dim, int rope_dim,
+                 int block_size, int64_t num_blocks, int dtype) {
+    if (num_seqs < 0 || total_q < 0 || max_blocks_per_seq < 0 || num_heads <= 0 || latent_dim <= 0 ||
+        rope_dim <= 0 || block_size <= 0 || num_blocks < 0)
+        return PKV_ERR_INVALID_ARG;
+    if (dtype != PKV_DTYPE_BF16) return PKV_ERR_UNSUPPORTED;
+    if ((latent_dim != 256 && latent_dim != 512) || rope_dim != pkv::kRopeDim || block_shift(block_size) < 0)
+        return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)total_q * num_heads > (int64_t)INT32_MAX - 128 || num_blocks > INT32_MAX ||
+        (int64_t)max_blocks_per_seq * block_size > INT32_MAX)
+        return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+// The cache as (64 columns, token in block, 64-column chunk, block): a box of 8 tokens x all
+// chunks lands as [chunk][token][64 columns].
+int encode_latent_map(CUtensorMap *map, const void *cache, int64_t num_blocks, int block_size, int row_cols) {
+    const uint64_t row = (uint64_t)row_cols * 2;
+    const uint64_t dims[4] = {64, (uint64_t)block_size, (uint64_t)(row_cols / 64), (uint64_t)num_blocks};
+    const uint64_t strides[3] = {row, 128, row * block_size};
+    const uint32_t box[4] = {64, 8, (uint32_t)(row_cols / 64), 1};
+    return pkv::encode_tiled(map, 4, cache, dims, strides, box);
+}
+
+}  // namespace
+
+extern "C" int pkv_step_metadata(int32_t *block_tables, int32_t *context_lens, int32_t *query_start_loc,
+                                 int64_t *slot_mapping, int32_t *free_end, const int32_t *cached_lens,
+                                 const int32_t *new_lens, const int32_t *free_blocks, const int32_t *free_begin,
+                                 int num_seqs, int max_blocks_per_seq, int64_t num_slots, int64_t num_free,
+                                 int64_t num_blocks, int block_size, void *stream) {
+    if (num_seqs < 0 || max_blocks_per_seq < 0 || num_slots < 0 || num_free < 0 || num_blocks < 0 ||
+        block_size <= 0)
+        return PKV_ERR_INVALID_ARG;
+    const int shift = block_shift(block_size);
+    if (shift < 0 || num_seqs > pkv::kStepMaxSeqs || num_slots > INT32_MAX || num_free > INT32_MAX ||
+        num_blocks > INT32_MAX || (int64_t)max_blocks_per_seq * block_size > INT32_MAX)
+        return PKV_ERR_UNSUPPORTED;
+    if (!query_start_loc || !free_end || !free_begin || (num_seqs > 0 && (!context_lens || !cached_lens || !new_lens)) ||
+        (num_seqs > 0 && max_blocks_per_seq > 0 && !block_tables) || (num_slots > 0 && !slot_mapping) ||
+        (num_free > 0 && !free_blocks))
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned_to(slot_mapping, 8)) return PKV_ERR_INVALID_ARG;
+    pkv::DeviceFacts d;
+    const int st = pkv::current_device(&d);
+    if (st != PKV_OK) return st;
+    pkv::StepArgs a;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.query_start_loc = query_start_loc;
+    a.slot_mapping = slot_mapping;
+    a.free_end = free_end;
+    a.cached_lens = cached_lens;
+    a.new_lens = new_lens;
+    a.free_blocks = free_blocks;
+    a.free_begin = free_begin;
+    a.num_seqs = num_seqs;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.block_shift = shift;
+    a.num_slots = num_slots;
+    a.num_free = num_free;
+    a.num_blocks = num_blocks;
+    a.err = d.err;
+    return pkv::launch_step_metadata(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+extern "C" int pkv_latent_cache_write(void *latent_cache, const void *latent, const void *rope,
+                                      const int64_t *slot_mapping, int64_t num_tokens, int64_t num_blocks,
+                                      int block_size, int latent_dim, int rope_dim, int dtype, void *stream) {
+    if (num_tokens < 0 || num_blocks < 0 || block_size <= 0 || latent_dim <= 0 || rope_dim <= 0)
+        return PKV_ERR_INVALID_ARG;
+    if (dtype != PKV_DTYPE_BF16 || latent_dim % 8 != 0 || rope_dim % 8 != 0 || latent_dim > 65536 ||
+        rope_dim > 65536)
+        return PKV_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PKV_OK;
+    if (!latent_cache || !latent || !rope || !slot_mapping) return PKV_ERR_INVALID_ARG;
+    if (!aligned_to(latent_cache, 16) || !aligned_to(latent, 16) || !aligned_to(rope, 16) ||
+        !aligned_to(slot_mapping, 8))
+        return PKV_ERR_INVALID_ARG;
+    pkv::DeviceFacts d;
+    const int st = pkv::current_device(&d);
+    if (st != PKV_OK) return st;
+    return pkv::launch_latent_cache_write(latent_cache, latent, rope, slot_mapping, num_tokens,
+                                          num_blocks * block_size, latent_dim * 2, rope_dim * 2, d.sms, d.err,
+                                          static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+extern "C" size_t pkv_latent_workspace_size(int op, int num_seqs, int total_q_tokens, int64_t total_context,
+                                            int num_heads, int latent_dim, int rope_dim) {
+    if (check_latent(num_seqs, total_q_tokens, 0, num_heads, latent_dim, rope_dim, 16, 0, PKV_DTYPE_BF16) != PKV_OK ||
+        total_context < 0)
+        return 0;
+    pkv::DeviceFacts d;
+    if (pkv::current_device(&d) != PKV_OK) return 0;
+    if (op == PKV_OP_LATENT_ABSORBED) {
+        pkv::AbsorbedPlan p;
+        pkv::plan_absorbed(latent_dim, d.sms, &p);
+        return p.ws_bytes;
+    }
+    return 0;
+}
+
+extern "C" int pkv_latent_attention_absorbed(void *out, const void *q, const int32_t *query_start_loc,
+                                             const void *latent_cache, const int32_t *block_tables,
+                                             const int32_t *context_lens, int num_seqs, int total_q_tokens,
+                                             int max_blocks_per_seq, int num_heads, int latent_dim, int rope_dim,
+                                             int block_size, int64_t num_blocks, float scale, int causal,
+                                             int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    int st = check_latent(num_seqs, total_q_tokens, max_blocks_per_seq, num_heads, latent_dim, rope_dim, block_size,
+                          num_blocks, dtype);
+    if (st != PKV_OK) return st;
+    if (!(scale > 0.f) || scale == INFINITY) return PKV_ERR_INVALID_ARG;
+    if (!query_start_loc && total_q_tokens != num_seqs) return PKV_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_q_tokens == 0) return PKV_OK;
+    if (!out || !q || !latent_cache || !block_tables || !context_lens) return PKV_ERR_INVALID_ARG;
+    if (!aligned_to(out, 16) || !aligned_to(q, 16) || !aligned_to(latent_cache, 16)) return PKV_ERR_INVALID_ARG;
+    if (num_blocks == 0 || max_blocks_per_seq == 0) return PKV_ERR_INVALID_ARG;
+    pkv::DeviceFacts d;
+    st = pkv::current_device(&d);
+    if (st != PKV_OK) return st;
+    pkv::AbsorbedPlan p;
+    pkv::plan_absorbed(latent_dim, d.sms, &p);
+    if (!workspace || workspace_bytes < p.ws_bytes) return PKV_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned_to(workspace, 256)) return PKV_ERR_INVALID_ARG;
+    const int cols = latent_dim + rope_dim;
+    CUtensorMap qmap, kvmap;
+    const uint64_t qdims[2] = {(uint64_t)cols, (uint64_t)total_q_tokens * num_heads};
+    const uint64_t qstride[1] = {(uint64_t)cols * 2};
+    const uint32_t qbox[2] = {64, (uint32_t)pkv::kLatentRows};
+    st = pkv::encode_tiled(&qmap, 2, q, qdims, qstride, qbox);
+    if (st == PKV_OK) st = encode_latent_map(&kvmap, latent_cache, num_blocks, block_size, cols);
+    if (st != PKV_OK) return st;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    pkv::AbsorbedArgs a;
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.query_start_loc = query_start_loc;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.num_seqs = num_seqs;
+    a.total_q = total_q_tokens;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.block_shift = block_shift(block_size);
+    a.num_heads = num_heads;
+    a.grid = p.grid;
+    a.causal = causal != 0;
+    a.num_blocks = num_blocks;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.ws_jobs = reinterpret_cast<pkv::MergeJob *>(ws + p.off_jobs);
+    a.ws_ml = reinterpret_cast<float2 *>(ws + p.off_ml);
+    a.ws_o = reinterpret_cast<float *>(ws + p.off_o);
+    a.err = d.err;
+    a.wait_ns = pkv::wait_limit_ns();
+    return pkv::launch_latent_absorbed(latent_dim, qmap, kvmap, a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}

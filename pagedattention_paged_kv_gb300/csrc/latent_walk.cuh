@@ -1,0 +1,181 @@
+// latent_walk.cuh -- how the latent-attention kernels read a ragged batch: one sequence's
+// lengths with their checks, the block-wide sum of every sequence's work units, and a
+// warp's walk over the sequences of its CTA's share.  No per-sequence table is kept in
+// shared memory, which the tiles need.
+#pragma once
+
+#include "pkv_common.cuh"
+
+namespace pkv {
+
+struct SeqBatch {
+    const int32_t *query_start_loc;  // null: sequence s has the one query row s
+    const int32_t *context_lens;
+    int num_seqs;
+    int total_q;                     // rows of q and out
+    int64_t max_context;             // positions a block-table row can hold
+    int *err;
+};
+
+// A sequence's lengths.  q_len = 0: nothing to compute.  dead: its rows are inside the
+// output but there is nothing valid to compute (idle, or bad metadata): zero rows.
+struct SeqInfo {
+    int ctx, q0, q_len;
+    bool dead;
+};
+
+__device__ __forceinline__ SeqInfo read_seq(const SeqBatch &b, int s, bool report) {
+    SeqInfo r;
+    const int64_t q0 = b.query_start_loc ? b.query_start_loc[s] : s;
+    const int64_t q1 = b.query_start_loc ? b.query_start_loc[s + 1] : s + 1;
+    r.q0 = (int)q0;
+    r.q_len = 0;
+    r.ctx = 0;
+    r.dead = false;
+    if (q0 < 0 || q1 < q0 || q1 > b.total_q) {
+        if (report) flag_error(b.err, PKV_DEVERR_QUERY_LEN);
+        return r;
+    }
+    if (q1 == q0) return r;
+    r.q_len = (int)(q1 - q0);
+    r.ctx = b.context_lens[s];
+    if (r.ctx < 0 || r.ctx > b.max_context) {
+        if (report) flag_error(b.err, PKV_DEVERR_CONTEXT_LEN);
+        r.dead = true;
+    } else if (r.q_len > r.ctx) {
+        // an idle slot of a decode batch (context 0) is no error
+        if (report && b.query_start_loc) flag_error(b.err, PKV_DEVERR_QUERY_LEN);
+        r.dead = true;
+    }
+    return r;
+}
+
+// Units(const SeqInfo &) -> int64_t gives the work units of a live sequence.
+template <typename Units>
+__device__ __forceinline__ int64_t seq_units_of(const SeqBatch &b, const Units &units, int s, bool report) {
+    const SeqInfo q = read_seq(b, s, report);
+    return q.q_len == 0 || q.dead ? 0 : units(q);
+}
+
+// The threads of a block take equal runs of consecutive sequences; run = units before this
+// thread's first one.
+struct BatchScan {
+    int beg, end;
+    int64_t run, local, total;
+};
+
+// Whole block; tmp holds one entry per warp.  Ends with __syncthreads.
+template <typename Units>
+__device__ __forceinline__ BatchScan scan_batch(const SeqBatch &b, const Units &units, int64_t *tmp,
+                                                bool report) {
+    BatchScan r;
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+    const int per = (b.num_seqs + nt - 1) / nt;
+    r.beg = min(b.num_seqs, tid * per);
+    r.end = min(b.num_seqs, r.beg + per);
+    r.local = 0;
+    for (int s = r.beg; s < r.end; ++s) r.local += seq_units_of(b, units, s, report);
+    int64_t x = r.local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) tmp[warp] = x;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int i = 0; i < nw; ++i) {
+        const int64_t v = tmp[i];
+        if (i < warp) before += v;
+        total += v;
+    }
+    r.run = before + x - r.local;
+    r.total = total;
+    __syncthreads();
+    return r;
+}
+
+// The sequence that holds unit f and the units before it: the one thread whose run holds f
+// writes them.  Callers synchronise afterwards.
+template <typename Units>
+__device__ __forceinline__ void find_unit(const SeqBatch &b, const Units &units, const BatchScan &sc, int64_t f,
+                                          int *seq, int64_t *pre) {
+    if (f < sc.run || f >= sc.run + sc.local) return;
+    int64_t run = sc.run;
+    for (int s = sc.beg; s < sc.end; ++s) {
+        const int64_t u = seq_units_of(b, units, s, false);
+        if (f < run + u) {
+            *seq = s;
+            *pre = run;
+            return;
+        }
+        run += u;
+    }
+}
+
+// A warp's walk over the sequences from a starting one on, 32 sequences to a round of loads.
+// Every call is warp-wide; the current sequence's data is uniform.
+template <typename Units>
+struct SeqWalk {
+    int base;          // sequence of lane 0
+    int s;             // current sequence
+    int64_t pre;       // units before it
+    int64_t units;     // its units (> 0)
+    SeqInfo q;
+    SeqInfo mine;      // this lane's sequence
+    int64_t my_units;
+
+    __device__ __forceinline__ void load(const SeqBatch &b, const Units &u, int first) {
+        base = first;
+        const int i = first + (int)(threadIdx.x & 31);
+        my_units = 0;
+        mine.ctx = mine.q0 = mine.q_len = 0;
+        if (i < b.num_seqs) {
+            mine = read_seq(b, i, false);
+            if (mine.q_len > 0 && !mine.dead) my_units = u(mine);
+        }
+    }
+    __device__ __forceinline__ void take(int l) {
+        s = base + l;
+        q.ctx = __shfl_sync(0xffffffffu, mine.ctx, l);
+        q.q0 = __shfl_sync(0xffffffffu, mine.q0, l);
+        q.q_len = __shfl_sync(0xffffffffu, mine.q_len, l);
+        q.dead = false;
+        units = __shfl_sync(0xffffffffu, my_units, l);
+    }
+    __device__ __forceinline__ void start(const SeqBatch &b, const Units &u, int seq, int64_t before) {
+        load(b, u, seq);
+        pre = before;
+        take(0);
+    }
+    // Moves on until the current sequence holds unit f (f >= pre, f below the batch's total).
+    __device__ __forceinline__ void seek(const SeqBatch &b, const Units &u, int64_t f) {
+        while (f >= pre + units) {
+            pre += units;
+            unsigned later = 0;
+            const int at = s - base;
+            later = __ballot_sync(0xffffffffu, my_units > 0) & (at >= 31 ? 0u : 0xffffffffu << (at + 1));
+            while (later == 0) {
+                if (base + 32 >= b.num_seqs) return;  // past the last sequence (not reached for f < total)
+                load(b, u, base + 32);
+                later = __ballot_sync(0xffffffffu, my_units > 0);
+            }
+            take(__ffs(later) - 1);
+        }
+    }
+};
+
+// Zero rows of the dead sequences among cta, cta + grid, ...; one warp a sequence.
+__device__ __forceinline__ void zero_dead_rows(const SeqBatch &b, int cta, int grid, __nv_bfloat16 *out,
+                                               int64_t row_elems) {
+    const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+    for (int64_t s = cta + (int64_t)grid * (threadIdx.x >> 5); s < b.num_seqs; s += (int64_t)grid * nw) {
+        const SeqInfo q = read_seq(b, (int)s, false);
+        if (q.q_len == 0 || !q.dead) continue;
+        uint4 *o = reinterpret_cast<uint4 *>(out + q.q0 * row_elems);
+        const int64_t n = q.q_len * row_elems / 8;
+        for (int64_t i = lane; i < n; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+}  // namespace pkv
