@@ -383,6 +383,32 @@ int pkv_latent_attention_absorbed(void *out, const void *q, const int32_t *query
                                   int block_size, int64_t num_blocks, float scale, int causal, int dtype,
                                   void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Expanded form, for prompts and prompt chunks: every cached token's per-head keys and values
+ * are computed from its latent row once per call (into the workspace, rounded to bf16), then
+ *     out[i][h] = softmax_j(scale * q[i][h] . [W_k[h] c_j ; r_j]) W_v[h] c_j
+ *   q   [total_q_tokens, num_heads, nope_dim + rope_dim]  bf16 (rotary columns last)
+ *   out [total_q_tokens, num_heads, v_dim]                bf16, 32-byte aligned
+ *   w_k [num_heads, nope_dim, latent_dim], w_v [num_heads, v_dim, latent_dim]  bf16
+ * over the sequences of query_start_loc as in pkv_paged_attention_varlen (any q_len >= 0; for a
+ * few query tokens a sequence the absorbed form does far less work).  total_context is at least
+ * the sum of context_lens over the sequences with query rows, as the caller knows it on the
+ * host; a batch whose sum of contexts, each rounded up to 128, exceeds the room this gives
+ * (total_context + 127 num_seqs, rounded down to 128) is refused on the device
+ * (PKV_DEVERR_CONTEXT_LEN, all rows zero).
+ * Supported: latent_dim, rope_dim, block_size and dtype as for the absorbed form, nope_dim =
+ * v_dim = 128, num_heads * (total_context + 127 num_seqs) < 2^31 - 128.
+ * Workspace: pkv_latent_workspace_size(PKV_OP_LATENT_EXPANDED, ...): 512 bytes a (head, token)
+ * and about 40 MB.
+ */
+int pkv_latent_attention_expanded(void *out, const void *q, const int32_t *query_start_loc,
+                                  const void *latent_cache, const int32_t *block_tables,
+                                  const int32_t *context_lens, const void *w_k, const void *w_v, int num_seqs,
+                                  int total_q_tokens, int64_t total_context, int max_blocks_per_seq,
+                                  int num_heads, int latent_dim, int rope_dim, int nope_dim, int v_dim,
+                                  int block_size, int64_t num_blocks, float scale, int causal, int dtype,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
 /* Workspace bytes of a latent-attention call on the current device for these sizes (0 if
  * they are unsupported).  total_context is used by PKV_OP_LATENT_EXPANDED only. */
 size_t pkv_latent_workspace_size(int op, int num_seqs, int total_q_tokens, int64_t total_context,

@@ -12,6 +12,7 @@ Calls (names as in the C ABI, without the ``pkv_`` prefix):
   step_metadata             a step's lengths, offsets, block tables and slot map, on the device
   latent_cache_write        latent rows into the block-paged latent cache
   latent_attention_absorbed attention over the latent cache, projections folded into q and out
+  latent_attention_expanded the same with per-head keys and values expanded (prompt chunks)
   workspace_size            device scratch the attention calls need
   latent_workspace_size     the same for the latent-attention calls
   get_device_error          flags the kernels raised on bad device metadata
@@ -94,6 +95,8 @@ def lib() -> ctypes.CDLL:
         L.pkv_step_metadata.argtypes = [vp] * 9 + [i32, i32, i64, i64, i64, i32, vp]
         L.pkv_latent_cache_write.argtypes = [vp, vp, vp, vp, i64, i64, i32, i32, i32, i32, vp]
         L.pkv_latent_attention_absorbed.argtypes = [vp] * 6 + [i32] * 7 + [i64, f32, i32, i32, vp, sz, vp]
+        L.pkv_latent_attention_expanded.argtypes = [vp] * 8 + [i32, i32, i64] + [i32] * 7 + [i64, f32, i32, i32, vp,
+                                                                                             sz, vp]
         L.pkv_latent_workspace_size.argtypes = [i32, i32, i32, i64, i32, i32, i32]
         L.pkv_latent_workspace_size.restype = sz
         L.pkv_status_string.argtypes = [i32]
@@ -114,7 +117,8 @@ def lib() -> ctypes.CDLL:
                      "pkv_block_manager_share", "pkv_block_manager_ref_count",
                      "pkv_block_manager_copy_on_write", "pkv_paged_attention_decode_kvwrite",
                      "pkv_paged_attention_decode_kvwrite_fp8", "pkv_copy_to_device", "pkv_copy_to_host",
-                     "pkv_step_metadata", "pkv_latent_cache_write", "pkv_latent_attention_absorbed"):
+                     "pkv_step_metadata", "pkv_latent_cache_write", "pkv_latent_attention_absorbed",
+                     "pkv_latent_attention_expanded"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -445,6 +449,34 @@ def latent_attention_absorbed(out, q, latent_cache, block_tables, context_lens, 
         _ptr(block_tables), _ptr(context_lens), S, T, block_tables.shape[1], H, R, cols - R, bs, NB, float(scale),
         int(bool(causal)), DTYPE_BF16, _ptr(ws), ws.numel() * ws.element_size(), _stream_ptr(stream)),
         "latent_attention_absorbed")
+
+
+def latent_attention_expanded(out, q, query_start_loc, latent_cache, block_tables, context_lens, w_k, w_v,
+                              scale: float, total_context: int, causal: bool = True, workspace=None,
+                              stream=None) -> None:
+    """Latent attention with per-head keys and values expanded from the cache: q [T, H, 128 + P]
+    bf16 (rotary part last), out [T, H, 128] bf16, query_start_loc [S + 1] int32 (device),
+    latent_cache [NB, bs, R + P] bf16, w_k and w_v [H, 128, R] bf16; total_context is at least the
+    sum of context_lens of the sequences with query rows (host)."""
+    import torch
+    S = _latent_common(out, q, latent_cache, block_tables, context_lens, query_start_loc)
+    _require(w_k, torch.bfloat16, "w_k", 3)
+    _require(w_v, torch.bfloat16, "w_v", 3)
+    _on_current_device(w_k, w_v)
+    T, H, qcols = q.shape
+    NB, bs, cols = latent_cache.shape
+    nope, R = w_k.shape[1:]
+    P = cols - R
+    if query_start_loc is None or w_k.shape[0] != H or w_v.shape[0] != H or w_v.shape[2] != R \
+            or out.shape[2] != w_v.shape[1] or P <= 0 or qcols != nope + P:
+        raise ValueError("shape mismatch")
+    n = latent_workspace_size(OP_LATENT_EXPANDED, S, T, H, R, P, total_context)
+    ws = _call_workspace(workspace, n, q, stream)
+    _check(lib().pkv_latent_attention_expanded(
+        _ptr(out), _ptr(q), _ptr(query_start_loc), _ptr(latent_cache), _ptr(block_tables), _ptr(context_lens),
+        _ptr(w_k), _ptr(w_v), S, T, int(total_context), block_tables.shape[1], H, R, P, nope, w_v.shape[1], bs, NB,
+        float(scale), int(bool(causal)), DTYPE_BF16, _ptr(ws), ws.numel() * ws.element_size(), _stream_ptr(stream)),
+        "latent_attention_expanded")
 
 
 def copy_blocks(k_cache, v_cache, block_pairs, stream=None) -> None:

@@ -6,6 +6,7 @@
 #include "../../include/pagedkv.h"
 #include "api_common.h"
 #include "latent_absorbed.cuh"
+#include "latent_expanded.cuh"
 #include "step_metadata.cuh"
 
 namespace pkv {
@@ -126,6 +127,12 @@ extern "C" size_t pkv_latent_workspace_size(int op, int num_seqs, int total_q_to
         pkv::plan_absorbed(latent_dim, d.sms, &p);
         return p.ws_bytes;
     }
+    if (op == PKV_OP_LATENT_EXPANDED) {
+        pkv::ExpandedPlan p;
+        pkv::plan_expanded(num_seqs, total_context, num_heads, d.sms, &p);
+        if (p.padded * num_heads > (int64_t)INT32_MAX - 128) return 0;
+        return p.ws_bytes;
+    }
     return 0;
 }
 
@@ -182,4 +189,99 @@ extern "C" int pkv_latent_attention_absorbed(void *out, const void *q, const int
     return pkv::launch_latent_absorbed(latent_dim, qmap, kvmap, a, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PKV_OK
                : PKV_ERR_CUDA;
+}
+
+extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int32_t *query_start_loc,
+                                             const void *latent_cache, const int32_t *block_tables,
+                                             const int32_t *context_lens, const void *w_k, const void *w_v,
+                                             int num_seqs, int total_q_tokens, int64_t total_context,
+                                             int max_blocks_per_seq, int num_heads, int latent_dim, int rope_dim,
+                                             int nope_dim, int v_dim, int block_size, int64_t num_blocks,
+                                             float scale, int causal, int dtype, void *workspace,
+                                             size_t workspace_bytes, void *stream) {
+    int st = check_latent(num_seqs, total_q_tokens, max_blocks_per_seq, num_heads, latent_dim, rope_dim, block_size,
+                          num_blocks, dtype);
+    if (st != PKV_OK) return st;
+    if (total_context < 0 || nope_dim <= 0 || v_dim <= 0 || !(scale > 0.f) || scale == INFINITY)
+        return PKV_ERR_INVALID_ARG;
+    if (nope_dim != pkv::kExpHeadDim || v_dim != pkv::kExpHeadDim) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || total_q_tokens == 0) return PKV_OK;
+    if (!out || !q || !query_start_loc || !latent_cache || !block_tables || !context_lens || !w_k || !w_v)
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned_to(out, 32) || !aligned_to(q, 16) || !aligned_to(latent_cache, 16) || !aligned_to(w_k, 16) ||
+        !aligned_to(w_v, 16))
+        return PKV_ERR_INVALID_ARG;
+    if (num_blocks == 0 || max_blocks_per_seq == 0) return PKV_ERR_INVALID_ARG;
+    pkv::DeviceFacts d;
+    st = pkv::current_device(&d);
+    if (st != PKV_OK) return st;
+    pkv::ExpandedPlan p;
+    pkv::plan_expanded(num_seqs, total_context, num_heads, d.sms, &p);
+    if (p.padded * num_heads > (int64_t)INT32_MAX - 128) return PKV_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < p.ws_bytes) return PKV_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned_to(workspace, 256)) return PKV_ERR_INVALID_ARG;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    pkv::ExpandedBuffers buf;
+    buf.tile_off = reinterpret_cast<int32_t *>(ws + p.off_tiles);
+    buf.rope = reinterpret_cast<__nv_bfloat16 *>(ws + p.off_rope);
+    buf.kv = reinterpret_cast<__nv_bfloat16 *>(ws + p.off_kv);
+    buf.padded = p.padded;
+
+    CUtensorMap latmap, wkmap, wvmap, qmap, kvmap, ropemap;
+    st = encode_latent_map(&latmap, latent_cache, num_blocks, block_size, latent_dim + rope_dim);
+    const uint64_t wdims[2] = {(uint64_t)latent_dim, (uint64_t)num_heads * pkv::kExpHeadDim};
+    const uint64_t wstride[1] = {(uint64_t)latent_dim * 2};
+    const uint32_t rows128[2] = {64, 128};
+    if (st == PKV_OK) st = pkv::encode_tiled(&wkmap, 2, w_k, wdims, wstride, rows128);
+    if (st == PKV_OK) st = pkv::encode_tiled(&wvmap, 2, w_v, wdims, wstride, rows128);
+    const uint64_t qcols = (uint64_t)nope_dim + rope_dim;
+    const uint64_t qdims[4] = {64, qcols / 64, (uint64_t)num_heads, (uint64_t)total_q_tokens};
+    const uint64_t qstride[3] = {128, qcols * 2, qcols * 2 * num_heads};
+    const uint32_t qbox[4] = {64, 1, 1, 128};
+    if (st == PKV_OK) st = pkv::encode_tiled(&qmap, 4, q, qdims, qstride, qbox);
+    // a call whose sequences have no context at all has nothing to expand, but maps must be valid
+    const int64_t padded = p.padded > 0 ? p.padded : pkv::kExpTile;
+    const uint64_t kvdims[2] = {2 * pkv::kExpHeadDim, (uint64_t)padded * num_heads};
+    const uint64_t kvstride[1] = {4 * pkv::kExpHeadDim};
+    if (st == PKV_OK) st = pkv::encode_tiled(&kvmap, 2, buf.kv, kvdims, kvstride, rows128);
+    const uint64_t rdims[2] = {pkv::kExpRope, (uint64_t)padded};
+    const uint64_t rstride[1] = {pkv::kExpRope * 2};
+    if (st == PKV_OK) st = pkv::encode_tiled(&ropemap, 2, buf.rope, rdims, rstride, rows128);
+    if (st != PKV_OK) return st;
+
+    pkv::ExpandArgs e;
+    e.query_start_loc = query_start_loc;
+    e.block_tables = block_tables;
+    e.context_lens = context_lens;
+    e.num_seqs = num_seqs;
+    e.total_q = total_q_tokens;
+    e.max_blocks_per_seq = max_blocks_per_seq;
+    e.block_shift = block_shift(block_size);
+    e.num_heads = num_heads;
+    e.grid = p.grid;
+    e.num_blocks = num_blocks;
+    e.buf = buf;
+    e.err = d.err;
+    e.wait_ns = pkv::wait_limit_ns();
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (pkv::launch_latent_expand(latent_dim, latmap, wkmap, wvmap, e, s) != cudaSuccess) return PKV_ERR_CUDA;
+
+    pkv::ExpandedArgs a;
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.query_start_loc = query_start_loc;
+    a.context_lens = context_lens;
+    a.num_seqs = num_seqs;
+    a.total_q = total_q_tokens;
+    a.num_heads = num_heads;
+    a.grid = p.grid;
+    a.max_context = (int64_t)max_blocks_per_seq * block_size;
+    a.causal = causal != 0;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.buf = buf;
+    a.ws_jobs = reinterpret_cast<pkv::MergeJob *>(ws + p.off_jobs);
+    a.ws_ml = reinterpret_cast<float2 *>(ws + p.off_ml);
+    a.ws_o = reinterpret_cast<float *>(ws + p.off_o);
+    a.err = d.err;
+    a.wait_ns = e.wait_ns;
+    return pkv::launch_latent_expanded(qmap, kvmap, ropemap, a, s) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

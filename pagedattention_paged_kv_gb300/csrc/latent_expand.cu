@@ -1,0 +1,317 @@
+// latent_expand.cu -- per-head keys and values from the block-paged latent cache (sm_103a).
+//
+//   k[h][j] = W_k[h] c_j (128 columns),  v[h][j] = W_v[h] c_j (128 columns)
+// for every cached token j of the sequences with query rows: a matrix product of the gathered
+// latent rows [tokens, R] with the stacked weights [256 rows a head, R], written as bf16 rows
+// of 256 columns a (head, token), and the rotary parts copied beside them.
+//
+// Bound: tensor.  2 * 256 * R operations against 512 bytes written a (token, head): 512
+// operations a byte at R = 512.  A CTA keeps 128 tokens (all of R) in shared memory and streams
+// the weights of one head after the other past them in 64-column chunks; the accumulator
+// (128 tokens x 256 columns, half of TMEM) is double-buffered, so the stores of one head run
+// under the products of the next.  Units are (128-token tile, head) pairs, cut into equal
+// contiguous shares, so a CTA reloads its tokens only when its share crosses a tile.
+// Waits are bounded in time; no CTA waits on another CTA.
+#include "attn_block.cuh"
+#include "latent_expanded.cuh"
+#include "latent_walk.cuh"
+#include "pkv_split.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kExpandThreads = 192;  // loads, MMAs, four epilogue warps
+
+template <int R>
+struct ExpandSmem {
+    static constexpr int NCH = R / 64 + 1;
+    static constexpr uint32_t BOX = NCH * 1024;           // 8 tokens, all chunks
+    static constexpr uint32_t A_BYTES = (kExpTile / 8) * BOX;
+    static constexpr uint32_t W_STAGE = 256 * 128;        // 256 weight rows x 64 columns
+    static constexpr int NST = R == 512 ? 2 : 4;
+    static constexpr uint32_t OFF_W = A_BYTES;
+    static constexpr uint32_t OFF_EPI = OFF_W + NST * W_STAGE;
+    static constexpr uint32_t OFF_MISC = OFF_EPI + 4 * 4096;
+    static constexpr uint32_t BYTES = OFF_MISC + 1024 + 1024;
+    static_assert(BYTES <= 232448, "fits one CTA");
+};
+
+struct ExpandMisc {
+    uint64_t a_full, a_empty, mma_done;
+    uint64_t w_full[4], w_empty[4];
+    uint64_t acc_full[2], acc_free[2];
+    int64_t scan[8];
+    int64_t start_pre;
+    int start_seq;
+    uint32_t tmem_slot;
+    int abort_flag;
+};
+static_assert(sizeof(ExpandMisc) <= 1024, "fits its place");
+
+}  // namespace
+
+// Units of a sequence: 128-token tiles x heads.
+struct ExpandUnits {
+    int num_heads;
+    __device__ __forceinline__ int64_t operator()(const SeqInfo &q) const {
+        return (int64_t)((q.ctx + kExpTile - 1) / kExpTile) * num_heads;
+    }
+};
+
+template <int R>
+__global__ void __launch_bounds__(kExpandThreads, 1)
+latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap wk_map,
+                     const __grid_constant__ CUtensorMap wv_map, const ExpandArgs a) {
+    using L = ExpandSmem<R>;
+    constexpr int NST = L::NST, KCH = R / 64;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sA = smem, *sW = smem + L::OFF_W, *sEpi = smem + L::OFF_EPI;
+    ExpandMisc &ms = *reinterpret_cast<ExpandMisc *>(smem + L::OFF_MISC);
+    volatile int *abort_flag = &ms.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x, H = a.num_heads;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&ms.a_full, 1);
+        mbar_init(&ms.a_empty, 5);  // the tile's last product and the four epilogue warps
+        mbar_init(&ms.mma_done, 1);
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&ms.w_full[i], 1);
+            mbar_init(&ms.w_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ms.acc_full[i], 1);
+            mbar_init(&ms.acc_free[i], 4);
+        }
+        ms.abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (threadIdx.x == 32) {
+        tma_prefetch_desc(&kv_map);
+        tma_prefetch_desc(&wk_map);
+        tma_prefetch_desc(&wv_map);
+    }
+    pdl_wait();
+    pdl_trigger();
+    const SeqBatch sb{a.query_start_loc, a.context_lens, a.num_seqs, a.total_q,
+                      (int64_t)a.max_blocks_per_seq << a.block_shift, a.err};
+    const ExpandUnits units{H};
+    const BatchScan sc = scan_batch(sb, units, ms.scan, c == 0);
+    // A batch with more tokens than the caller counted is refused whole; the attention kernel
+    // sees the same sum and writes zero rows.
+    const int64_t T = sc.total <= a.buf.padded / kExpTile * H ? sc.total : 0;
+    if (c == 0) {
+        if (T != sc.total && threadIdx.x == 0) flag_error(a.err, PKV_DEVERR_CONTEXT_LEN);
+        int64_t run = sc.run;
+        for (int s = sc.beg; s < sc.end; ++s) {
+            a.buf.tile_off[s] = (int32_t)(run / H);
+            run += seq_units_of(sb, units, s, false);
+        }
+    }
+    const int ge = split_ctas(T, a.grid, 1);
+    if (T == 0 || c >= ge) return;
+    const int64_t lo = share_begin(c, T, ge), hi = share_begin(c + 1, T, ge);
+    find_unit(sb, units, sc, lo, &ms.start_seq, &ms.start_pre);
+    if (warp == 1) tmem_alloc(&ms.tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ms.tmem_slot;
+    SeqWalk<ExpandUnits> w;
+    w.start(sb, units, ms.start_seq, ms.start_pre);
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
+    };
+    bool ok = true;
+
+    if (warp == 0) {
+        // ------------------------------ TMA producer ------------------------------
+        const uint64_t policy = l2_policy_evict_normal();
+        uint32_t st = 0, ph = 0, fill = 0, aloads = 0;
+        for (int64_t f = lo; f < hi && ok; ++f) {
+            w.seek(sb, units, f);
+            const int64_t o = f - w.pre;
+            const int tile = (int)(o / H), h = (int)(o - (int64_t)tile * H);
+            if (f == lo || h == 0) {
+                // the tile's 16 groups of 8 tokens, one a lane
+                const int64_t pos = (int64_t)tile * kExpTile + 8 * lane;
+                const int boxes = (int)min64(kExpTile / 8, (w.q.ctx - (int64_t)tile * kExpTile + 7) >> 3);
+                int bid = -1;
+                if (lane < boxes) {
+                    bid = a.block_tables[(int64_t)w.s * a.max_blocks_per_seq + (pos >> a.block_shift)];
+                    if (bid < 0 || bid >= a.num_blocks) {
+                        flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+                        bid = -1;  // an out-of-range box is filled with zeros
+                    }
+                }
+                ok = aloads == 0 || wait_all(&ms.a_empty, (aloads - 1) & 1);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&ms.a_full, boxes * L::BOX);
+                __syncwarp();
+                if (lane < boxes)
+                    tma_load_4d(sA + lane * L::BOX, &kv_map, &ms.a_full, 0,
+                                (int)(pos & ((1 << a.block_shift) - 1)), 0, bid, policy);
+                ++aloads;
+            }
+            if (lane == 0) {
+#pragma unroll 1
+                for (int kc = 0; kc < KCH; ++kc) {
+                    ok = mbar_wait(&ms.w_empty[st], ph ^ 1, abort_flag, a.wait_ns);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&ms.w_full[st], L::W_STAGE);
+                    uint8_t *dst = sW + st * L::W_STAGE;
+                    tma_load_2d(dst, &wk_map, &ms.w_full[st], kc * 64, h * kExpHeadDim, policy);
+                    tma_load_2d(dst + L::W_STAGE / 2, &wv_map, &ms.w_full[st], kc * 64, h * kExpHeadDim, policy);
+                    ++fill;
+                    if (++st == NST) { st = 0; ph ^= 1; }
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (!ok && lane == 0) {
+            flag_error(a.err, PKV_DEVERR_TIMEOUT);
+            *abort_flag = 1;
+            const uint32_t pending = minu32(fill, NST);  // copies in flight land first
+            for (uint32_t k = fill - pending; k < fill; ++k) mbar_wait(&ms.w_full[k % NST], (k / NST) & 1, nullptr);
+            if (aloads > 0) mbar_wait(&ms.a_full, (aloads - 1) & 1, nullptr);
+        }
+    } else if (warp == 1) {
+        // ------------------------------ MMA issuer ------------------------------
+        constexpr uint32_t IDESC = umma_idesc_bf16(kExpTile, 256, 0, 0);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t da = umma_desc_sw128(smem_u32(sA), 16, L::BOX);
+        const uint64_t dw0 = umma_desc_sw128(smem_u32(sW), 16, 1024);
+        uint32_t st = 0, ph = 0, n = 0, atiles = 0;
+        for (int64_t f = lo; f < hi && ok; ++f, ++n) {
+            w.seek(sb, units, f);
+            const int64_t o = f - w.pre;
+            const int h = __shfl_sync(0xffffffffu, (int)(o % H), 0);
+            if (f == lo || h == 0) {
+                if (!wait_all(&ms.a_full, atiles & 1)) { ok = false; break; }
+                ++atiles;
+            }
+            if (n >= 2 && !wait_all(&ms.acc_free[n & 1], ((n >> 1) - 1) & 1)) { ok = false; break; }
+            for (int kc = 0; kc < KCH; ++kc) {
+                if (!wait_all(&ms.w_full[st], ph)) { ok = false; break; }
+                tc_fence_after();
+                const uint64_t dw = dw0 + st * (L::W_STAGE >> 4);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    umma_bf16_warp(tm + (n & 1) * 256, da + ((kc * 1024 + ks * 32) >> 4), dw + ((ks * 32) >> 4), IDESC,
+                                   kc > 0 || ks > 0);
+                umma_commit_warp(&ms.w_empty[st]);
+                if (++st == NST) { st = 0; ph ^= 1; }
+            }
+            if (!ok) break;
+            umma_commit_warp(&ms.acc_full[n & 1]);
+            if (h == H - 1) umma_commit_warp(&ms.a_empty);
+        }
+        if (!ok) {
+            if (lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+        umma_commit_warp(&ms.mma_done);  // every MMA is done before TMEM is released
+        mbar_wait(&ms.mma_done, 0, nullptr);
+        __syncwarp();
+    } else {
+        // ------------- epilogue: one token a thread, stored as whole 128-byte lines -------------
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;
+        uint8_t *ebuf = sEpi + quarter * 4096;
+        const int er = lane >> 3, ec = lane & 7;
+        uint32_t n = 0, atiles = 0;
+        for (int64_t f = lo; f < hi && ok; ++f, ++n) {
+            w.seek(sb, units, f);
+            const int64_t o = f - w.pre;
+            const int tile = (int)(o / H), h = (int)(o - (int64_t)tile * H);
+            const int64_t row0 = (w.pre / H + tile) * kExpTile;  // the tile's first padded token
+            const int valid = (int)min64(kExpTile, w.q.ctx - (int64_t)tile * kExpTile);
+            if (f == lo || h == 0) {
+                if (!wait_all(&ms.a_full, atiles & 1)) { ok = false; break; }
+                ++atiles;
+                if (h == 0) {
+                    // the rotary chunk of the tile's rows, 8 lanes a row
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = quarter * 32 + 4 * k + er;
+                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < valid)
+                            x = *reinterpret_cast<const uint4 *>(sA + (r >> 3) * L::BOX + (L::NCH - 1) * 1024 +
+                                                                 (r & 7) * 128 + ((ec ^ (r & 7)) << 4));
+                        *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(a.buf.rope + (row0 + r) * kExpRope) +
+                                                   ec * 16) = x;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.a_empty);
+            }
+            if (!wait_all(&ms.acc_full[n & 1], (n >> 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+            uint8_t *dst = reinterpret_cast<uint8_t *>(a.buf.kv + ((int64_t)h * a.buf.padded + row0) * 256);
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+                uint32_t r0[32], r1[32];
+                const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + (n & 1) * 256 + g * 64;
+                tmem_ld32(t, r0);
+                tmem_ld32(t + 32, r1);
+                tmem_wait_ld();
+                reg_order32(r0);
+                reg_order32(r1);
+                if (row >= valid) {  // past the context the product saw whatever the slots held
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r0[j] = r1[j] = 0u;
+                }
+#pragma unroll
+                for (int cc = 0; cc < 8; ++cc) {
+                    const uint32_t *s = cc < 4 ? r0 + 8 * cc : r1 + 8 * (cc - 4);
+                    uint4 x;
+                    x.x = pack_bf16x2(__uint_as_float(s[0]), __uint_as_float(s[1]));
+                    x.y = pack_bf16x2(__uint_as_float(s[2]), __uint_as_float(s[3]));
+                    x.z = pack_bf16x2(__uint_as_float(s[4]), __uint_as_float(s[5]));
+                    x.w = pack_bf16x2(__uint_as_float(s[6]), __uint_as_float(s[7]));
+                    *reinterpret_cast<uint4 *>(ebuf + lane * 128 + ((cc ^ (lane & 7)) << 4)) = x;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int rr = 4 * k + er;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(ebuf + rr * 128 + ((ec ^ (rr & 7)) << 4));
+                    *reinterpret_cast<uint4 *>(dst + (int64_t)(quarter * 32 + rr) * 512 + g * 128 + ec * 16) = x;
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.acc_free[n & 1]);
+        }
+        if (!ok) {
+            if (lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int R>
+static cudaError_t launch_expand(const CUtensorMap &kv_map, const CUtensorMap &wk_map, const CUtensorMap &wv_map,
+                                 const ExpandArgs &a, cudaStream_t stream) {
+    static SmemAllowance allowed;
+    const cudaError_t e = allow_dynamic_smem(latent_expand_kernel<R>, ExpandSmem<R>::BYTES, allowed);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(latent_expand_kernel<R>, dim3(a.grid), dim3(kExpandThreads), ExpandSmem<R>::BYTES, stream,
+                      kv_map, wk_map, wv_map, a);
+}
+
+cudaError_t launch_latent_expand(int latent_dim, const CUtensorMap &kv_map, const CUtensorMap &wk_map,
+                                 const CUtensorMap &wv_map, const ExpandArgs &a, cudaStream_t stream) {
+    return latent_dim == 512 ? launch_expand<512>(kv_map, wk_map, wv_map, a, stream)
+                             : launch_expand<256>(kv_map, wk_map, wv_map, a, stream);
+}
+
+}  // namespace pkv

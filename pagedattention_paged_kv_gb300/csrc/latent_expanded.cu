@@ -1,0 +1,553 @@
+// latent_expanded.cu -- attention of prompt chunks over expanded per-head keys and values of
+// a latent cache (sm_103a): scores over 128 + 64 columns (a head's key part, then the rotary
+// part all heads share), values of 128 columns.
+//
+//   out[i][h] = softmax_j(scale * (q_nope . k[h][j] + q_rope . r_j)) v[h][j],  j <= position of i
+//
+// Bound: tensor, 2 * (192 + 128) operations a visible (query, key) pair and head.
+//
+// Layout
+//  * A work tile is 256 query tokens of one head as two 128-row MMA halves; its units are
+//    128-key chunks, causal tiles stop at their last query's position.  A persistent grid
+//    takes equal contiguous shares of the flat unit list; split tiles are merged by
+//    log-sum-exp weights (merge.cuh).
+//  * The producer streams K (three 64-column pieces: two of the head's keys, one rotary) and V
+//    (two pieces) of a chunk; Q takes 96 KiB, so there are two K places and one V place, and
+//    a chunk's V is fetched while its scores are computed.
+//  * Per half TMEM holds S (128 columns, overwritten by the bf16 weights P) and O (128).  The
+//    issuer runs PV of one half and QK of its next chunk while the other half's warpgroup (one
+//    thread a row) computes its weights, as in the paged prefill.
+//  * Waits are bounded in time; no CTA waits on another CTA.
+#include "attn_block.cuh"
+#include "fp32x2.cuh"
+#include "latent_expanded.cuh"
+#include "latent_walk.cuh"
+#include "pkv_split.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kExpandedThreads = 384;  // loads, MMAs, two idle warps, two softmax warpgroups
+
+struct ExpandedSmem {
+    static constexpr uint32_t PIECE = 128 * 128;             // 128 rows x 64 columns
+    static constexpr uint32_t Q_BYTES = 2 * 3 * PIECE;       // [half][piece]
+    static constexpr uint32_t K_SLOT = 3 * PIECE, V_SLOT = 2 * PIECE;
+    static constexpr uint32_t OFF_K = Q_BYTES;               // two slots
+    static constexpr uint32_t OFF_V = OFF_K + 2 * K_SLOT;    // one slot
+    static constexpr uint32_t OFF_MISC = OFF_V + V_SLOT;
+    static constexpr uint32_t BYTES = OFF_MISC + 1024 + 1024;
+    static constexpr uint32_t HALF_COLS = 256, COL_O = 128;
+    static_assert(BYTES <= 232448, "fits one CTA");
+};
+
+struct ExpandedMisc {
+    uint64_t q_full, q_empty, v_full, v_empty, mma_done;
+    uint64_t k_full[2], k_empty[2];
+    uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+    int64_t scan[16];
+    int64_t start_pre;
+    int start_seq;
+    uint32_t tmem_slot;
+    int abort_flag;
+};
+static_assert(sizeof(ExpandedMisc) <= 1024, "fits its place");
+
+// Closed forms for the tiles of one (sequence, head).  Causal: full tile qt visits
+// A + 2 (qt + 1) chunks, A = ceil((ctx - q_len) / 128); the last, partial one all of them.
+struct ExpandedTiles {
+    int64_t A, nfull, rem, nk;
+    bool causal;
+    __device__ __forceinline__ ExpandedTiles(const SeqInfo &q, bool causal_) : causal(causal_) {
+        A = (q.ctx - q.q_len + kExpTile - 1) / kExpTile;
+        nfull = q.q_len / kExpQTile;
+        rem = q.q_len % kExpQTile;
+        nk = (q.ctx + kExpTile - 1) / kExpTile;
+    }
+    __device__ __forceinline__ int64_t before(int64_t qt) const {  // chunks before tile qt <= nfull
+        return causal ? qt * A + qt * (qt + 1) : qt * nk;
+    }
+    __device__ __forceinline__ int64_t chunks(int64_t qt) const {
+        return !causal || qt >= nfull ? nk : A + 2 * (qt + 1);
+    }
+    __device__ __forceinline__ int64_t per_head() const { return before(nfull) + (rem > 0 ? nk : 0); }
+    __device__ __forceinline__ int64_t tile_of(int64_t o) const {  // tile that holds chunk o
+        if (o >= before(nfull)) return nfull;
+        int64_t lo = 0, hi = nfull;
+        while (hi - lo > 1) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (before(mid) <= o) lo = mid; else hi = mid;
+        }
+        return lo;
+    }
+};
+
+struct ExpandedUnits {
+    int num_heads;
+    bool causal;
+    __device__ __forceinline__ int64_t operator()(const SeqInfo &q) const {
+        return ExpandedTiles(q, causal).per_head() * num_heads;
+    }
+};
+
+// Units of the expansion, whose sum tells whether the batch fits the workspace.
+struct TokenTiles {
+    __device__ __forceinline__ int64_t operator()(const SeqInfo &q) const { return (q.ctx + kExpTile - 1) / kExpTile; }
+};
+
+struct ExpandedSegment {
+    int h;
+    int64_t tile_begin;  // first unit of the tile
+    int64_t qt;          // tile
+    int kb, chunks;      // first chunk of the segment, chunks in it
+    int tokens;          // query tokens of the tile
+    bool whole;
+};
+
+__device__ __forceinline__ ExpandedSegment expanded_segment(const SeqInfo &q, bool causal, int64_t pre, int64_t f,
+                                                            int64_t hi) {
+    ExpandedSegment g;
+    const ExpandedTiles t(q, causal);
+    const int64_t ph = t.per_head(), o = f - pre;
+    g.h = (int)(o / ph);
+    const int64_t o1 = o - g.h * ph;
+    g.qt = t.tile_of(o1);
+    g.kb = (int)(o1 - t.before(g.qt));
+    g.tile_begin = f - g.kb;
+    const int64_t n = t.chunks(g.qt);
+    g.chunks = (int)min64(n - g.kb, hi - f);
+    g.tokens = (int)min64(kExpQTile, q.q_len - g.qt * kExpQTile);
+    g.whole = g.kb == 0 && g.chunks == n;
+    return g;
+}
+
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kExpandedThreads, 1)
+latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
+                       const __grid_constant__ CUtensorMap rope_map, const ExpandedArgs a) {
+    using L = ExpandedSmem;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = smem, *sK = smem + L::OFF_K, *sV = smem + L::OFF_V;
+    ExpandedMisc &ms = *reinterpret_cast<ExpandedMisc *>(smem + L::OFF_MISC);
+    volatile int *abort_flag = &ms.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&ms.q_full, 1);
+        mbar_init(&ms.q_empty, 1);
+        mbar_init(&ms.v_full, 1);
+        mbar_init(&ms.v_empty, 1);
+        mbar_init(&ms.mma_done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ms.k_full[i], 1);
+            mbar_init(&ms.k_empty[i], 1);
+            mbar_init(&ms.s_full[i], 1);
+            mbar_init(&ms.p_full[i], 4);  // one arrival per softmax warp of the half
+            mbar_init(&ms.pv_done[i], 1);
+            mbar_init(&ms.o_free[i], 4);
+        }
+        ms.abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (threadIdx.x == 32) {
+        tma_prefetch_desc(&q_map);
+        tma_prefetch_desc(&kv_map);
+        tma_prefetch_desc(&rope_map);
+    }
+    pdl_wait();
+    pdl_trigger();
+    const SeqBatch sb{a.query_start_loc, a.context_lens, a.num_seqs, a.total_q, a.max_context, a.err};
+    const ExpandedUnits units{a.num_heads, a.causal};
+    // (the expansion kernel has reported bad sequences already)
+    const bool fits = scan_batch(sb, TokenTiles{}, ms.scan, false).total <= a.buf.padded / kExpTile;
+    const BatchScan sc = scan_batch(sb, units, ms.scan, false);
+    const int64_t T = fits ? sc.total : 0;
+    const int ge = split_ctas(T, a.grid, 1);
+    const bool works = T > 0 && c < ge;
+    const int64_t lo = works ? share_begin(c, T, ge) : 0, hi = works ? share_begin(c + 1, T, ge) : 0;
+    if (works) find_unit(sb, units, sc, lo, &ms.start_seq, &ms.start_pre);
+    __syncthreads();
+
+    // The merge job of the boundary before this CTA's share (see latent_absorbed.cu).
+    if (threadIdx.x == 0) {
+        MergeJob j;
+        no_job(j);
+        if (works && c > 0) {
+            const SeqInfo q = read_seq(sb, ms.start_seq, false);
+            const ExpandedSegment g = expanded_segment(q, a.causal, ms.start_pre, lo, hi);
+            if (g.kb != 0 && g.tile_begin >= share_begin(c - 1, T, ge)) {
+                j.item_begin = g.tile_begin;
+                j.total_units = T;
+                j.out_row0 = q.q0 + g.qt * kExpQTile;
+                j.c0 = c - 1;
+                j.c1 = share_owner(g.tile_begin + ExpandedTiles(q, a.causal).chunks(g.qt) - 1, T, ge);
+                j.ge = ge;
+                j.rows = g.tokens;
+                j.rows_per_token = 1;
+                j.head0 = g.h;
+            }
+        }
+        if (c > 0) a.ws_jobs[c - 1] = j;
+        if (c == a.grid - 1) {
+            no_job(j);
+            a.ws_jobs[c] = j;
+        }
+    }
+    zero_dead_rows(sb, c, a.grid, a.out, (int64_t)a.num_heads * kExpHeadDim, !fits);
+    if (!works) return;
+
+    if (warp == 1) tmem_alloc(&ms.tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ms.tmem_slot;
+    SeqWalk<ExpandedUnits> w;
+    w.start(sb, units, ms.start_seq, ms.start_pre);
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
+    };
+    bool ok = true;
+
+    if (warp == 0) {
+        // ------------------------------ TMA producer ------------------------------
+        const uint64_t policy = l2_policy_evict_normal();
+        uint32_t n = 0, segs = 0;  // chunks and tiles issued
+        bool v_pending = false;
+        for (int64_t f = lo; f < hi && ok;) {
+            w.seek(sb, units, f);
+            const ExpandedSegment g = expanded_segment(w.q, a.causal, w.pre, f, hi);
+            const int64_t tok = (int64_t)a.buf.tile_off[w.s] * kExpTile;
+            if (lane == 0) {
+                auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, a.wait_ns); };
+                if (segs > 0) ok = wait(&ms.q_empty, (segs - 1) & 1);
+                if (ok) {
+                    const int nh = g.tokens > 128 ? 2 : 1;
+                    mbar_arrive_expect_tx(&ms.q_full, nh * 3 * L::PIECE);
+                    for (int h = 0; h < nh; ++h)
+                        for (int p = 0; p < 3; ++p)
+                            tma_load_4d(sQ + (h * 3 + p) * L::PIECE, &q_map, &ms.q_full, 0, p, g.h,
+                                        (int)(w.q.q0 + g.qt * kExpQTile) + h * 128, policy);
+                    ++segs;
+                }
+                for (int ch = 0; ch < g.chunks && ok; ++ch, ++n) {
+                    const int64_t key0 = tok + (int64_t)(g.kb + ch) * kExpTile;
+                    const int row = (int)(g.h * a.buf.padded + key0);
+                    uint8_t *k = sK + (n & 1) * L::K_SLOT;
+                    ok = n < 2 || wait(&ms.k_empty[n & 1], ((n >> 1) - 1) & 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&ms.k_full[n & 1], L::K_SLOT);
+                    tma_load_2d(k, &kv_map, &ms.k_full[n & 1], 0, row, policy);
+                    tma_load_2d(k + L::PIECE, &kv_map, &ms.k_full[n & 1], 64, row, policy);
+                    tma_load_2d(k + 2 * L::PIECE, &rope_map, &ms.k_full[n & 1], 0, (int)key0, policy);
+                    v_pending = true;
+                    ok = n < 1 || wait(&ms.v_empty, (n - 1) & 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&ms.v_full, L::V_SLOT);
+                    tma_load_2d(sV, &kv_map, &ms.v_full, 128, row, policy);
+                    tma_load_2d(sV + L::PIECE, &kv_map, &ms.v_full, 192, row, policy);
+                    v_pending = false;
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            f += g.chunks;
+        }
+        if (!ok && lane == 0) {
+            flag_error(a.err, PKV_DEVERR_TIMEOUT);
+            *abort_flag = 1;
+            // copies in flight land first
+            const uint32_t nk = n + (v_pending ? 1 : 0);
+            for (uint32_t k = nk > 2 ? nk - 2 : 0; k < nk; ++k) mbar_wait(&ms.k_full[k & 1], (k >> 1) & 1, nullptr);
+            if (n > 0) mbar_wait(&ms.v_full, (n - 1) & 1, nullptr);
+            if (segs > 0) mbar_wait(&ms.q_full, (segs - 1) & 1, nullptr);
+        }
+    } else if (warp == 1) {
+        // ------------------------------ MMA issuer ------------------------------
+        // PV_h(c), then QK_h(c + 1) over the same S columns; the halves alternate.
+        constexpr uint32_t IDESC_QK = umma_idesc_bf16(128, kExpTile, 0, 0);
+        constexpr uint32_t IDESC_PV = umma_idesc_bf16(128, kExpHeadDim, 0, 1);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t dq0 = umma_desc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t dk0 = umma_desc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t dv = umma_desc_sw128(smem_u32(sV), L::PIECE, 1024);
+        uint32_t n = 0;             // chunk whose V is next
+        uint32_t gh[2] = {0, 0};    // chunks each half has processed
+        uint32_t segh[2] = {0, 0};  // tiles each half has processed
+        uint32_t segs = 0;
+        auto issue_qk = [&](int h, uint32_t chunk) {
+            const uint64_t dk = dk0 + (chunk & 1) * (L::K_SLOT >> 4);
+            const uint64_t dq = dq0 + h * (3 * L::PIECE >> 4);
+#pragma unroll
+            for (int ks = 0; ks < 12; ++ks) {
+                const uint32_t off = ((ks / 4) * L::PIECE + (ks % 4) * 32) >> 4;
+                umma_bf16_warp(tm + h * L::HALF_COLS, dq + off, dk + off, IDESC_QK, ks > 0);
+            }
+            umma_commit_warp(&ms.s_full[h]);
+        };
+        for (int64_t f = lo; f < hi && ok;) {
+            w.seek(sb, units, f);
+            const ExpandedSegment g = expanded_segment(w.q, a.causal, w.pre, f, hi);
+            const int chunks = __shfl_sync(0xffffffffu, g.chunks, 0);
+            const int nh = __shfl_sync(0xffffffffu, g.tokens > 128 ? 2 : 1, 0);
+            if (!wait_all(&ms.q_full, segs & 1) || !wait_all(&ms.k_full[n & 1], (n >> 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (h < nh) issue_qk(h, n);
+            umma_commit_warp(&ms.k_empty[n & 1]);
+            if (chunks == 1) umma_commit_warp(&ms.q_empty);
+            for (int ch = 0; ch < chunks && ok; ++ch, ++n) {
+                const bool more = ch + 1 < chunks;
+                if (!wait_all(&ms.v_full, n & 1)) { ok = false; break; }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (h >= nh) break;
+                    if (ch == 0 && segh[h] > 0 && !wait_all(&ms.o_free[h], (segh[h] - 1) & 1)) { ok = false; break; }
+                    if (!wait_all(&ms.p_full[h], (gh[h] + ch) & 1)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t tP = tm + h * L::HALF_COLS;
+#pragma unroll
+                    for (int ks = 0; ks < kExpTile / 16; ++ks)
+                        umma_bf16_tmem_a_warp(tP + L::COL_O, tP + ks * 8, dv + ((ks * 2048) >> 4), IDESC_PV,
+                                              ch > 0 || ks > 0);
+                    umma_commit_warp(&ms.pv_done[h]);
+                    if (h == nh - 1) umma_commit_warp(&ms.v_empty);
+                    if (more) {
+                        if (h == 0 && !wait_all(&ms.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1)) { ok = false; break; }
+                        tc_fence_after();
+                        issue_qk(h, n + 1);
+                        if (h == nh - 1) {
+                            umma_commit_warp(&ms.k_empty[(n + 1) & 1]);
+                            if (ch + 2 == chunks) umma_commit_warp(&ms.q_empty);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (h < nh) {
+                    gh[h] += chunks;
+                    segh[h] += 1;
+                }
+            f += g.chunks;
+            ++segs;
+        }
+        if (!ok) {
+            if (lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+        umma_commit_warp(&ms.mma_done);  // every MMA is done before TMEM is released
+        mbar_wait(&ms.mma_done, 0, nullptr);
+        __syncwarp();
+    } else if (warp >= 4) {
+        // -------------- softmax: one warpgroup per half, one row per thread --------------
+        const int h = (warp - 4) >> 2;
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;
+        const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + h * L::HALF_COLS;
+        const uint32_t tO = tS + L::COL_O;
+        const float sl2 = a.scale_log2;
+        const uint64_t sc2 = f2_pack(sl2, sl2);
+        uint32_t gh = 0;  // chunks this half has processed
+        for (int64_t f = lo; f < hi && ok;) {
+            w.seek(sb, units, f);
+            const ExpandedSegment g = expanded_segment(w.q, a.causal, w.pre, f, hi);
+            if (h == 1 && g.tokens <= 128) {  // this half has no query rows here
+                f += g.chunks;
+                continue;
+            }
+            const int ctx = w.q.ctx;
+            const int tok = h * 128 + row;  // token inside the tile
+            const int64_t pos = (int64_t)(ctx - w.q.q_len) + g.qt * kExpQTile + min(tok, g.tokens - 1);
+            const int64_t lim = a.causal ? pos + 1 : ctx;
+            float m_ref = -INFINITY, l = 0.f;
+            for (int ch = 0; ch < g.chunks; ++ch, ++gh) {
+                if (!wait_all(&ms.s_full[h], gh & 1)) { ok = false; break; }
+                tc_fence_after();
+                const int vis = (int)max64(0, min64(lim - (int64_t)(g.kb + ch) * kExpTile, kExpTile));
+                const bool full = __all_sync(0xffffffffu, vis >= kExpTile);
+                // The row's 128 scores in two rounds of 64 columns, against a lazily moved
+                // reference maximum; a move in the second round rescales the first round's
+                // weights, already in TMEM, and any move rescales O.
+                float a_o = 1.f, a_p0 = 1.f;
+                bool any_o = false, any_p0 = false;
+                uint64_t ps2[2] = {0, 0};
+#pragma unroll 1
+                for (int r = 0; r < 2; ++r) {
+                    uint32_t v[64];
+                    float red0, red1;
+                    tmem_ld32_max(tS + r * 64, reinterpret_cast<uint32_t(&)[32]>(v[0]), red0);
+                    tmem_ld32_max(tS + r * 64 + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]), red1);
+                    tmem_wait_ld();
+                    reg_order32(reinterpret_cast<uint32_t(&)[32]>(v[0]));
+                    reg_order32(reinterpret_cast<uint32_t(&)[32]>(v[32]));
+                    float rm = fmaxf(red0, red1);
+                    if (!full) {
+                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (r * 64 + j >= vis) v[j] = __float_as_uint(-INFINITY);
+#pragma unroll
+                        for (int j = 0; j < 64; j += 8)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                m4[k] = fmax3(m4[k], __uint_as_float(v[j + 2 * k]), __uint_as_float(v[j + 2 * k + 1]));
+                        rm = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    }
+                    const float mx = rm * sl2;
+                    const bool up = mx > m_ref + kRescaleSlack;
+                    if (__any_sync(0xffffffffu, up)) {
+                        const float alpha = up ? fast_exp2(m_ref - mx) : 1.f;
+                        l *= alpha;
+                        ps2[0] = f2_mul(ps2[0], f2_pack(alpha, alpha));
+                        ps2[1] = f2_mul(ps2[1], f2_pack(alpha, alpha));
+                        a_o *= alpha;
+                        any_o = true;
+                        if (r > 0) {
+                            a_p0 = alpha;
+                            any_p0 = true;
+                        }
+                        if (up) m_ref = mx;
+                    }
+                    const float base = m_ref == -INFINITY ? 0.f : m_ref;
+                    const uint64_t nb2 = f2_pack(-base, -base);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(v[q * 32 + 2 * j]),
+                                                               __uint_as_float(v[q * 32 + 2 * j + 1])),
+                                                       sc2, nb2);
+                            float x0, x1;
+                            f2_unpack(x2, x0, x1);
+                            const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+                            pk[j] = pack_bf16x2(e0, e1);
+                            ps2[j & 1] = f2_add(ps2[j & 1], f2_pack(e0, e1));
+                        }
+                        tmem_st16(tS + (2 * r + q) * 16, pk);
+                    }
+                }
+                {
+                    float a0, a1, b0, b1;
+                    f2_unpack(ps2[0], a0, a1);
+                    f2_unpack(ps2[1], b0, b1);
+                    l += (a0 + a1) + (b0 + b1);
+                }
+                if (any_p0) {
+                    tmem_wait_st();
+#pragma unroll 1
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t x[16];
+                        tmem_ld16(tS + q * 16, x);
+                        tmem_wait_ld();
+                        reg_order16(x);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) x[j] = pack_bf16x2(bf16_lo(x[j]) * a_p0, bf16_hi(x[j]) * a_p0);
+                        tmem_st16(tS + q * 16, x);
+                    }
+                }
+                if (any_o && ch > 0) {
+                    if (!wait_all(&ms.pv_done[h], (gh - 1) & 1)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int q = 0; q < kExpHeadDim / 32; ++q) {
+                        uint32_t r[32];
+                        tmem_ld32(tO + q * 32, r);
+                        tmem_wait_ld();
+                        reg_order32(r);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * a_o);
+                        tmem_st32(tO + q * 32, r);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.p_full[h]);
+            }
+            if (!ok) break;
+            // ---- epilogue: O / l of a whole tile, or the part for the merge ----
+            if (!wait_all(&ms.pv_done[h], (gh - 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+            const float inv = g.whole ? 1.f / l : 1.f;
+            const int slot = g.whole ? 0 : part_slot(c, g.tile_begin, T, ge);
+            const bool live = tok < g.tokens;
+#pragma unroll 1
+            for (int q = 0; q < kExpHeadDim / 32; ++q) {
+                uint32_t r[32];
+                tmem_ld32(tO + q * 32, r);
+                tmem_wait_ld();
+                reg_order32(r);
+                if (live && g.whole) {
+                    __nv_bfloat16 *o = a.out + ((w.q.q0 + g.qt * kExpQTile + tok) * a.num_heads + g.h) * kExpHeadDim + q * 32;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t x[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            x[j] = pack_bf16x2(__uint_as_float(r[16 * k + 2 * j]) * inv,
+                                               __uint_as_float(r[16 * k + 2 * j + 1]) * inv);
+                        st_global_32(o + 16 * k, x);
+                    }
+                } else if (live) {
+                    float *o = a.ws_o + ((int64_t)slot * kExpQTile + tok) * kExpHeadDim + q * 32;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) st_global_32(o + 8 * k, reinterpret_cast<const uint32_t(&)[8]>(r[8 * k]));
+                }
+                __syncwarp();
+            }
+            if (!g.whole && live) a.ws_ml[(int64_t)slot * kExpQTile + tok] = make_float2(m_ref, l);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.o_free[h]);
+            f += g.chunks;
+        }
+        if (!ok) {
+            if (lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+void plan_expanded(int num_seqs, int64_t total_context, int num_heads, int sms, ExpandedPlan *p) {
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    p->grid = sms < kMergeMaxParts ? sms : kMergeMaxParts;
+    // each sequence is padded to whole tiles
+    p->padded = (total_context + (int64_t)num_seqs * (kExpTile - 1)) / kExpTile * kExpTile;
+    p->off_tiles = 0;
+    p->off_rope = up(sizeof(int32_t) * (size_t)num_seqs);
+    p->off_kv = p->off_rope + up((size_t)p->padded * kExpRope * 2);
+    p->off_jobs = p->off_kv + up((size_t)num_heads * p->padded * 2 * kExpHeadDim * 2);
+    p->off_ml = p->off_jobs + up(sizeof(MergeJob) * (size_t)p->grid);
+    p->off_o = p->off_ml + up(2 * (size_t)p->grid * kExpQTile * sizeof(float2));
+    p->ws_bytes = p->off_o + up(2 * (size_t)p->grid * kExpQTile * kExpHeadDim * sizeof(float));
+}
+
+cudaError_t launch_latent_expanded(const CUtensorMap &q_map, const CUtensorMap &kv_map, const CUtensorMap &rope_map,
+                                   const ExpandedArgs &a, cudaStream_t stream) {
+    static SmemAllowance allowed;
+    cudaError_t e = allow_dynamic_smem(latent_expanded_kernel, ExpandedSmem::BYTES, allowed);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(latent_expanded_kernel, dim3(a.grid), dim3(kExpandedThreads), ExpandedSmem::BYTES, stream, q_map,
+                   kv_map, rope_map, a);
+    if (e != cudaSuccess) return e;
+    const MergeArgs m{a.ws_jobs, a.ws_ml, a.ws_o, a.out, kExpQTile, a.num_heads};
+    return launch_merge<kExpHeadDim>(m, a.grid, stream);
+}
+
+}  // namespace pkv

@@ -1,0 +1,71 @@
+// latent_expanded.cuh -- arguments and launches of the expanded latent attention: the
+// expansion of cached latents into per-head keys and values (latent_expand.cu) and the
+// attention over them (latent_expanded.cu).
+#pragma once
+
+#include "merge.cuh"
+#include "pkv_common.cuh"
+
+namespace pkv {
+
+constexpr int kExpHeadDim = 128;  // non-rotary key columns, and value columns, of a head
+constexpr int kExpRope = 64;
+constexpr int kExpTile = 128;     // cached tokens of an expansion tile, keys of an attention chunk
+constexpr int kExpQTile = 256;    // query tokens of an attention tile (two MMA halves)
+
+// The expanded keys and values of a call: for head h and padded token i (each sequence starts
+// on a multiple of 128, tile_off[s] tiles in), row h * padded + i of kv is [128 key columns |
+// 128 value columns]; rope row i is the token's rotary key part.  Rows past a context are zero.
+struct ExpandedBuffers {
+    int32_t *tile_off;    // [num_seqs]
+    __nv_bfloat16 *rope;  // [padded][64]
+    __nv_bfloat16 *kv;    // [num_heads][padded][256]
+    int64_t padded;       // tokens, a multiple of 128
+};
+
+struct ExpandArgs {
+    const int32_t *query_start_loc;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    int num_seqs, total_q, max_blocks_per_seq, block_shift, num_heads, grid;
+    int64_t num_blocks;
+    ExpandedBuffers buf;
+    int *err;
+    uint64_t wait_ns;
+};
+
+struct ExpandedArgs {
+    __nv_bfloat16 *out;  // [total_q][num_heads][128]
+    const int32_t *query_start_loc;
+    const int32_t *context_lens;
+    int num_seqs, total_q, num_heads, grid;
+    int64_t max_context;
+    bool causal;
+    float scale_log2;
+    ExpandedBuffers buf;
+    MergeJob *ws_jobs;   // [grid]
+    float2 *ws_ml;       // [2 * grid][256]
+    float *ws_o;         // [2 * grid][256][128]
+    int *err;
+    uint64_t wait_ns;
+};
+
+struct ExpandedPlan {
+    int grid;
+    int64_t padded;
+    size_t off_tiles, off_rope, off_kv, off_jobs, off_ml, off_o, ws_bytes;
+};
+
+void plan_expanded(int num_seqs, int64_t total_context, int num_heads, int sms, ExpandedPlan *p);
+
+// kv_map: the latent cache in boxes of 8 tokens x all chunks; wk_map, wv_map: the weights as rows
+// [num_heads * 128][latent_dim] in boxes of 128 rows x 64 columns.
+cudaError_t launch_latent_expand(int latent_dim, const CUtensorMap &kv_map, const CUtensorMap &wk_map,
+                                 const CUtensorMap &wv_map, const ExpandArgs &a, cudaStream_t stream);
+
+// q_map: q as (64 columns, chunk, head, token) in boxes of 128 tokens x 64 columns; kv_map, rope_map:
+// the expanded rows in boxes of 128 rows x 64 columns.
+cudaError_t launch_latent_expanded(const CUtensorMap &q_map, const CUtensorMap &kv_map, const CUtensorMap &rope_map,
+                                   const ExpandedArgs &a, cudaStream_t stream);
+
+}  // namespace pkv

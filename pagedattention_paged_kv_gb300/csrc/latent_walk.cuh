@@ -165,13 +165,14 @@ struct SeqWalk {
     }
 };
 
-// Zero rows of the dead sequences among cta, cta + grid, ...; one warp a sequence.
+// Zero rows of the dead sequences (of every one, with `all`) among cta, cta + grid, ...; one
+// warp a sequence.
 __device__ __forceinline__ void zero_dead_rows(const SeqBatch &b, int cta, int grid, __nv_bfloat16 *out,
-                                               int64_t row_elems) {
+                                               int64_t row_elems, bool all = false) {
     const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
     for (int64_t s = cta + (int64_t)grid * (threadIdx.x >> 5); s < b.num_seqs; s += (int64_t)grid * nw) {
         const SeqInfo q = read_seq(b, (int)s, false);
-        if (q.q_len == 0 || !q.dead) continue;
+        if (q.q_len == 0 || !(q.dead || all)) continue;
         uint4 *o = reinterpret_cast<uint4 *>(out + q.q0 * row_elems);
         const int64_t n = q.q_len * row_elems / 8;
         for (int64_t i = lane; i < n; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);

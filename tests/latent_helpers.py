@@ -91,6 +91,29 @@ def absorbed_reference(b: Batch, causal=True, scale=SCALE):
     return out, tol
 
 
+def expanded_reference(b: Batch, w_k, w_v, causal=True, scale=SCALE, exact_keys=False):
+    """(out, tolerance) of the expanded form.  On top of the absorbed form's roundings the kernel
+    rounds keys and values to bf16: half a step moves a score by at most 2^-8 of the sum of
+    |q||k|, hence a weight and the normalising sum by that much each, and a value by 2^-8.
+    exact_keys: the keys are bf16 numbers, their rounding does nothing."""
+    T, H, R = b.q.shape[0], b.heads, b.latent
+    out = torch.zeros(T, H, w_v.shape[1], dtype=torch.float64, device=b.q.device)
+    tol = torch.zeros_like(out)
+    for s, (c, n) in enumerate(zip(b.ctx, b.q_lens)):
+        if n == 0 or c == 0:
+            continue
+        lo = b.offsets[s]
+        rows = b.rows[s].to(b.q.device).double()
+        k = torch.einsum("cr,hdr->hcd", rows[:, :R], w_k.double())
+        v = torch.einsum("cr,hdr->hcd", rows[:, :R], w_v.double())
+        k = torch.cat([k, rows[None, :, R:].expand(H, c, ROPE)], -1)
+        o, mag, sc = attend(b.q[lo:lo + n], k, v, n, scale, causal)
+        delta = ((0.0 if exact_keys else BF16_HALF) + 192 * 2.0 ** -24) * sc
+        out[lo:lo + n] = o
+        tol[lo:lo + n] = BF16_HALF * o.abs() + (2 * BF16_HALF + 2 * delta[..., None] + 2.0 ** -18) * mag
+    return out, tol
+
+
 def check(got, ref, tol, what=""):
     got = got.double()
     assert torch.isfinite(got).all(), f"{what}: {int((~torch.isfinite(got)).sum())} values not finite"
@@ -99,3 +122,7 @@ def check(got, ref, tol, what=""):
     assert (over <= 0).all(), (f"{what}: {int((over > 0).sum())} of {over.numel()} out of tolerance, worst at "
                                f"{worst}: got {got.flatten()[worst]:.6g} want {ref.flatten()[worst]:.6g} "
                                f"tol {tol.flatten()[worst]:.3g}")
+    # Independent roundings: each of the result, the weights and (expanded) the values and keys is
+    # off by 2^-8 / sqrt(3) of itself at most in the mean square, together under 2 x that.
+    rms = float((got - ref).square().mean().sqrt() / ref.square().mean().sqrt().clamp(min=1e-300)) if ref.any() else 0.0
+    assert rms <= 2 * BF16_HALF, f"{what}: rms error {rms:.3g} of the result"
