@@ -79,6 +79,7 @@ extern "C" {
 #define PKV_DEVERR_CONTEXT_LEN  0x4   /* context_len < 0 or > max_blocks_per_seq * block_size */
 #define PKV_DEVERR_QUERY_LEN    0x8   /* q_len < 0 or q_len > context_len */
 #define PKV_DEVERR_TIMEOUT      0x10  /* a pipeline wait gave up (internal fault) */
+#define PKV_DEVERR_VALUE        0x40  /* an expanded value past fp16's range was clamped to it */
 #define PKV_DEVERR_FREE_BLOCKS  0x20  /* a step needs more blocks than its free list holds */
 
 /* ---- dtypes --------------------------------------------------------------- */
@@ -385,7 +386,8 @@ int pkv_latent_attention_absorbed(void *out, const void *q, const int32_t *query
 
 /*
  * Expanded form, for prompts and prompt chunks: every cached token's per-head keys and values
- * are computed from its latent row once per call (into the workspace, rounded to bf16), then
+ * are computed from its latent row once per call (into the workspace; keys rounded to bf16,
+ * values to fp16), then
  *     out[i][h] = softmax_j(scale * q[i][h] . [W_k[h] c_j ; r_j]) W_v[h] c_j
  *   q   [total_q_tokens, num_heads, nope_dim + rope_dim]  bf16 (rotary columns last)
  *   out [total_q_tokens, num_heads, v_dim]                bf16, 32-byte aligned
@@ -395,7 +397,8 @@ int pkv_latent_attention_absorbed(void *out, const void *q, const int32_t *query
  * the sum of context_lens over the sequences with query rows, as the caller knows it on the
  * host; a batch whose sum of contexts, each rounded up to 128, exceeds the room this gives
  * (total_context + 127 num_seqs, rounded down to 128) is refused on the device
- * (PKV_DEVERR_CONTEXT_LEN, all rows zero).
+ * (PKV_DEVERR_CONTEXT_LEN, all rows zero).  The softmax weights are rounded to fp16; a finite
+ * value W_v[h] c_j beyond +-65504 is clamped there and flagged PKV_DEVERR_VALUE.
  * Supported: latent_dim, rope_dim, block_size and dtype as for the absorbed form, nope_dim =
  * v_dim = 128, num_heads * (total_context + 127 num_seqs) < 2^31 - 128.
  * Workspace: pkv_latent_workspace_size(PKV_OP_LATENT_EXPANDED, ...): 512 bytes a (head, token)

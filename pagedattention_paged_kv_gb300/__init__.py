@@ -44,6 +44,7 @@ DEVERR_CONTEXT_LEN = 0x4
 DEVERR_QUERY_LEN = 0x8
 DEVERR_TIMEOUT = 0x10
 DEVERR_FREE_BLOCKS = 0x20
+DEVERR_VALUE = 0x40
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpagedkv.so")

@@ -409,7 +409,8 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 __syncwarp();
                 bool rescale = false;
                 if (!meet(up && t > 0, rescale)) { ok = false; break; }
-                // the weights, while the tensor pipe finishes the last tile's PV
+                // The weights, while the tensor pipe finishes the last tile's PV.  The sum adds them as
+                // rounded, so a row that one key dominates loses nothing to their rounding.
                 const float base = m_ref == -INFINITY ? 0.f : m_ref;
                 uint32_t pk[32];
                 float s0 = 0.f, s1 = 0.f;
@@ -417,9 +418,9 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 for (int j = 0; j < 32; ++j) {
                     const float e0 = fast_exp2(fmaf(__uint_as_float(v[2 * j]), sl2, -base));
                     const float e1 = fast_exp2(fmaf(__uint_as_float(v[2 * j + 1]), sl2, -base));
-                    s0 += e0;
-                    s1 += e1;
                     pk[j] = pack_bf16x2(e0, e1);
+                    s0 += bf16_lo(pk[j]);
+                    s1 += bf16_hi(pk[j]);
                 }
                 l += s0 + s1;
                 if (gt > 0) {

@@ -224,7 +224,7 @@ extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int
     pkv::ExpandedBuffers buf;
     buf.tile_off = reinterpret_cast<int32_t *>(ws + p.off_tiles);
     buf.rope = reinterpret_cast<__nv_bfloat16 *>(ws + p.off_rope);
-    buf.kv = reinterpret_cast<__nv_bfloat16 *>(ws + p.off_kv);
+    buf.kv = reinterpret_cast<uint16_t *>(ws + p.off_kv);
     buf.padded = p.padded;
 
     CUtensorMap latmap, wkmap, wvmap, qmap, kvmap, ropemap;

@@ -2,8 +2,10 @@
 //
 //   k[h][j] = W_k[h] c_j (128 columns),  v[h][j] = W_v[h] c_j (128 columns)
 // for every cached token j of the sequences with query rows: a matrix product of the gathered
-// latent rows [tokens, R] with the stacked weights [256 rows a head, R], written as bf16 rows
-// of 256 columns a (head, token), and the rotary parts copied beside them.
+// latent rows [tokens, R] with the stacked weights [256 rows a head, R], written as rows of
+// 256 16-bit columns a (head, token), and the rotary parts copied beside them.  Keys are
+// rounded to bf16, values to fp16 (see latent_expanded.cu); a finite value past fp16's range
+// is clamped to it and flagged PKV_DEVERR_VALUE.
 //
 // Bound: tensor.  2 * 256 * R operations against 512 bytes written a (token, head): 512
 // operations a byte at R = 512.  A CTA keeps 128 tokens (all of R) in shared memory and streams
@@ -49,6 +51,19 @@ struct ExpandMisc {
     int abort_flag;
 };
 static_assert(sizeof(ExpandMisc) <= 1024, "fits its place");
+
+// Clamps a finite value to fp16's range; true if that changed it.
+__device__ __forceinline__ bool clamp_f16(uint32_t &x) {
+    const float v = __uint_as_float(x);
+    if (!(fabsf(v) > 65504.f) || fabsf(v) == INFINITY) return false;
+    x = __float_as_uint(copysignf(65504.f, v));
+    return true;
+}
+
+__device__ __forceinline__ uint32_t pack_16(bool f16, uint32_t lo, uint32_t hi) {
+    return f16 ? pack_f16x2(__uint_as_float(lo), __uint_as_float(hi))
+               : pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
+}
 
 }  // namespace
 
@@ -264,14 +279,25 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r0[j] = r1[j] = 0u;
                 }
+                const bool is_v = g >= 2;
+                if (is_v) {
+                    // clamping changes a value only past the range: compare before and after
+                    bool over = false;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        over |= clamp_f16(r0[j]);
+                        over |= clamp_f16(r1[j]);
+                    }
+                    if (over) flag_error(a.err, PKV_DEVERR_VALUE);
+                }
 #pragma unroll
                 for (int cc = 0; cc < 8; ++cc) {
                     const uint32_t *s = cc < 4 ? r0 + 8 * cc : r1 + 8 * (cc - 4);
                     uint4 x;
-                    x.x = pack_bf16x2(__uint_as_float(s[0]), __uint_as_float(s[1]));
-                    x.y = pack_bf16x2(__uint_as_float(s[2]), __uint_as_float(s[3]));
-                    x.z = pack_bf16x2(__uint_as_float(s[4]), __uint_as_float(s[5]));
-                    x.w = pack_bf16x2(__uint_as_float(s[6]), __uint_as_float(s[7]));
+                    x.x = pack_16(is_v, s[0], s[1]);
+                    x.y = pack_16(is_v, s[2], s[3]);
+                    x.z = pack_16(is_v, s[4], s[5]);
+                    x.w = pack_16(is_v, s[6], s[7]);
                     *reinterpret_cast<uint4 *>(ebuf + lane * 128 + ((cc ^ (lane & 7)) << 4)) = x;
                 }
                 __syncwarp();

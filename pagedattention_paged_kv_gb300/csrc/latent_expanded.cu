@@ -14,9 +14,14 @@
 //  * The producer streams K (three 64-column pieces: two of the head's keys, one rotary) and V
 //    (two pieces) of a chunk; Q takes 96 KiB, so there are two K places and one V place, and
 //    a chunk's V is fetched while its scores are computed.
-//  * Per half TMEM holds S (128 columns, overwritten by the bf16 weights P) and O (128).  The
+//  * Per half TMEM holds S (128 columns, overwritten by the 16-bit weights P) and O (128).  The
 //    issuer runs PV of one half and QK of its next chunk while the other half's warpgroup (one
 //    thread a row) computes its weights, as in the paged prefill.
+//  * Values and weights are fp16 (11 bits against bf16's 8; kind::f16 takes both operands of
+//    one type, so they go together): with bf16 the rounding of each weighed as much as that
+//    of the result and the error was 1.6 times the result's own rounding.  The weights stay
+//    below 2^8 by the rescale rule; values past fp16's range are clamped and flagged where
+//    they are made (latent_expand.cu).  Keys stay bf16, the type of the queries they meet.
 //  * Waits are bounded in time; no CTA waits on another CTA.
 #include "attn_block.cuh"
 #include "fp32x2.cuh"
@@ -275,7 +280,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         // ------------------------------ MMA issuer ------------------------------
         // PV_h(c), then QK_h(c + 1) over the same S columns; the halves alternate.
         constexpr uint32_t IDESC_QK = umma_idesc_bf16(128, kExpTile, 0, 0);
-        constexpr uint32_t IDESC_PV = umma_idesc_bf16(128, kExpHeadDim, 0, 1);
+        constexpr uint32_t IDESC_PV = umma_idesc_f16(128, kExpHeadDim, 0, 1);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t dq0 = umma_desc_sw128(smem_u32(sQ), 16, 1024);
         const uint64_t dk0 = umma_desc_sw128(smem_u32(sK), 16, 1024);
@@ -432,7 +437,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                             float x0, x1;
                             f2_unpack(x2, x0, x1);
                             const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-                            pk[j] = pack_bf16x2(e0, e1);
+                            pk[j] = pack_f16x2(e0, e1);
                             ps2[j & 1] = f2_add(ps2[j & 1], f2_pack(e0, e1));
                         }
                         tmem_st16(tS + (2 * r + q) * 16, pk);
@@ -453,7 +458,10 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                         tmem_wait_ld();
                         reg_order16(x);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) x[j] = pack_bf16x2(bf16_lo(x[j]) * a_p0, bf16_hi(x[j]) * a_p0);
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&x[j]));
+                            x[j] = pack_f16x2(p.x * a_p0, p.y * a_p0);
+                        }
                         tmem_st16(tS + q * 16, x);
                     }
                 }

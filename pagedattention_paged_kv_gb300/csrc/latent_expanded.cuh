@@ -19,7 +19,7 @@ constexpr int kExpQTile = 256;    // query tokens of an attention tile (two MMA 
 struct ExpandedBuffers {
     int32_t *tile_off;    // [num_seqs]
     __nv_bfloat16 *rope;  // [padded][64]
-    __nv_bfloat16 *kv;    // [num_heads][padded][256]
+    uint16_t *kv;         // [num_heads][padded][256]: bf16 keys, fp16 values
     int64_t padded;       // tokens, a multiple of 128
 };
 

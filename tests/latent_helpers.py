@@ -8,6 +8,7 @@ import torch
 
 ROPE = 64
 BF16_HALF = 2.0 ** -8      # half a bf16 step, relative
+F16_HALF = 2.0 ** -11      # half an fp16 step, relative
 SCALE = 1.0 / math.sqrt(128 + ROPE)
 
 
@@ -92,9 +93,11 @@ def absorbed_reference(b: Batch, causal=True, scale=SCALE):
 
 
 def expanded_reference(b: Batch, w_k, w_v, causal=True, scale=SCALE, exact_keys=False):
-    """(out, tolerance) of the expanded form.  On top of the absorbed form's roundings the kernel
-    rounds keys and values to bf16: half a step moves a score by at most 2^-8 of the sum of
-    |q||k|, hence a weight and the normalising sum by that much each, and a value by 2^-8.
+    """(out, tolerance) of the expanded form.  The kernel rounds keys to bf16: half a step moves a
+    score by at most 2^-8 of the sum of |q||k|, hence a weight and the normalising sum by that
+    much each.  Weights and values are fp16, half a step 2^-11 of each, and 2^-25 for values
+    under fp16's normal range (weights there are below 2^-14 of the row's largest: 2^-25 of it
+    for each key).  The rest as in the absorbed form.
     exact_keys: the keys are bf16 numbers, their rounding does nothing."""
     T, H, R = b.q.shape[0], b.heads, b.latent
     out = torch.zeros(T, H, w_v.shape[1], dtype=torch.float64, device=b.q.device)
@@ -110,7 +113,8 @@ def expanded_reference(b: Batch, w_k, w_v, causal=True, scale=SCALE, exact_keys=
         o, mag, sc = attend(b.q[lo:lo + n], k, v, n, scale, causal)
         delta = ((0.0 if exact_keys else BF16_HALF) + 192 * 2.0 ** -24) * sc
         out[lo:lo + n] = o
-        tol[lo:lo + n] = BF16_HALF * o.abs() + (2 * BF16_HALF + 2 * delta[..., None] + 2.0 ** -18) * mag
+        tol[lo:lo + n] = BF16_HALF * o.abs() + (2 * F16_HALF + 2 * delta[..., None] + 2.0 ** -18) * mag \
+            + 2.0 ** -25 * (1 + v.abs().sum(1))
     return out, tol
 
 

@@ -103,6 +103,22 @@ def test_bad_sequences_are_flagged_and_zero_and_leave_the_others():
     assert not out[20:50].any()
 
 
+def test_values_past_fp16_are_clamped_and_flagged():
+    b, w_k, w_v = make([40], [40], 2, 256, seed=12)
+    w_v.zero_()
+    w_v[:, 3, 7] = 1.0
+    b.cache[b.tables[0, 1], 2, 7] = 1e5   # token 18, alone past the range
+    b.rows[0][18, 7] = 65504.0
+    out = run(b, w_k, w_v)
+    assert pkv.get_device_error() == pkv.DEVERR_VALUE
+    w_k2 = w_k.clone()
+    w_k2[..., 7] = 0                      # its key would move with the clamp too
+    w_k[..., 7] = 0
+    out = run(b, w_k, w_v)
+    assert pkv.get_device_error() == pkv.DEVERR_VALUE
+    check(out, *expanded_reference(b, w_k2, w_v))
+
+
 def test_a_batch_past_its_total_context_is_refused():
     b, w_k, w_v = make([300, 500], [20, 30], 4, 256, seed=8)
     out = run(b, w_k, w_v, fill=5.0, total=300)
