@@ -17,19 +17,21 @@
 //    are tiles of 64 cached tokens.  A persistent grid takes equal contiguous shares of the
 //    flat unit list (pkv_split.cuh); items cut by a share boundary are merged by
 //    log-sum-exp weights (merge.cuh).
-//  * A tile arrives as eight TMA boxes of 8 tokens x all 64-column chunks, so any block
-//    size that is a multiple of 8 works and eight requests move 72 KiB.  In shared memory
-//    box b holds [chunk][8 tokens][128 bytes], 128-byte swizzled: the 8-row groups of a tile
-//    are a constant distance apart, which is what both operand descriptors need.
-//  * S = Q K^T runs with the rows on M = 64 and the tile's tokens on N = 64, so the softmax has
-//    one row per thread.  O^T += C^T P^T runs with the latent columns on M = 128 (R / 128 blocks),
+//  * A tile arrives as one TMA box a block and part (blocks of 8 to 64 tokens, several 64-column
+//    chunks).  In shared memory
+//    every 8 tokens of a part are [chunk][8 tokens][128 bytes], 128-byte swizzled, whatever the block
+//    size: the 8-row groups of a tile are a constant distance apart, which is what both operand
+//    descriptors need.
+//  * S = Q K^T runs with the rows on M = 64 and the tile's tokens on N = 64, so a row's scores stay
+//    in the four threads of a quad.  O^T += C^T P^T runs with the latent columns on M = 128 (R / 128 blocks),
 //    the rows on N and the tokens on K: the tile is read transposed in place (A MN-major) and P
 //    is the K-major B operand.  O^T of 64 rows then takes R / 2 TMEM columns; with the rows
 //    on M it would take all 512 and leave none for S.
-//  * The MMA warp issues QK of tile t+1 before PV of tile t, so the tensor pipe works during
-//    the softmax; a tile's stage is free after its PV.
+//  * QK of tile t+1 runs during the softmax of tile t; a tile's stage is free after its PV, part
+//    by part.
 //  * Waits are bounded in time; no CTA waits on another CTA.
 #include "attn_block.cuh"
+#include "fp32x2.cuh"
 #include "latent_absorbed.cuh"
 #include "latent_walk.cuh"
 #include "pkv_split.cuh"
@@ -41,11 +43,22 @@ namespace {
 
 constexpr int kMinTilesPerCta = 2;
 
+// A row's reference maximum moves, and O^T is rescaled, only when a tile's maximum exceeds it by
+// this much (log2 units).  bf16 weights and fp32 sums keep their relative precision up to 2^24
+// and far from overflow, and a move is rare enough to be handled off the critical path.
+constexpr float kAbsorbedSlack = 24.0f;
+
 template <int R>
 struct AbsorbedSmem {
     static constexpr int NCH = R / 64 + 1;                    // 64-column chunks of a row, rotary last
-    static constexpr uint32_t BOX = NCH * 1024;               // 8 tokens, all chunks
-    static constexpr uint32_t STAGE = 8 * BOX;                // one tile
+    // A tile's boxes come in PARTS groups of chunks with a barrier each, so that the scores over
+    // the first chunks are under way while the last ones are still arriving.
+    static constexpr int PARTS = NCH % 3 == 0 ? 3 : 1;
+    static constexpr int PCH = NCH / PARTS;                   // chunks of a part
+    static constexpr uint32_t GROUP = PCH * 1024;             // 8 tokens, a part's chunks
+    static constexpr uint32_t PART = 8 * GROUP;               // a part of a tile
+    static constexpr uint32_t STAGE = PARTS * PART;           // one tile
+    static constexpr uint32_t chunk_at(int j) { return (j / PCH) * PART + (j % PCH) * 1024; }
     static constexpr uint32_t Q_CH = kLatentRows * 128;       // 64 rows x 64 columns
     static constexpr uint32_t OFF_Q = 0;
     static constexpr uint32_t OFF_P = NCH * Q_CH;             // P: 64 rows x 64 tokens, bf16
@@ -60,19 +73,22 @@ struct AbsorbedSmem {
 };
 
 struct AbsorbedMisc {
-    uint64_t q_full, q_empty, pv_done, p_full, o_free, mma_done, group;
-    uint64_t s_full[2];
-    uint64_t kv_full[4], kv_empty[4];
+    uint64_t q_full, q_empty, pv_done, p_full, o_free, qk_over, pv_over, group, rescaled;
+    uint64_t s_full[2], s_free[2];
+    uint64_t kv_full[4][3], kv_empty[4][3];
     uint32_t tmem_slot;
     int abort_flag;
     int64_t scan[8];
-    int64_t start_pre;
-    int start_seq;
-    int flag[2][4];
+    WalkStart start;
+    int moved[2][4];  // by tile parity and softmax warp: a row's reference maximum moved
     float alpha[2][kLatentRows];
     float inv[kLatentRows];
 };
 static_assert(sizeof(AbsorbedMisc) <= 2048, "fits its place");
+
+__device__ __forceinline__ uint64_t uniform_desc(uint64_t d) {
+    return (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)(d >> 32), 0) << 32 | __shfl_sync(0xffffffffu, (uint32_t)d, 0);
+}
 
 // Units of a sequence: 64-row groups x 64-token tiles.
 struct AbsorbedUnits {
@@ -98,7 +114,7 @@ __device__ __forceinline__ AbsorbedSegment segment_at(const AbsorbedArgs &a, con
     AbsorbedSegment g;
     const int nk = (q.ctx + kLatentTile - 1) / kLatentTile;
     const int64_t o = f - pre;
-    const int64_t grp = o / nk;
+    const int64_t grp = quotient(o, nk);
     g.kb = (int)(o - grp * nk);
     g.item_begin = f - g.kb;
     g.tiles = (int)min64(nk - g.kb, hi - f);
@@ -132,12 +148,19 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         mbar_init(&ms.pv_done, 1);
         mbar_init(&ms.p_full, 4);  // one arrival per softmax warp
         mbar_init(&ms.o_free, 4);
-        mbar_init(&ms.mma_done, 1);
+        mbar_init(&ms.qk_over, 1);
+        mbar_init(&ms.pv_over, 1);
         mbar_init(&ms.group, 4);
-        for (int i = 0; i < 2; ++i) mbar_init(&ms.s_full[i], 1);
+        mbar_init(&ms.rescaled, 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ms.s_full[i], 1);
+            mbar_init(&ms.s_free[i], 4);
+        }
         for (int i = 0; i < NST; ++i) {
-            mbar_init(&ms.kv_full[i], 1);
-            mbar_init(&ms.kv_empty[i], 1);
+            for (int p = 0; p < L::PARTS; ++p) {
+                mbar_init(&ms.kv_full[i][p], 1);
+                mbar_init(&ms.kv_empty[i][p], 1);
+            }
         }
         ms.abort_flag = 0;
         fence_barrier_init();
@@ -146,6 +169,9 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         tma_prefetch_desc(&q_map);
         tma_prefetch_desc(&kv_map);
     }
+    // Before the previous kernel's end is waited for: a CTA of this kernel has the SM's shared
+    // memory, so no other holder of TMEM is there.
+    if (warp == 1) tmem_alloc(&ms.tmem_slot, 512);
     pdl_wait();
     pdl_trigger();
 
@@ -156,102 +182,113 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     const int64_t T = sc.total;
     const int ge = split_ctas(T, a.grid, kMinTilesPerCta);
     const bool works = T > 0 && c < ge;
-    const int64_t lo = works ? share_begin(c, T, ge) : 0, hi = works ? share_begin(c + 1, T, ge) : 0;
-    if (works) find_unit(sb, units, sc, lo, &ms.start_seq, &ms.start_pre);
-    __syncthreads();
-
-    // The merge job of the boundary before this CTA's share: the item split there, when that
-    // is its first split.
-    if (threadIdx.x == 0) {
-        MergeJob j;
-        no_job(j);
-        if (works && c > 0) {
-            const SeqInfo q = read_seq(sb, ms.start_seq, false);
-            const int64_t nk = (q.ctx + kLatentTile - 1) / kLatentTile;
-            const int64_t grp = (lo - ms.start_pre) / nk, begin = ms.start_pre + grp * nk;
-            if (begin != lo && begin >= share_begin(c - 1, T, ge)) {
-                j.item_begin = begin;
-                j.total_units = T;
-                j.out_row0 = (int64_t)q.q0 * a.num_heads + grp * kLatentRows;
-                j.c0 = c - 1;
-                j.c1 = share_owner(begin + nk - 1, T, ge);
-                j.ge = ge;
-                j.rows = (int)min64(kLatentRows, (int64_t)q.q_len * a.num_heads - grp * kLatentRows);
-                j.rows_per_token = 1;
-                j.head0 = 0;
-            }
-        }
-        if (c > 0) a.ws_jobs[c - 1] = j;
-        if (c == a.grid - 1) {
-            no_job(j);
-            a.ws_jobs[c] = j;
-        }
-    }
-    zero_dead_rows(sb, c, a.grid, a.out, (int64_t)a.num_heads * R);
-    if (!works) return;
-
-    if (warp == 1) tmem_alloc(&ms.tmem_slot, 512);
+    const int64_t lo = works ? quotient(c * T, ge) : 0, hi = works ? quotient((c + 1) * T, ge) : 0;
+    if (works) find_unit(sb, units, sc, lo, &ms.start);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ms.tmem_slot;
+    if (warp >= 2 && warp < 6) {
+        // The merge job of the boundary before this CTA's share: the item split there, when that
+        // is its first split.
+        if (threadIdx.x == 64) {
+            MergeJob j;
+            no_job(j);
+            if (works && c > 0) {
+                const SeqInfo q = ms.start.q;
+                const int64_t nk = (q.ctx + kLatentTile - 1) / kLatentTile;
+                const int64_t grp = quotient(lo - ms.start.pre, nk), begin = ms.start.pre + grp * nk;
+                if (begin != lo && begin >= quotient((c - 1) * T, ge)) {
+                    j.item_begin = begin;
+                    j.total_units = T;
+                    j.out_row0 = (int64_t)q.q0 * a.num_heads + grp * kLatentRows;
+                    j.c0 = c - 1;
+                    j.c1 = share_owner(begin + nk - 1, T, ge);
+                    j.ge = ge;
+                    j.rows = (int)min64(kLatentRows, (int64_t)q.q_len * a.num_heads - grp * kLatentRows);
+                    j.rows_per_token = 1;
+                    j.head0 = 0;
+                }
+            }
+            if (c > 0) a.ws_jobs[c - 1] = j;
+            if (c == a.grid - 1) {
+                no_job(j);
+                a.ws_jobs[c] = j;
+            }
+        }
+        __syncwarp();
+        zero_dead_rows(sb, c, a.grid, a.out, (int64_t)a.num_heads * R, warp - 2, 4);
+    }
+    if (!works) {
+        __syncwarp();
+        if (warp == 1) tmem_dealloc(tmem, 512);
+        return;
+    }
     SeqWalk<AbsorbedUnits> w;
-    w.start(sb, units, ms.start_seq, ms.start_pre);
+    w.start(ms.start);
 
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
         const uint64_t policy = l2_policy_evict_normal();
-        uint32_t st = 0, ph = 0, fill = 0;  // ring slot and phase of the next tile; tiles issued
+        uint32_t st = 0, ph = 0, fill = 0;  // ring slot and phase of the next tile; parts issued
         uint32_t qloads = 0;
+        const int per_tile = kLatentTile >> a.block_shift;             // blocks of a tile
+        const int box_bytes = L::GROUP << (a.block_shift - 3);          // a block's share of a part
         bool ok = true;
         for (int64_t f = lo; f < hi && ok;) {
             w.seek(sb, units, f);
             const AbsorbedSegment g = segment_at(a, w.q, w.pre, f, hi);
+            // A window of 32 blocks, one a lane (32 / per_tile tiles); the ids of the next window are
+            // loaded while the current one is issued.
+            const int32_t *table = a.block_tables + (int64_t)w.s * a.max_blocks_per_seq;
+            const int64_t block0 = (int64_t)g.kb * per_tile;
+            const int64_t seq_blocks = ((int64_t)w.q.ctx + (1 << a.block_shift) - 1) >> a.block_shift;
+            const int nblocks = (int)(min64(seq_blocks, block0 + (int64_t)g.tiles * per_tile) - block0);
+            auto block_of = [&](int i) -> int {
+                if (i + lane >= nblocks) return -1;
+                const int id = table[block0 + i + lane];
+                if (id >= 0 && id < a.num_blocks) return id;
+                flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+                return -1;  // an out-of-range box is filled with zeros
+            };
+            int bid = -1, bid_next = block_of(0);  // under way while Q is asked for
             if (lane == 0) {
                 if (qloads > 0) ok = mbar_wait(&ms.q_empty, (qloads - 1) & 1, abort_flag, a.wait_ns);
                 if (ok) {
                     mbar_arrive_expect_tx(&ms.q_full, NCH * L::Q_CH);
-#pragma unroll 1
-                    for (int ch = 0; ch < NCH; ++ch)
-                        tma_load_2d(sQ + ch * L::Q_CH, &q_map, &ms.q_full, ch * 64, (int)g.row0, policy);
+                    tma_load_3d(sQ, &q_map, &ms.q_full, 0, (int)g.row0, 0, policy);
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             ++qloads;
-            // A window is 4 tiles = 32 groups of 8 tokens, one group a lane; the block ids of the
-            // next window are loaded while the current one is issued.
-            const int32_t *table = a.block_tables + (int64_t)w.s * a.max_blocks_per_seq;
-            const int ctx = w.q.ctx;
-            const int64_t first = (int64_t)g.kb * kLatentTile + 8 * lane;
-            const int64_t last = min64(ctx, (int64_t)(g.kb + g.tiles) * kLatentTile);
-            auto block_of = [&](int tile) -> int {
-                const int64_t pos = first + (int64_t)tile * kLatentTile;
-                if (pos >= last) return -1;
-                const int id = table[pos >> a.block_shift];
-                if (id >= 0 && id < a.num_blocks) return id;
-                flag_error(a.err, PKV_DEVERR_BLOCK_ID);
-                return -1;  // an out-of-range box is filled with zeros
-            };
-            const int in_block = (int)(first & ((1 << a.block_shift) - 1));  // a tile is a multiple of any block
-            int bid = -1, bid_next = block_of(0);
-            for (int t = 0; t < g.tiles; ++t) {
-                if ((t & 3) == 0) {
+            for (int t = 0, i0 = 0; t < g.tiles; ++t, i0 += per_tile) {
+                if ((i0 & 31) == 0) {
                     bid = bid_next;
-                    bid_next = block_of(t + 4);
+                    bid_next = block_of(i0 + 32);
                 }
-                const int64_t key0 = (int64_t)(g.kb + t) * kLatentTile;
-                const int boxes = (int)min64(8, (ctx - key0 + 7) >> 3);
-                if (lane == 0) {
-                    ok = mbar_wait(&ms.kv_empty[st], ph ^ 1, abort_flag, a.wait_ns);
-                    if (ok) mbar_arrive_expect_tx(&ms.kv_full[st], boxes * L::BOX);
+                const int boxes = min(per_tile, nblocks - i0);
+                // One lane issues: the copies of several lanes would go out one after the other at
+                // ~90 cycles each, against ~30 for one lane's.
+#pragma unroll
+                for (int p = 0; p < L::PARTS; ++p) {
+                    if (lane == 0) {
+                        ok = mbar_wait(&ms.kv_empty[st][p], ph ^ 1, abort_flag, a.wait_ns);
+                        if (ok) mbar_arrive_expect_tx(&ms.kv_full[st][p], boxes * box_bytes);
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    uint8_t *dst = sKV + st * L::STAGE + p * L::PART;
+#pragma unroll 1
+                    for (int i = 0; i < boxes; ++i) {
+                        const int id = __shfl_sync(0xffffffffu, bid, (i0 + i) & 31);
+                        if (lane == 0)
+                            tma_load_5d(dst + i * box_bytes, &kv_map, &ms.kv_full[st][p], 0, 0, p * L::PCH, 0, id,
+                                        policy);
+                    }
+                    ++fill;
                 }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
-                if ((lane >> 3) == (t & 3) && (lane & 7) < boxes)
-                    tma_load_4d(sKV + st * L::STAGE + (lane & 7) * L::BOX, &kv_map, &ms.kv_full[st], 0, in_block, 0,
-                                bid, policy);
-                ++fill;
                 if (++st == NST) { st = 0; ph ^= 1; }
             }
             f += g.tiles;
@@ -260,69 +297,109 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             flag_error(a.err, PKV_DEVERR_TIMEOUT);
             *abort_flag = 1;
             // copies in flight land before the shared memory is given back
-            const uint32_t pending = minu32(fill, NST);
-            for (uint32_t k = fill - pending; k < fill; ++k) mbar_wait(&ms.kv_full[k % NST], (k / NST) & 1, nullptr);
+            const uint32_t pending = minu32(fill, NST * L::PARTS);  // fill counts parts
+            for (uint32_t k = fill - pending; k < fill; ++k) {
+                const uint32_t tile = k / L::PARTS;
+                mbar_wait(&ms.kv_full[tile % NST][k % L::PARTS], (tile / NST) & 1, nullptr);
+            }
             if (qloads > 0) mbar_wait(&ms.q_full, (qloads - 1) & 1, nullptr);
         }
     } else if (warp == 1) {
-        // ------------------------------ MMA issuer ------------------------------
-        // The whole warp runs on uniform values; one elected lane issues (tcgen05.cuh).
+        // ------------------------------ QK issuer ------------------------------
+        // The issuers are whole warps on uniform values of which one elected lane issues
+        // (tcgen05.cuh).  QK and PV have a warp each: a tile that is late holds up no finished
+        // one, and the tensor pipe takes from both.
         auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
         };
         constexpr uint32_t IDESC_QK = umma_idesc_bf16(kLatentRows, kLatentTile, 0, 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t dq = umma_desc_sw128(smem_u32(sQ), 16, 1024);
-        const uint64_t dk0 = umma_desc_sw128(smem_u32(sKV), 16, L::BOX);
-        const uint64_t dv0 = umma_desc_sw128(smem_u32(sKV), 1024, L::BOX);
-        const uint64_t dp = umma_desc_sw128(smem_u32(sP), 16, 1024);
-        uint32_t st = 0, ph = 0;   // ring slot of the next tile's QK
-        uint32_t vst = 0;          // ring slot of the next tile's PV
-        uint32_t gq = 0, gv = 0;   // tiles whose QK / PV has been issued
+        const uint64_t dk0 = umma_desc_sw128(smem_u32(sKV), 16, L::GROUP);
+        uint32_t st = 0, ph = 0;  // ring slot of the next tile
+        uint32_t gq = 0;          // tiles issued
         uint32_t seg_i = 0;
-        bool ok = true, issued = false;
-        auto issue_qk = [&]() -> bool {
-            if (!wait_all(&ms.kv_full[st], ph)) return false;
-            tc_fence_after();
-            const uint64_t dk = dk0 + st * (L::STAGE >> 4);
-            const uint32_t tS = tm + (gq & 1) * kLatentTile;
+        bool ok = true;
+        for (int64_t f = lo; f < hi && ok;) {
+            w.seek(sb, units, f);
+            const AbsorbedSegment g = segment_at(a, w.q, w.pre, f, hi);
+            const int tiles = __shfl_sync(0xffffffffu, g.tiles, 0);
+            ok = wait_all(&ms.q_full, seg_i & 1);
+            for (int t = 0; t < tiles && ok; ++t) {
+                // S has two places: the scores of two tiles before have been read
+                if (gq >= 2 && !wait_all(&ms.s_free[gq & 1], ((gq >> 1) - 1) & 1)) { ok = false; break; }
+                const uint32_t tS = tm + (gq & 1) * kLatentTile;
 #pragma unroll
-            for (int ks = 0; ks < NCH * 4; ++ks)
-                umma_bf16_warp(tS, dq + (((ks / 4) * L::Q_CH + (ks % 4) * 32) >> 4),
-                               dk + (((ks / 4) * 1024 + (ks % 4) * 32) >> 4), IDESC_QK, ks > 0);
-            umma_commit_warp(&ms.s_full[gq & 1]);
-            issued = true;
-            ++gq;
-            if (++st == NST) { st = 0; ph ^= 1; }
-            return true;
+                for (int part = 0; part < L::PARTS; ++part) {
+                    if (!wait_all(&ms.kv_full[st][part], ph)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint64_t dk = dk0 + st * (L::STAGE >> 4);
+#pragma unroll
+                    for (int k = part * L::PCH * 4; k < (part + 1) * L::PCH * 4; ++k)
+                        umma_bf16_warp(tS, dq + (((k / 4) * L::Q_CH + (k % 4) * 32) >> 4),
+                                       dk + ((L::chunk_at(k / 4) + (k % 4) * 32) >> 4), IDESC_QK, k > 0);
+                }
+                if (!ok) break;
+                umma_commit_warp(&ms.s_full[gq & 1]);
+                ++gq;
+                if (++st == NST) { st = 0; ph ^= 1; }
+            }
+            umma_commit_warp(&ms.q_empty);
+            f += g.tiles;
+            ++seg_i;
+        }
+        if (!ok) {
+            if (lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+        umma_commit_warp(&ms.qk_over);  // every MMA is done before TMEM is released
+        mbar_wait(&ms.qk_over, 0, nullptr);
+        __syncwarp();
+    } else if (warp == 6) {
+        // ------------------------------ PV issuer ------------------------------
+        auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
         };
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        // per M block: its two chunks may lie in different parts
+        uint64_t dv0[MB];
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+            dv0[mb] = umma_desc_sw128(smem_u32(sKV) + L::chunk_at(2 * mb),
+                                      L::chunk_at(2 * mb + 1) - L::chunk_at(2 * mb), L::GROUP);
+        const uint64_t dp = umma_desc_sw128(smem_u32(sP), 16, 1024);
+        uint32_t st = 0, gv = 0, seg_i = 0, moves = 0;
+        bool ok = true;
         for (int64_t f = lo; f < hi && ok;) {
             w.seek(sb, units, f);
             const AbsorbedSegment g = segment_at(a, w.q, w.pre, f, hi);
             const int tiles = __shfl_sync(0xffffffffu, g.tiles, 0);
             const int n = __shfl_sync(0xffffffffu, (g.rows + 15) & ~15, 0);
             const uint32_t idesc_pv = umma_idesc_bf16(128, n, 1, 0);
-            if (!wait_all(&ms.q_full, seg_i & 1) || !issue_qk()) { ok = false; break; }
-            if (tiles == 1) umma_commit_warp(&ms.q_empty);
-            for (int t = 0; t < tiles; ++t) {
-                if (t + 1 < tiles) {
-                    if (!issue_qk()) { ok = false; break; }
-                    if (t + 2 == tiles) umma_commit_warp(&ms.q_empty);
-                }
-                if (t == 0 && seg_i > 0 && !wait_all(&ms.o_free, (seg_i - 1) & 1)) { ok = false; break; }
+            if (seg_i > 0) ok = wait_all(&ms.o_free, (seg_i - 1) & 1);
+            for (int t = 0; t < tiles && ok; ++t) {
                 if (!wait_all(&ms.p_full, gv & 1)) { ok = false; break; }
+                const volatile int *mv = ms.moved[gv & 1];
+                if (__any_sync(0xffffffffu, mv[0] | mv[1] | mv[2] | mv[3])) {
+                    if (!wait_all(&ms.rescaled, moves & 1)) { ok = false; break; }
+                    ++moves;
+                }
                 tc_fence_after();
-                const uint64_t dv = dv0 + vst * (L::STAGE >> 4);
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb)
+                for (int mb = 0; mb < MB; ++mb) {
 #pragma unroll
                     for (int ks = 0; ks < kLatentTile / 16; ++ks)
-                        umma_bf16_warp(tm + L::COL_O + mb * kLatentRows, dv + ((mb * 2048 + ks * 2 * L::BOX) >> 4),
-                                       dp + ((ks * 32) >> 4), idesc_pv, t > 0 || ks > 0);
-                umma_commit_warp(&ms.kv_empty[vst]);
+                        umma_bf16_warp(tm + L::COL_O + mb * kLatentRows,
+                                       dv0[mb] + ((st * L::STAGE + ks * 2 * L::GROUP) >> 4), dp + ((ks * 32) >> 4),
+                                       idesc_pv, t > 0 || ks > 0);
+                    // a part is free behind the block that reads its last value chunk
+#pragma unroll
+                    for (int p = 0; p < L::PARTS; ++p)
+                        if (mb == min((p + 1) * L::PCH - 1, 2 * MB - 1) / 2) umma_commit_warp(&ms.kv_empty[st][p]);
+                }
                 umma_commit_warp(&ms.pv_done);
                 ++gv;
-                if (++vst == NST) vst = 0;
+                if (++st == NST) st = 0;
             }
             f += g.tiles;
             ++seg_i;
@@ -331,20 +408,24 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             if (lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
             *abort_flag = 1;
         }
-        if (issued) {  // every MMA is done before TMEM is released
-            umma_commit_warp(&ms.mma_done);
-            mbar_wait(&ms.mma_done, 0, nullptr);
-        }
+        umma_commit_warp(&ms.pv_over);
+        mbar_wait(&ms.pv_over, 0, nullptr);
         __syncwarp();
     } else {
-        // ------------- softmax: M = 64 puts row 16 q + i on TMEM lane 32 q + i -------------
+        // ------------- softmax: M = 64 puts row 16 q + i on TMEM lane 32 q + i, i < 16 -------------
         const int quarter = warp & 3;  // the TMEM lanes this warp may access
         const int tid = threadIdx.x - 64;
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t tO = tl + L::COL_O;
-        const bool has_row = lane < 16;
-        const int row = quarter * 16 + (lane & 15);
+        // S is read 16 lanes at a time over all 32 threads (tmem_ld_16x64): this thread has rows
+        // ra and ra + 8, a quarter of the columns of each.
+        const int ra = quarter * 16 + (lane >> 2);
+        const int c0 = 2 * (lane & 3);
         const float sl2 = a.scale_log2;
+        // where this lane's stmatrix rows go: rows 0..7 and 8..15 of the quarter, two 16-byte
+        // chunks of P at a time
+        const int pr = quarter * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+        const uint32_t p_row = smem_u32(sP) + pr * 128;
         uint32_t gt = 0;    // tiles seen
         uint32_t meets = 0; // meetings of the four warps
         bool ok = true;
@@ -352,114 +433,124 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
         };
-        // Meeting of the four warps that also tells whether any thread brought `x` (a barrier
-        // with a limit, unlike bar.sync).  Flags alternate: a warp writes meeting m + 2's only
-        // after every warp reached m + 1, past its reads of m.
-        auto meet = [&](bool x, bool &any) -> bool {
-            const bool mine = __any_sync(0xffffffffu, x);
-            int *fl = ms.flag[meets & 1];
-            if (lane == 0) {
-                fl[quarter] = mine;
-                mbar_arrive(&ms.group);
-            }
-            if (!wait_all(&ms.group, meets & 1)) return false;
-            any = (fl[0] | fl[1] | fl[2] | fl[3]) != 0;
-            ++meets;
+        // Meeting of the four warps (a barrier with a limit, unlike bar.sync).
+        auto meet = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.group);
+            return wait_all(&ms.group, meets++ & 1);
+        };
+        // O^T, after tile `tile`'s predecessors and before its own PV: every column (= row of the
+        // item) times the factor by which its reference maximum moved in that tile.
+        auto rescale_if_moved = [&](uint32_t tile, int ncols) -> bool {
+            if (!wait_all(&ms.p_full, tile & 1)) return false;  // every warp's say about the tile
+            const volatile int *mv = ms.moved[tile & 1];
+            if (!__any_sync(0xffffffffu, mv[0] | mv[1] | mv[2] | mv[3])) return true;
+            if (tile > 0 && !wait_all(&ms.pv_done, (tile - 1) & 1)) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll 1
+                for (int cb = 0; cb < ncols; cb += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(tO + mb * kLatentRows + cb, r);
+                    tmem_wait_ld();
+                    reg_order32(r);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        r[j] = __float_as_uint(__uint_as_float(r[j]) * ms.alpha[tile & 1][cb + j]);
+                    tmem_st32(tO + mb * kLatentRows + cb, r);
+                }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.rescaled);
             return true;
         };
         for (int64_t f = lo; f < hi && ok;) {
             w.seek(sb, units, f);
             const AbsorbedSegment g = segment_at(a, w.q, w.pre, f, hi);
             const int ctx = w.q.ctx;
-            const bool live = has_row && row < g.rows;
-            // keys this row may see; lanes without a row mask nothing
-            const int lim = !live || !a.causal ? ctx : ctx - w.q.q_len + (g.row_in_seq + row) / a.num_heads + 1;
+            const bool live[2] = {ra < g.rows, ra + 8 < g.rows};
+            int lim[2];  // keys the rows may see; rows past the item mask nothing
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                lim[k] = !live[k] || !a.causal
+                             ? ctx
+                             : ctx - w.q.q_len + (g.row_in_seq + ra + 8 * k) / a.num_heads + 1;
             const int ncols = (g.rows + 31) & ~31;  // TMEM columns of O^T to visit
-            float m_ref = -INFINITY, l = 0.f;
+            float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
             for (int t = 0; t < g.tiles; ++t, ++gt) {
                 const int64_t key0 = (int64_t)(g.kb + t) * kLatentTile;
+                if (t > 0 && !rescale_if_moved(gt - 1, ncols)) { ok = false; break; }  // its PV may wait for it
                 if (!wait_all(&ms.s_full[gt & 1], (gt >> 1) & 1)) { ok = false; break; }
                 tc_fence_after();
-                uint32_t v[64];
-                float red0, red1;
-                const uint32_t tS = tl + (gt & 1) * kLatentTile;
-                tmem_ld32_max(tS, reinterpret_cast<uint32_t(&)[32]>(v[0]), red0);
-                tmem_ld32_max(tS + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]), red1);
+                uint32_t v[32];
+                tmem_ld_16x64(tl + (gt & 1) * kLatentTile, v);
                 tmem_wait_ld();
-                reg_order32(reinterpret_cast<uint32_t(&)[32]>(v[0]));
-                reg_order32(reinterpret_cast<uint32_t(&)[32]>(v[32]));
-                float rm = fmaxf(red0, red1);
-                const int vis = (int)max64(0, min64(lim - key0, kLatentTile));
-                if (!__all_sync(0xffffffffu, vis >= kLatentTile)) {
-                    rm = -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) {
-                        if (j >= vis) v[j] = __float_as_uint(-INFINITY);
-                        rm = fmaxf(rm, __uint_as_float(v[j]));
-                    }
-                }
-                const float mx = rm * sl2;
-                const bool up = live && mx > m_ref + kRescaleSlack;
-                const float alpha = up ? fast_exp2(m_ref - mx) : 1.f;
-                if (up) {
-                    l *= alpha;
-                    m_ref = mx;
-                }
-                if (has_row) ms.alpha[gt & 1][row] = alpha;
+                reg_order32(v);
+                tc_fence_before();
                 __syncwarp();
-                bool rescale = false;
-                if (!meet(up && t > 0, rescale)) { ok = false; break; }
+                if (lane == 0) mbar_arrive(&ms.s_free[gt & 1]);
+                const int vis0 = (int)min64(lim[0] - key0, kLatentTile), vis1 = (int)min64(lim[1] - key0, kLatentTile);
+                if (!__all_sync(0xffffffffu, vis0 >= kLatentTile && vis1 >= kLatentTile)) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (8 * (j >> 2) + c0 + (j & 1) >= ((j & 2) ? vis1 : vis0)) v[j] = __float_as_uint(-INFINITY);
+                }
+                bool up[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        mx = fmax3(mx, __uint_as_float(v[4 * i + 2 * k]), __uint_as_float(v[4 * i + 2 * k + 1]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * sl2;  // scale > 0 keeps the order
+                    up[k] = live[k] && mx > m_ref[k] + kAbsorbedSlack;
+                    const float alpha = up[k] ? fast_exp2(m_ref[k] - mx) : 1.f;
+                    if (up[k]) {
+                        l[k] *= alpha;
+                        m_ref[k] = mx;
+                    }
+                    if ((lane & 3) == 0) ms.alpha[gt & 1][ra + 8 * k] = alpha;
+                }
+                const bool moved = __any_sync(0xffffffffu, (up[0] || up[1]) && t > 0);
+                if (lane == 0) ms.moved[gt & 1][quarter] = moved;
                 // The weights, while the tensor pipe finishes the last tile's PV.  The sum adds them as
                 // rounded, so a row that one key dominates loses nothing to their rounding.
-                const float base = m_ref == -INFINITY ? 0.f : m_ref;
-                uint32_t pk[32];
-                float s0 = 0.f, s1 = 0.f;
+                uint32_t pk[16];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float e0 = fast_exp2(fmaf(__uint_as_float(v[2 * j]), sl2, -base));
-                    const float e1 = fast_exp2(fmaf(__uint_as_float(v[2 * j + 1]), sl2, -base));
-                    pk[j] = pack_bf16x2(e0, e1);
-                    s0 += bf16_lo(pk[j]);
-                    s1 += bf16_hi(pk[j]);
-                }
-                l += s0 + s1;
-                if (gt > 0) {
-                    if (!wait_all(&ms.pv_done, (gt - 1) & 1)) { ok = false; break; }
-                    tc_fence_after();
-                }
-                if (rescale) {
-                    // O^T's columns are the rows: scale each by its row's factor (rare: the first
-                    // tiles of an item and jumps of a maximum by more than 2^8)
-#pragma unroll 1
-                    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll 1
-                        for (int cb = 0; cb < ncols; cb += 32) {
-                            uint32_t r[32];
-                            tmem_ld32(tO + mb * kLatentRows + cb, r);
-                            tmem_wait_ld();
-                            reg_order32(r);
+                for (int k = 0; k < 2; ++k) {
+                    const float base = m_ref[k] == -INFINITY ? 0.f : m_ref[k];
+                    float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                r[j] = __float_as_uint(__uint_as_float(r[j]) * ms.alpha[gt & 1][cb + j]);
-                            tmem_st32(tO + mb * kLatentRows + cb, r);
-                        }
-                    tmem_wait_st();
+                    for (int i = 0; i < 8; ++i) {
+                        const float e0 = fast_exp2(fmaf(__uint_as_float(v[4 * i + 2 * k]), sl2, -base));
+                        const float e1 = fast_exp2(fmaf(__uint_as_float(v[4 * i + 2 * k + 1]), sl2, -base));
+                        pk[2 * i + k] = pack_bf16x2(e0, e1);
+                        s0 += bf16_lo(pk[2 * i + k]);
+                        s1 += bf16_hi(pk[2 * i + k]);
+                    }
+                    l[k] += s0 + s1;
                 }
-                if (has_row) {
+                // P has one place: the last tile's PV comes first
+                if (gt > 0 && !wait_all(&ms.pv_done, (gt - 1) & 1)) { ok = false; break; }
 #pragma unroll
-                    for (int cc = 0; cc < 8; ++cc)
-                        *reinterpret_cast<uint4 *>(sP + row * 128 + ((cc ^ (row & 7)) << 4)) =
-                            make_uint4(pk[4 * cc], pk[4 * cc + 1], pk[4 * cc + 2], pk[4 * cc + 3]);
-                }
+                for (int i = 0; i < 8; i += 2)  // 16-byte chunks i and i + 1 of the quarter's 16 rows
+                    stmatrix_x4(p_row + (((i + (lane >> 4)) ^ (pr & 7)) << 4), pk[2 * i], pk[2 * i + 1], pk[2 * i + 2],
+                                pk[2 * i + 3]);
                 if (key0 + kLatentTile > ctx) {
                     // Slots past the context may hold NaN, and 0 * NaN would reach O^T: their value
                     // columns are zeroed once the copy has landed.
                     const uint32_t st = gt % NST;
-                    if (!wait_all(&ms.kv_full[st], (gt / NST) & 1)) { ok = false; break; }
+                    bool landed = true;
+#pragma unroll
+                    for (int p = 0; p < L::PARTS; ++p) landed = landed && wait_all(&ms.kv_full[st][p], (gt / NST) & 1);
+                    if (!landed) { ok = false; break; }
                     const int r0 = (int)(ctx - key0), pieces = (kLatentTile - r0) * (R / 8);
                     for (int i = tid; i < pieces; i += 128) {
                         const int rr = r0 + i / (R / 8), x = i % (R / 8);
-                        *reinterpret_cast<uint4 *>(sKV + st * L::STAGE + (rr >> 3) * L::BOX + (x >> 3) * 1024 +
+                        *reinterpret_cast<uint4 *>(sKV + st * L::STAGE + (rr >> 3) * L::GROUP + L::chunk_at(x >> 3) +
                                                    (rr & 7) * 128 + ((x & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
@@ -469,15 +560,22 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 if (lane == 0) mbar_arrive(&ms.p_full);
             }
             if (!ok) break;
+            if (!rescale_if_moved(gt - 1, ncols)) { ok = false; break; }
             // ---- epilogue: O / l of a whole item, or the part for the merge ----
             if (!wait_all(&ms.pv_done, (gt - 1) & 1)) { ok = false; break; }
             tc_fence_after();
-            if (has_row) ms.inv[row] = l > 0.f ? 1.f / l : 0.f;
-            __syncwarp();
-            bool any;
-            if (!meet(false, any)) { ok = false; break; }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {  // the four threads of a row hold its sum in parts
+                l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+                l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+                if ((lane & 3) == 0) ms.inv[ra + 8 * k] = l[k] > 0.f ? 1.f / l[k] : 0.f;
+            }
+            if (!meet()) { ok = false; break; }
             const int slot = g.whole ? 0 : part_slot(c, g.item_begin, T, ge);
-            if (!g.whole && live) a.ws_ml[(int64_t)slot * kLatentRows + row] = make_float2(m_ref, l);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (!g.whole && live[k] && (lane & 3) == 0)
+                    a.ws_ml[(int64_t)slot * kLatentRows + ra + 8 * k] = make_float2(m_ref[k], l[k]);
             const int odd = lane & 1;
 #pragma unroll 1
             for (int mb = 0; mb < MB; ++mb)
@@ -510,8 +608,8 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 }
             tc_fence_before();
             if (lane == 0) mbar_arrive(&ms.o_free);
-            // inv is written again only after the next item's first meeting, which every warp
-            // reaches past its reads
+            // inv is written again only behind the next item's tiles, whose weights every warp's
+            // arrival is part of
             f += g.tiles;
         }
         if (!ok) {
@@ -533,6 +631,10 @@ void plan_absorbed(int latent_dim, int sms, AbsorbedPlan *p) {
     p->off_ml = up(sizeof(MergeJob) * (size_t)p->grid);
     p->off_o = p->off_ml + up(2 * (size_t)p->grid * kLatentRows * sizeof(float2));
     p->ws_bytes = p->off_o + up(2 * (size_t)p->grid * kLatentRows * latent_dim * sizeof(float));
+}
+
+int absorbed_box_chunks(int latent_dim) {
+    return latent_dim == 512 ? AbsorbedSmem<512>::PCH : AbsorbedSmem<256>::PCH;
 }
 
 template <int R>

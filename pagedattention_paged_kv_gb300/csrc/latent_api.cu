@@ -40,14 +40,15 @@ int check_latent(int num_seqs, int total_q, int max_blocks_per_seq, int num_head
     return PKV_OK;
 }
 
-// The cache as (64 columns, token in block, 64-column chunk, block): a box of 8 tokens x all
-// chunks lands as [chunk][token][64 columns].
-int encode_latent_map(CUtensorMap *map, const void *cache, int64_t num_blocks, int block_size, int row_cols) {
+// The cache as (64 columns, token in group, 64-column chunk, group of 8 tokens, block): a box of
+// one block (at most 64 tokens) x box_chunks chunks lands as [group][chunk][8 tokens][64 columns].
+int encode_latent_map(CUtensorMap *map, const void *cache, int64_t num_blocks, int block_size, int row_cols,
+                      int box_chunks) {
     const uint64_t row = (uint64_t)row_cols * 2;
-    const uint64_t dims[4] = {64, (uint64_t)block_size, (uint64_t)(row_cols / 64), (uint64_t)num_blocks};
-    const uint64_t strides[3] = {row, 128, row * block_size};
-    const uint32_t box[4] = {64, 8, (uint32_t)(row_cols / 64), 1};
-    return pkv::encode_tiled(map, 4, cache, dims, strides, box);
+    const uint64_t dims[5] = {64, 8, (uint64_t)(row_cols / 64), (uint64_t)(block_size / 8), (uint64_t)num_blocks};
+    const uint64_t strides[4] = {row, 128, row * 8, row * block_size};
+    const uint32_t box[5] = {64, 8, (uint32_t)box_chunks, (uint32_t)(block_size / 8), 1};
+    return pkv::encode_tiled(map, 5, cache, dims, strides, box);
 }
 
 }  // namespace
@@ -160,11 +161,12 @@ extern "C" int pkv_latent_attention_absorbed(void *out, const void *q, const int
     if (!aligned_to(workspace, 256)) return PKV_ERR_INVALID_ARG;
     const int cols = latent_dim + rope_dim;
     CUtensorMap qmap, kvmap;
-    const uint64_t qdims[2] = {(uint64_t)cols, (uint64_t)total_q_tokens * num_heads};
-    const uint64_t qstride[1] = {(uint64_t)cols * 2};
-    const uint32_t qbox[2] = {64, (uint32_t)pkv::kLatentRows};
-    st = pkv::encode_tiled(&qmap, 2, q, qdims, qstride, qbox);
-    if (st == PKV_OK) st = encode_latent_map(&kvmap, latent_cache, num_blocks, block_size, cols);
+    const uint64_t qdims[3] = {64, (uint64_t)total_q_tokens * num_heads, (uint64_t)(cols / 64)};
+    const uint64_t qstride[2] = {(uint64_t)cols * 2, 128};
+    const uint32_t qbox[3] = {64, (uint32_t)pkv::kLatentRows, (uint32_t)(cols / 64)};
+    st = pkv::encode_tiled(&qmap, 3, q, qdims, qstride, qbox);
+    if (st == PKV_OK) st = encode_latent_map(&kvmap, latent_cache, num_blocks, block_size, cols,
+                                                 pkv::absorbed_box_chunks(latent_dim));
     if (st != PKV_OK) return st;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     pkv::AbsorbedArgs a;
@@ -228,7 +230,8 @@ extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int
     buf.padded = p.padded;
 
     CUtensorMap latmap, wkmap, wvmap, qmap, kvmap, ropemap;
-    st = encode_latent_map(&latmap, latent_cache, num_blocks, block_size, latent_dim + rope_dim);
+    st = encode_latent_map(&latmap, latent_cache, num_blocks, block_size, latent_dim + rope_dim,
+                           (latent_dim + rope_dim) / 64);
     const uint64_t wdims[2] = {(uint64_t)latent_dim, (uint64_t)num_heads * pkv::kExpHeadDim};
     const uint64_t wstride[1] = {(uint64_t)latent_dim * 2};
     const uint32_t rows128[2] = {64, 128};

@@ -45,8 +45,7 @@ struct ExpandMisc {
     uint64_t w_full[4], w_empty[4];
     uint64_t acc_full[2], acc_free[2];
     int64_t scan[8];
-    int64_t start_pre;
-    int start_seq;
+    WalkStart start;
     uint32_t tmem_slot;
     int abort_flag;
 };
@@ -129,14 +128,14 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
     const int ge = split_ctas(T, a.grid, 1);
     if (T == 0 || c >= ge) return;
     const int64_t lo = share_begin(c, T, ge), hi = share_begin(c + 1, T, ge);
-    find_unit(sb, units, sc, lo, &ms.start_seq, &ms.start_pre);
+    find_unit(sb, units, sc, lo, &ms.start);
     if (warp == 1) tmem_alloc(&ms.tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ms.tmem_slot;
     SeqWalk<ExpandUnits> w;
-    w.start(sb, units, ms.start_seq, ms.start_pre);
+    w.start(ms.start);
     auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
     };
@@ -151,12 +150,14 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
             const int64_t o = f - w.pre;
             const int tile = (int)(o / H), h = (int)(o - (int64_t)tile * H);
             if (f == lo || h == 0) {
-                // the tile's 16 groups of 8 tokens, one a lane
-                const int64_t pos = (int64_t)tile * kExpTile + 8 * lane;
-                const int boxes = (int)min64(kExpTile / 8, (w.q.ctx - (int64_t)tile * kExpTile + 7) >> 3);
+                // the tile's blocks, one a lane (at most 16)
+                const int64_t b0 = (int64_t)tile * kExpTile >> a.block_shift;
+                const int64_t seq_blocks = ((int64_t)w.q.ctx + (1 << a.block_shift) - 1) >> a.block_shift;
+                const int boxes = (int)min64(kExpTile >> a.block_shift, seq_blocks - b0);
+                const int box_bytes = L::BOX << (a.block_shift - 3);
                 int bid = -1;
                 if (lane < boxes) {
-                    bid = a.block_tables[(int64_t)w.s * a.max_blocks_per_seq + (pos >> a.block_shift)];
+                    bid = a.block_tables[(int64_t)w.s * a.max_blocks_per_seq + b0 + lane];
                     if (bid < 0 || bid >= a.num_blocks) {
                         flag_error(a.err, PKV_DEVERR_BLOCK_ID);
                         bid = -1;  // an out-of-range box is filled with zeros
@@ -164,11 +165,12 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
                 }
                 ok = aloads == 0 || wait_all(&ms.a_empty, (aloads - 1) & 1);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&ms.a_full, boxes * L::BOX);
-                __syncwarp();
-                if (lane < boxes)
-                    tma_load_4d(sA + lane * L::BOX, &kv_map, &ms.a_full, 0,
-                                (int)(pos & ((1 << a.block_shift) - 1)), 0, bid, policy);
+                if (lane == 0) mbar_arrive_expect_tx(&ms.a_full, boxes * box_bytes);
+#pragma unroll 1
+                for (int i = 0; i < boxes; ++i) {
+                    const int id = __shfl_sync(0xffffffffu, bid, i);
+                    if (lane == 0) tma_load_5d(sA + i * box_bytes, &kv_map, &ms.a_full, 0, 0, 0, 0, id, policy);
+                }
                 ++aloads;
             }
             if (lane == 0) {

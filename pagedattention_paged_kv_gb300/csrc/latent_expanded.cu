@@ -53,8 +53,7 @@ struct ExpandedMisc {
     uint64_t k_full[2], k_empty[2];
     uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
     int64_t scan[16];
-    int64_t start_pre;
-    int start_seq;
+    WalkStart start;
     uint32_t tmem_slot;
     int abort_flag;
 };
@@ -181,7 +180,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     const int ge = split_ctas(T, a.grid, 1);
     const bool works = T > 0 && c < ge;
     const int64_t lo = works ? share_begin(c, T, ge) : 0, hi = works ? share_begin(c + 1, T, ge) : 0;
-    if (works) find_unit(sb, units, sc, lo, &ms.start_seq, &ms.start_pre);
+    if (works) find_unit(sb, units, sc, lo, &ms.start);
     __syncthreads();
 
     // The merge job of the boundary before this CTA's share (see latent_absorbed.cu).
@@ -189,8 +188,8 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         MergeJob j;
         no_job(j);
         if (works && c > 0) {
-            const SeqInfo q = read_seq(sb, ms.start_seq, false);
-            const ExpandedSegment g = expanded_segment(q, a.causal, ms.start_pre, lo, hi);
+            const SeqInfo q = ms.start.q;
+            const ExpandedSegment g = expanded_segment(q, a.causal, ms.start.pre, lo, hi);
             if (g.kb != 0 && g.tile_begin >= share_begin(c - 1, T, ge)) {
                 j.item_begin = g.tile_begin;
                 j.total_units = T;
@@ -209,7 +208,8 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             a.ws_jobs[c] = j;
         }
     }
-    zero_dead_rows(sb, c, a.grid, a.out, (int64_t)a.num_heads * kExpHeadDim, !fits);
+    zero_dead_rows(sb, c, a.grid, a.out, (int64_t)a.num_heads * kExpHeadDim, warp,
+                   kExpandedThreads / 32, !fits);
     if (!works) return;
 
     if (warp == 1) tmem_alloc(&ms.tmem_slot, 512);
@@ -218,7 +218,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     tc_fence_after();
     const uint32_t tmem = ms.tmem_slot;
     SeqWalk<ExpandedUnits> w;
-    w.start(sb, units, ms.start_seq, ms.start_pre);
+    w.start(ms.start);
     auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
     };

@@ -95,22 +95,37 @@ __device__ __forceinline__ BatchScan scan_batch(const SeqBatch &b, const Units &
     return r;
 }
 
-// The sequence that holds unit f and the units before it: the one thread whose run holds f
-// writes them.  Callers synchronise afterwards.
+// Where a CTA's share starts: the sequence that holds its first unit.
+struct WalkStart {
+    int64_t pre, units;  // units before the sequence, its units
+    SeqInfo q;
+    int s;
+};
+
+// The one thread whose run holds unit f writes *start.  Callers synchronise afterwards.
 template <typename Units>
 __device__ __forceinline__ void find_unit(const SeqBatch &b, const Units &units, const BatchScan &sc, int64_t f,
-                                          int *seq, int64_t *pre) {
+                                          WalkStart *start) {
     if (f < sc.run || f >= sc.run + sc.local) return;
     int64_t run = sc.run;
     for (int s = sc.beg; s < sc.end; ++s) {
-        const int64_t u = seq_units_of(b, units, s, false);
+        const SeqInfo q = read_seq(b, s, false);
+        const int64_t u = q.q_len == 0 || q.dead ? 0 : units(q);
         if (f < run + u) {
-            *seq = s;
-            *pre = run;
+            start->pre = run;
+            start->units = u;
+            start->q = q;
+            start->s = s;
             return;
         }
         run += u;
     }
+}
+
+// a / b for a >= 0, b > 0; the 64-bit division, many times slower, only where it is needed.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
 }
 
 // A warp's walk over the sequences from a starting one on, 32 sequences to a round of loads.
@@ -143,10 +158,14 @@ struct SeqWalk {
         q.dead = false;
         units = __shfl_sync(0xffffffffu, my_units, l);
     }
-    __device__ __forceinline__ void start(const SeqBatch &b, const Units &u, int seq, int64_t before) {
-        load(b, u, seq);
-        pre = before;
-        take(0);
+    // The sequences behind the first are loaded by the first seek that leaves it.
+    __device__ __forceinline__ void start(const WalkStart &st) {
+        s = st.s;
+        pre = st.pre;
+        units = st.units;
+        q = st.q;
+        base = s - 31;  // the last lane's sequence: no lane holds a later one
+        my_units = 0;
     }
     // Moves on until the current sequence holds unit f (f >= pre, f below the batch's total).
     __device__ __forceinline__ void seek(const SeqBatch &b, const Units &u, int64_t f) {
@@ -165,12 +184,12 @@ struct SeqWalk {
     }
 };
 
-// Zero rows of the dead sequences (of every one, with `all`) among cta, cta + grid, ...; one
-// warp a sequence.
+// Zero rows of the dead sequences (of every one, with `all`) among cta, cta + grid, ..., by warp
+// `w` of `nw`; one warp a sequence.
 __device__ __forceinline__ void zero_dead_rows(const SeqBatch &b, int cta, int grid, __nv_bfloat16 *out,
-                                               int64_t row_elems, bool all = false) {
-    const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
-    for (int64_t s = cta + (int64_t)grid * (threadIdx.x >> 5); s < b.num_seqs; s += (int64_t)grid * nw) {
+                                               int64_t row_elems, int w, int nw, bool all = false) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t s = cta + (int64_t)grid * w; s < b.num_seqs; s += (int64_t)grid * nw) {
         const SeqInfo q = read_seq(b, (int)s, false);
         if (q.q_len == 0 || !(q.dead || all)) continue;
         uint4 *o = reinterpret_cast<uint4 *>(out + q.q0 * row_elems);
