@@ -335,28 +335,65 @@ def paged_attention_decode_kvwrite(out, q, k_new, v_new, k_cache, v_cache, block
         _check(lib().pkv_paged_attention_decode_kvwrite(*args, DTYPE_BF16, *tail), "paged_attention_decode_kvwrite")
 
 
-def _on_current_device(*tensors):
+def _on_current_device(dev: int) -> None:
     """The library launches on the current device: tensors of another one are refused."""
     import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensor on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
-def _call_workspace(workspace, nbytes, like, stream):
-    """The caller's workspace (a contiguous CUDA buffer of enough bytes), or a fresh one that
-    stays alive until `stream` is past the call."""
+def _bad_tensor(t, dtype, name, ndim, dev):
+    """The complaint about a tensor that _ptrs refused."""
+    _require(t, dtype, name, ndim)
+    raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{dev}")
+
+
+def _ptrs(dev, dtype, *named):
+    """Addresses of tensors given as (tensor, name, ndim), checked to be contiguous, of dtype and
+    on CUDA device dev.  The calls below run in a few microseconds on the GPU, so their checks
+    are kept to one look at each property."""
+    out = []
+    for t, name, ndim in named:
+        try:
+            if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or t.dim() != ndim:
+                _bad_tensor(t, dtype, name, ndim, dev)
+            out.append(t.data_ptr())
+        except AttributeError:
+            raise ValueError(f"{name} must be a CUDA tensor") from None
+    return out
+
+
+def _device_of(t, name) -> int:
+    """The CUDA device of a call's first tensor, which has to be the current one."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():
+        _on_current_device(dev)
+    return dev
+
+
+def _raw_stream(stream, dev):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _call_workspace(workspace, nbytes, dev, stream):
+    """(address, bytes, owner) of the caller's workspace (a contiguous CUDA buffer of enough
+    bytes), or of a fresh one that stays alive until `stream` is past the call."""
     import torch
     if workspace is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
         if stream is not None:
             ws.record_stream(stream)
-        return ws
-    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    _on_current_device(workspace)
-    return _workspace(workspace, nbytes, like.device)
+        return ws.data_ptr(), nbytes, ws
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    have = workspace.numel() * workspace.element_size()
+    if have < nbytes:
+        raise PagedKVError(-3, "workspace")
+    return workspace.data_ptr(), have, workspace
 
 
 def step_metadata(block_tables, context_lens, query_start_loc, slot_mapping, free_end, cached_lens, new_lens,
@@ -367,41 +404,37 @@ def step_metadata(block_tables, context_lens, query_start_loc, slot_mapping, fre
     token), and the new entries of block_tables [S, MB] int32.  context_lens may be cached_lens
     and free_end may be free_begin: a replayed call then advances its own state."""
     import torch
-    i32 = torch.int32
-    _require(block_tables, i32, "block_tables", 2)
-    for t, n in ((context_lens, "context_lens"), (query_start_loc, "query_start_loc"), (free_end, "free_end"),
-                 (cached_lens, "cached_lens"), (new_lens, "new_lens"), (free_blocks, "free_blocks"),
-                 (free_begin, "free_begin")):
-        _require(t, i32, n, 1)
-    _require(slot_mapping, torch.int64, "slot_mapping", 1)
-    _on_current_device(block_tables, context_lens, query_start_loc, slot_mapping, free_end, cached_lens, new_lens,
-                       free_blocks, free_begin)
-    S = cached_lens.shape[0]
-    if new_lens.shape[0] != S or context_lens.shape[0] != S or block_tables.shape[0] != S \
-            or query_start_loc.shape[0] != S + 1 or free_end.shape[0] != 1 or free_begin.shape[0] != 1:
+    dev = _device_of(block_tables, "block_tables")
+    bt, cl, qsl, fe, ca, ne, fb, fbeg = _ptrs(
+        dev, torch.int32, (block_tables, "block_tables", 2), (context_lens, "context_lens", 1),
+        (query_start_loc, "query_start_loc", 1), (free_end, "free_end", 1), (cached_lens, "cached_lens", 1),
+        (new_lens, "new_lens", 1), (free_blocks, "free_blocks", 1), (free_begin, "free_begin", 1))
+    sm, = _ptrs(dev, torch.int64, (slot_mapping, "slot_mapping", 1))
+    S, MB = block_tables.shape
+    if new_lens.numel() != S or cached_lens.numel() != S or context_lens.numel() != S \
+            or query_start_loc.numel() != S + 1 or free_end.numel() != 1 or free_begin.numel() != 1:
         raise ValueError("shape mismatch")
-    _check(lib().pkv_step_metadata(
-        _ptr(block_tables), _ptr(context_lens), _ptr(query_start_loc), _ptr(slot_mapping), _ptr(free_end),
-        _ptr(cached_lens), _ptr(new_lens), _ptr(free_blocks), _ptr(free_begin), S, block_tables.shape[1],
-        slot_mapping.shape[0], free_blocks.shape[0], int(num_blocks), int(block_size), _stream_ptr(stream)),
-        "step_metadata")
+    st = lib().pkv_step_metadata(bt, cl, qsl, sm, fe, ca, ne, fb, fbeg, S, MB, slot_mapping.numel(),
+                                 free_blocks.numel(), num_blocks, block_size, _raw_stream(stream, dev))
+    if st:
+        raise PagedKVError(st, "step_metadata")
 
 
 def latent_cache_write(latent_cache, latent, rope, slot_mapping, stream=None) -> None:
     """latent_cache [NB, bs, R + P] bf16 <- rows [latent ; rope] (latent [T, R], rope [T, P] bf16)
     at int64 slot_mapping [T]; negative slots are skipped."""
     import torch
-    _require(latent_cache, torch.bfloat16, "latent_cache", 3)
-    _require(latent, torch.bfloat16, "latent", 2)
-    _require(rope, torch.bfloat16, "rope", 2)
-    _require(slot_mapping, torch.int64, "slot_mapping", 1)
-    _on_current_device(latent_cache, latent, rope, slot_mapping)
+    dev = _device_of(latent_cache, "latent_cache")
+    lc, la, ro = _ptrs(dev, torch.bfloat16, (latent_cache, "latent_cache", 3), (latent, "latent", 2), (rope, "rope", 2))
+    sm, = _ptrs(dev, torch.int64, (slot_mapping, "slot_mapping", 1))
     NB, bs, cols = latent_cache.shape
     T, R = latent.shape
-    if rope.shape[0] != T or slot_mapping.shape[0] != T or R + rope.shape[1] != cols:
+    P = cols - R
+    if tuple(rope.shape) != (T, P) or slot_mapping.numel() != T:
         raise ValueError("shape mismatch")
-    _check(lib().pkv_latent_cache_write(_ptr(latent_cache), _ptr(latent), _ptr(rope), _ptr(slot_mapping), T, NB, bs,
-                                        R, rope.shape[1], DTYPE_BF16, _stream_ptr(stream)), "latent_cache_write")
+    st = lib().pkv_latent_cache_write(lc, la, ro, sm, T, NB, bs, R, P, DTYPE_BF16, _raw_stream(stream, dev))
+    if st:
+        raise PagedKVError(st, "latent_cache_write")
 
 
 def latent_workspace_size(op: int, num_seqs: int, total_q_tokens: int, num_heads: int, latent_dim: int,
@@ -413,22 +446,20 @@ def latent_workspace_size(op: int, num_seqs: int, total_q_tokens: int, num_heads
     return int(n)
 
 
-def _latent_common(out, q, latent_cache, block_tables, context_lens, query_start_loc):
+def _latent_tensors(out, q, latent_cache, block_tables, context_lens, query_start_loc):
+    """(device, sequences, addresses) of the tensors both forms take, checked."""
     import torch
-    _require(out, torch.bfloat16, "out", 3)
-    _require(q, torch.bfloat16, "q", 3)
-    _require(latent_cache, torch.bfloat16, "latent_cache", 3)
-    _require(block_tables, torch.int32, "block_tables", 2)
-    _require(context_lens, torch.int32, "context_lens", 1)
+    dev = _device_of(q, "q")
+    po, pq, pc = _ptrs(dev, torch.bfloat16, (out, "out", 3), (q, "q", 3), (latent_cache, "latent_cache", 3))
+    pt, pl = _ptrs(dev, torch.int32, (block_tables, "block_tables", 2), (context_lens, "context_lens", 1))
+    S = context_lens.numel()
+    ps = None
     if query_start_loc is not None:
-        _require(query_start_loc, torch.int32, "query_start_loc", 1)
-    _on_current_device(out, q, latent_cache, block_tables, context_lens, query_start_loc)
-    S = context_lens.shape[0]
-    if tuple(out.shape[:2]) != tuple(q.shape[:2]) or block_tables.shape[0] != S \
-            or (query_start_loc is not None and query_start_loc.shape[0] != S + 1) \
-            or (query_start_loc is None and q.shape[0] != S):
+        ps, = _ptrs(dev, torch.int32, (query_start_loc, "query_start_loc", 1))
+    if out.shape[:2] != q.shape[:2] or block_tables.shape[0] != S \
+            or (q.shape[0] != S if query_start_loc is None else query_start_loc.numel() != S + 1):
         raise ValueError("shape mismatch")
-    return S
+    return dev, S, (po, pq, ps, pc, pt, pl)
 
 
 def latent_attention_absorbed(out, q, latent_cache, block_tables, context_lens, scale: float, query_start_loc=None,
@@ -437,19 +468,19 @@ def latent_attention_absorbed(out, q, latent_cache, block_tables, context_lens, 
     rotary part), out [T, H, R] bf16 (to be multiplied by W_v), latent_cache [NB, bs, R + P] bf16,
     block_tables [S, MB] int32, context_lens [S] int32.  Without query_start_loc one row per
     sequence; with it [S + 1] int32 (device), each sequence's last q_len positions."""
-    S = _latent_common(out, q, latent_cache, block_tables, context_lens, query_start_loc)
+    dev, S, ptrs = _latent_tensors(out, q, latent_cache, block_tables, context_lens, query_start_loc)
     T, H, cols = q.shape
     NB, bs, ccols = latent_cache.shape
     R = out.shape[2]
     if ccols != cols or cols <= R:
         raise ValueError("shape mismatch")
     n = latent_workspace_size(OP_LATENT_ABSORBED, S, T, H, R, cols - R)
-    ws = _call_workspace(workspace, n, q, stream)
-    _check(lib().pkv_latent_attention_absorbed(
-        _ptr(out), _ptr(q), _ptr(query_start_loc) if query_start_loc is not None else None, _ptr(latent_cache),
-        _ptr(block_tables), _ptr(context_lens), S, T, block_tables.shape[1], H, R, cols - R, bs, NB, float(scale),
-        int(bool(causal)), DTYPE_BF16, _ptr(ws), ws.numel() * ws.element_size(), _stream_ptr(stream)),
-        "latent_attention_absorbed")
+    ws, have, keep = _call_workspace(workspace, n, dev, stream)
+    st = lib().pkv_latent_attention_absorbed(
+        *ptrs, S, T, block_tables.shape[1], H, R, cols - R, bs, NB, scale, bool(causal), DTYPE_BF16, ws, have,
+        _raw_stream(stream, dev))
+    if st:
+        raise PagedKVError(st, "latent_attention_absorbed")
 
 
 def latent_attention_expanded(out, q, query_start_loc, latent_cache, block_tables, context_lens, w_k, w_v,
@@ -460,24 +491,24 @@ def latent_attention_expanded(out, q, query_start_loc, latent_cache, block_table
     latent_cache [NB, bs, R + P] bf16, w_k and w_v [H, 128, R] bf16; total_context is at least the
     sum of context_lens of the sequences with query rows (host)."""
     import torch
-    S = _latent_common(out, q, latent_cache, block_tables, context_lens, query_start_loc)
-    _require(w_k, torch.bfloat16, "w_k", 3)
-    _require(w_v, torch.bfloat16, "w_v", 3)
-    _on_current_device(w_k, w_v)
+    if query_start_loc is None:
+        raise ValueError("query_start_loc must be a CUDA tensor")
+    dev, S, ptrs = _latent_tensors(out, q, latent_cache, block_tables, context_lens, query_start_loc)
+    pk, pv = _ptrs(dev, torch.bfloat16, (w_k, "w_k", 3), (w_v, "w_v", 3))
     T, H, qcols = q.shape
     NB, bs, cols = latent_cache.shape
-    nope, R = w_k.shape[1:]
+    Hk, nope, R = w_k.shape
     P = cols - R
-    if query_start_loc is None or w_k.shape[0] != H or w_v.shape[0] != H or w_v.shape[2] != R \
-            or out.shape[2] != w_v.shape[1] or P <= 0 or qcols != nope + P:
+    if Hk != H or w_v.shape[0] != H or w_v.shape[2] != R or out.shape[2] != w_v.shape[1] or P <= 0 \
+            or qcols != nope + P:
         raise ValueError("shape mismatch")
     n = latent_workspace_size(OP_LATENT_EXPANDED, S, T, H, R, P, total_context)
-    ws = _call_workspace(workspace, n, q, stream)
-    _check(lib().pkv_latent_attention_expanded(
-        _ptr(out), _ptr(q), _ptr(query_start_loc), _ptr(latent_cache), _ptr(block_tables), _ptr(context_lens),
-        _ptr(w_k), _ptr(w_v), S, T, int(total_context), block_tables.shape[1], H, R, P, nope, w_v.shape[1], bs, NB,
-        float(scale), int(bool(causal)), DTYPE_BF16, _ptr(ws), ws.numel() * ws.element_size(), _stream_ptr(stream)),
-        "latent_attention_expanded")
+    ws, have, keep = _call_workspace(workspace, n, dev, stream)
+    st = lib().pkv_latent_attention_expanded(
+        *ptrs, pk, pv, S, T, total_context, block_tables.shape[1], H, R, P, nope, w_v.shape[1], bs, NB, scale,
+        bool(causal), DTYPE_BF16, ws, have, _raw_stream(stream, dev))
+    if st:
+        raise PagedKVError(st, "latent_attention_expanded")
 
 
 def copy_blocks(k_cache, v_cache, block_pairs, stream=None) -> None:

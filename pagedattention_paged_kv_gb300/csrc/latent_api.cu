@@ -183,7 +183,7 @@ extern "C" int pkv_latent_attention_absorbed(void *out, const void *q, const int
     a.causal = causal != 0;
     a.num_blocks = num_blocks;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.ws_jobs = reinterpret_cast<pkv::MergeJob *>(ws + p.off_jobs);
+    a.ws_jobs = reinterpret_cast<pkv::AbsorbedJob *>(ws + p.off_jobs);
     a.ws_ml = reinterpret_cast<float2 *>(ws + p.off_ml);
     a.ws_o = reinterpret_cast<float *>(ws + p.off_o);
     a.err = d.err;

@@ -127,12 +127,6 @@ __device__ __forceinline__ ExpandedSegment expanded_segment(const SeqInfo &q, bo
     return g;
 }
 
-__device__ __forceinline__ void st_global_32(void *p, const uint32_t (&v)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-
 }  // namespace
 
 __global__ void __launch_bounds__(kExpandedThreads, 1)
