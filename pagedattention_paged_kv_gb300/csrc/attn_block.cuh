@@ -55,6 +55,26 @@ cudaError_t allow_dynamic_smem(void (*kernel)(Params...), size_t smem, SmemAllow
     return cudaSuccess;
 }
 
+// launch_pdl (below) with the grid in clusters of `cluster` CTAs.
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, int cluster, size_t smem,
+                               cudaStream_t stream, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 // Launches `kernel` on `stream` with programmatic stream serialization, so that its
 // launch overlaps the tail of the previous kernel (the kernel calls pdl_wait before it
 // touches memory).

@@ -230,8 +230,7 @@ extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int
     buf.padded = p.padded;
 
     CUtensorMap latmap, wkmap, wvmap, qmap, kvmap, ropemap;
-    st = encode_latent_map(&latmap, latent_cache, num_blocks, block_size, latent_dim + rope_dim,
-                           (latent_dim + rope_dim) / 64);
+    st = encode_latent_map(&latmap, latent_cache, num_blocks, block_size, latent_dim + rope_dim, latent_dim / 64);
     const uint64_t wdims[2] = {(uint64_t)latent_dim, (uint64_t)num_heads * pkv::kExpHeadDim};
     const uint64_t wstride[1] = {(uint64_t)latent_dim * 2};
     const uint32_t rows128[2] = {64, 128};
@@ -256,12 +255,13 @@ extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int
     e.query_start_loc = query_start_loc;
     e.block_tables = block_tables;
     e.context_lens = context_lens;
+    e.cache = static_cast<const __nv_bfloat16 *>(latent_cache);
     e.num_seqs = num_seqs;
     e.total_q = total_q_tokens;
     e.max_blocks_per_seq = max_blocks_per_seq;
     e.block_shift = block_shift(block_size);
     e.num_heads = num_heads;
-    e.grid = p.grid;
+    e.grid = p.grid / 2 * 2;
     e.num_blocks = num_blocks;
     e.buf = buf;
     e.err = d.err;

@@ -8,12 +8,16 @@
 // is clamped to it and flagged PKV_DEVERR_VALUE.
 //
 // Bound: tensor.  2 * 256 * R operations against 512 bytes written a (token, head): 512
-// operations a byte at R = 512.  A CTA keeps 128 tokens (all of R) in shared memory and streams
-// the weights of one head after the other past them in 64-column chunks; the accumulator
-// (128 tokens x 256 columns, half of TMEM) is double-buffered, so the stores of one head run
-// under the products of the next.  Units are (128-token tile, head) pairs, cut into equal
-// contiguous shares, so a CTA reloads its tokens only when its share crosses a tile.
-// Waits are bounded in time; no CTA waits on another CTA.
+// operations a byte at R = 512.  What feeds the tensor pipe is the question: a CTA keeps 128
+// tokens (all of R) in shared memory and streams the weights of one head after the other past
+// them, 64 bytes a cycle at the full rate, about twice what the L2 gives each of 152 SMs at
+// once.  So two CTAs with a token tile each form a cluster that walks the heads in step: each
+// loads half of every weight chunk and multicasts it to both.  The accumulator (128 tokens x
+// 256 columns, half of TMEM) is double-buffered, so the stores of one head run under the
+// products of the next.  Units are (pair of token tiles, head), cut into equal contiguous
+// shares, so a cluster reloads its tokens only when its share crosses a pair.
+// Waits are bounded in time.  The CTAs of a cluster (always resident together) wait for each
+// other's weight halves; no cluster waits for another.
 #include "attn_block.cuh"
 #include "latent_expanded.cuh"
 #include "latent_walk.cuh"
@@ -28,14 +32,14 @@ constexpr int kExpandThreads = 192;  // loads, MMAs, four epilogue warps
 
 template <int R>
 struct ExpandSmem {
-    static constexpr int NCH = R / 64 + 1;
-    static constexpr uint32_t BOX = NCH * 1024;           // 8 tokens, all chunks
-    static constexpr uint32_t A_BYTES = (kExpTile / 8) * BOX;
-    static constexpr uint32_t W_STAGE = 256 * 128;        // 256 weight rows x 64 columns
-    static constexpr int NST = R == 512 ? 2 : 4;
+    static constexpr int KCH = R / 64;
+    static constexpr uint32_t GROUP = KCH * 1024;         // 8 tokens, all latent chunks
+    static constexpr uint32_t A_BYTES = (kExpTile / 8) * GROUP;
+    static constexpr uint32_t W_HALF = 128 * 128;         // 128 weight rows x 64 columns
+    static constexpr uint32_t W_STAGE = 2 * W_HALF;       // keys' rows, values' rows
+    static constexpr int NST = R == 512 ? 3 : 4;
     static constexpr uint32_t OFF_W = A_BYTES;
-    static constexpr uint32_t OFF_EPI = OFF_W + NST * W_STAGE;
-    static constexpr uint32_t OFF_MISC = OFF_EPI + 4 * 4096;
+    static constexpr uint32_t OFF_MISC = OFF_W + NST * W_STAGE;
     static constexpr uint32_t BYTES = OFF_MISC + 1024 + 1024;
     static_assert(BYTES <= 232448, "fits one CTA");
 };
@@ -64,14 +68,35 @@ __device__ __forceinline__ uint32_t pack_16(bool f16, uint32_t lo, uint32_t hi) 
                : pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
 }
 
+// The rotary parts of a warp's 32 rows of a tile, 8 lanes a row: cache rows tok0 + r of sequence s
+// (zeros past the context and for bad block ids) to padded rows row0 + r.
+template <int R>
+__device__ __forceinline__ void copy_rope(const ExpandArgs &a, int s, int64_t tok0, int64_t row0, int quarter,
+                                          int valid) {
+    const int lane = threadIdx.x & 31, er = lane >> 3, ec = lane & 7;
+    const int32_t *table = a.block_tables + (int64_t)s * a.max_blocks_per_seq;
+    uint4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int r = quarter * 32 + 4 * k + er;
+        const int64_t t = tok0 + r;
+        const int id = r < valid ? table[t >> a.block_shift] : -1;
+        x[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (id >= 0 && id < a.num_blocks) {
+            const int64_t slot = ((int64_t)id << a.block_shift) + (t & ((1 << a.block_shift) - 1));
+            x[k] = __ldg(reinterpret_cast<const uint4 *>(a.cache + slot * (R + kExpRope) + R) + ec);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        reinterpret_cast<uint4 *>(a.buf.rope + (row0 + quarter * 32 + 4 * k + er) * kExpRope)[ec] = x[k];
+}
+
 }  // namespace
 
-// Units of a sequence: 128-token tiles x heads.
+// Units of a sequence: 128-token tiles.
 struct ExpandUnits {
-    int num_heads;
-    __device__ __forceinline__ int64_t operator()(const SeqInfo &q) const {
-        return (int64_t)((q.ctx + kExpTile - 1) / kExpTile) * num_heads;
-    }
+    __device__ __forceinline__ int64_t operator()(const SeqInfo &q) const { return (q.ctx + kExpTile - 1) / kExpTile; }
 };
 
 template <int R>
@@ -79,22 +104,23 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap wk_map,
                      const __grid_constant__ CUtensorMap wv_map, const ExpandArgs a) {
     using L = ExpandSmem<R>;
-    constexpr int NST = L::NST, KCH = R / 64;
+    constexpr int NST = L::NST, KCH = L::KCH;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sA = smem, *sW = smem + L::OFF_W, *sEpi = smem + L::OFF_EPI;
+    uint8_t *sA = smem, *sW = smem + L::OFF_W;
     ExpandMisc &ms = *reinterpret_cast<ExpandMisc *>(smem + L::OFF_MISC);
     volatile int *abort_flag = &ms.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x, H = a.num_heads;
+    const int H = a.num_heads;
+    const int rank = (int)cluster_rank(), c = blockIdx.x >> 1, nc = a.grid >> 1;  // cluster, clusters
 
     if (threadIdx.x == 0) {
         mbar_init(&ms.a_full, 1);
-        mbar_init(&ms.a_empty, 5);  // the tile's last product and the four epilogue warps
+        mbar_init(&ms.a_empty, 1);
         mbar_init(&ms.mma_done, 1);
         for (int i = 0; i < NST; ++i) {
             mbar_init(&ms.w_full[i], 1);
-            mbar_init(&ms.w_empty[i], 1);
+            mbar_init(&ms.w_empty[i], 2);  // both CTAs' products have read the stage
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms.acc_full[i], 1);
@@ -108,53 +134,59 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
         tma_prefetch_desc(&wk_map);
         tma_prefetch_desc(&wv_map);
     }
+    if (warp == 1) tmem_alloc(&ms.tmem_slot, 512);
     pdl_wait();
     pdl_trigger();
     const SeqBatch sb{a.query_start_loc, a.context_lens, a.num_seqs, a.total_q,
                       (int64_t)a.max_blocks_per_seq << a.block_shift, a.err};
-    const ExpandUnits units{H};
-    const BatchScan sc = scan_batch(sb, units, ms.scan, c == 0);
+    const ExpandUnits units{};
+    const BatchScan sc = scan_batch(sb, units, ms.scan, blockIdx.x == 0);
     // A batch with more tokens than the caller counted is refused whole; the attention kernel
     // sees the same sum and writes zero rows.
-    const int64_t T = sc.total <= a.buf.padded / kExpTile * H ? sc.total : 0;
-    if (c == 0) {
-        if (T != sc.total && threadIdx.x == 0) flag_error(a.err, PKV_DEVERR_CONTEXT_LEN);
+    const int64_t NT = sc.total <= a.buf.padded / kExpTile ? sc.total : 0;
+    if (blockIdx.x == 0) {
+        if (NT != sc.total && threadIdx.x == 0) flag_error(a.err, PKV_DEVERR_CONTEXT_LEN);
         int64_t run = sc.run;
         for (int s = sc.beg; s < sc.end; ++s) {
-            a.buf.tile_off[s] = (int32_t)(run / H);
+            a.buf.tile_off[s] = (int32_t)run;
             run += seq_units_of(sb, units, s, false);
         }
     }
-    const int ge = split_ctas(T, a.grid, 1);
-    if (T == 0 || c >= ge) return;
-    const int64_t lo = share_begin(c, T, ge), hi = share_begin(c + 1, T, ge);
-    find_unit(sb, units, sc, lo, &ms.start);
-    if (warp == 1) tmem_alloc(&ms.tmem_slot, 512);
+    const int64_t T = (NT + 1) / 2 * H;  // (pair, head) units
+    const int ge = split_ctas(T, nc, 1);
+    const bool works = T > 0 && c < ge;
+    const int64_t lo = works ? quotient(c * T, ge) : 0, hi = works ? quotient((c + 1) * T, ge) : 0;
+    const int64_t g0 = 2 * quotient(lo, H) + rank;  // this CTA's first token tile
+    if (works) find_unit(sb, units, sc, g0, &ms.start);
     tc_fence_before();
-    __syncthreads();
+    cluster_barrier();  // the barriers of both CTAs are there before either is signalled
     tc_fence_after();
     const uint32_t tmem = ms.tmem_slot;
-    SeqWalk<ExpandUnits> w;
-    w.start(ms.start);
     auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
     };
     bool ok = true;
+    SeqWalk<ExpandUnits> w;
+    if (g0 < NT) w.start(ms.start);
 
-    if (warp == 0) {
+    if (!works) {
+        // nothing to do but to meet the other CTA at the end
+    } else if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
         const uint64_t policy = l2_policy_evict_normal();
+        const CUtensorMap *w_map = rank == 0 ? &wk_map : &wv_map;
         uint32_t st = 0, ph = 0, fill = 0, aloads = 0;
+        int64_t p = quotient(lo, H);
+        int h = (int)(lo - p * H);
         for (int64_t f = lo; f < hi && ok; ++f) {
-            w.seek(sb, units, f);
-            const int64_t o = f - w.pre;
-            const int tile = (int)(o / H), h = (int)(o - (int64_t)tile * H);
-            if (f == lo || h == 0) {
+            const int64_t g = 2 * p + rank;
+            if ((f == lo || h == 0) && g < NT) {
+                w.seek(sb, units, g);
                 // the tile's blocks, one a lane (at most 16)
-                const int64_t b0 = (int64_t)tile * kExpTile >> a.block_shift;
+                const int64_t b0 = (g - w.pre) * kExpTile >> a.block_shift;
                 const int64_t seq_blocks = ((int64_t)w.q.ctx + (1 << a.block_shift) - 1) >> a.block_shift;
                 const int boxes = (int)min64(kExpTile >> a.block_shift, seq_blocks - b0);
-                const int box_bytes = L::BOX << (a.block_shift - 3);
+                const int box_bytes = L::GROUP << (a.block_shift - 3);
                 int bid = -1;
                 if (lane < boxes) {
                     bid = a.block_tables[(int64_t)w.s * a.max_blocks_per_seq + b0 + lane];
@@ -178,15 +210,16 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
                 for (int kc = 0; kc < KCH; ++kc) {
                     ok = mbar_wait(&ms.w_empty[st], ph ^ 1, abort_flag, a.wait_ns);
                     if (!ok) break;
+                    // both halves land here: this CTA's own and the other one's
                     mbar_arrive_expect_tx(&ms.w_full[st], L::W_STAGE);
-                    uint8_t *dst = sW + st * L::W_STAGE;
-                    tma_load_2d(dst, &wk_map, &ms.w_full[st], kc * 64, h * kExpHeadDim, policy);
-                    tma_load_2d(dst + L::W_STAGE / 2, &wv_map, &ms.w_full[st], kc * 64, h * kExpHeadDim, policy);
+                    tma_load_2d_multicast(sW + st * L::W_STAGE + rank * L::W_HALF, w_map, &ms.w_full[st], kc * 64,
+                                          h * kExpHeadDim, 3, policy);
                     ++fill;
                     if (++st == NST) { st = 0; ph ^= 1; }
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (++h == H) { h = 0; ++p; }
         }
         if (!ok && lane == 0) {
             flag_error(a.err, PKV_DEVERR_TIMEOUT);
@@ -197,16 +230,17 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
+        // A CTA without a tile of its own (the last pair of an odd count) multiplies whatever its
+        // shared memory holds, so that the stages go on in step; nothing of it is stored.
         constexpr uint32_t IDESC = umma_idesc_bf16(kExpTile, 256, 0, 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint64_t da = umma_desc_sw128(smem_u32(sA), 16, L::BOX);
+        const uint64_t da = umma_desc_sw128(smem_u32(sA), 16, L::GROUP);
         const uint64_t dw0 = umma_desc_sw128(smem_u32(sW), 16, 1024);
         uint32_t st = 0, ph = 0, n = 0, atiles = 0;
+        int64_t p = quotient(lo, H);
+        int h = (int)(lo - p * H);
         for (int64_t f = lo; f < hi && ok; ++f, ++n) {
-            w.seek(sb, units, f);
-            const int64_t o = f - w.pre;
-            const int h = __shfl_sync(0xffffffffu, (int)(o % H), 0);
-            if (f == lo || h == 0) {
+            if ((f == lo || h == 0) && 2 * p + rank < NT) {
                 if (!wait_all(&ms.a_full, atiles & 1)) { ok = false; break; }
                 ++atiles;
             }
@@ -219,12 +253,16 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
                 for (int ks = 0; ks < 4; ++ks)
                     umma_bf16_warp(tm + (n & 1) * 256, da + ((kc * 1024 + ks * 32) >> 4), dw + ((ks * 32) >> 4), IDESC,
                                    kc > 0 || ks > 0);
-                umma_commit_warp(&ms.w_empty[st]);
+                umma_commit_multicast_warp(&ms.w_empty[st], 3);
                 if (++st == NST) { st = 0; ph ^= 1; }
             }
             if (!ok) break;
             umma_commit_warp(&ms.acc_full[n & 1]);
-            if (h == H - 1) umma_commit_warp(&ms.a_empty);
+            if (++h == H) {
+                umma_commit_warp(&ms.a_empty);
+                h = 0;
+                ++p;
+            }
         }
         if (!ok) {
             if (lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
@@ -234,94 +272,63 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
         mbar_wait(&ms.mma_done, 0, nullptr);
         __syncwarp();
     } else {
-        // ------------- epilogue: one token a thread, stored as whole 128-byte lines -------------
+        // ------------- epilogue: one token a thread, 32 bytes a store -------------
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
-        uint8_t *ebuf = sEpi + quarter * 4096;
-        const int er = lane >> 3, ec = lane & 7;
-        uint32_t n = 0, atiles = 0;
+        uint32_t n = 0;
+        int64_t p = quotient(lo, H);
+        int h = (int)(lo - p * H);
         for (int64_t f = lo; f < hi && ok; ++f, ++n) {
-            w.seek(sb, units, f);
-            const int64_t o = f - w.pre;
-            const int tile = (int)(o / H), h = (int)(o - (int64_t)tile * H);
-            const int64_t row0 = (w.pre / H + tile) * kExpTile;  // the tile's first padded token
-            const int valid = (int)min64(kExpTile, w.q.ctx - (int64_t)tile * kExpTile);
-            if (f == lo || h == 0) {
-                if (!wait_all(&ms.a_full, atiles & 1)) { ok = false; break; }
-                ++atiles;
-                if (h == 0) {
-                    // the rotary chunk of the tile's rows, 8 lanes a row
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int r = quarter * 32 + 4 * k + er;
-                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                        if (r < valid)
-                            x = *reinterpret_cast<const uint4 *>(sA + (r >> 3) * L::BOX + (L::NCH - 1) * 1024 +
-                                                                 (r & 7) * 128 + ((ec ^ (r & 7)) << 4));
-                        *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(a.buf.rope + (row0 + r) * kExpRope) +
-                                                   ec * 16) = x;
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.a_empty);
+            const int64_t g = 2 * p + rank, row0 = g * kExpTile;  // the tile's first padded token
+            int valid = 0;
+            if (g < NT) {
+                w.seek(sb, units, g);
+                valid = (int)min64(kExpTile, w.q.ctx - (g - w.pre) * kExpTile);
+                if (h == 0) copy_rope<R>(a, w.s, (g - w.pre) * kExpTile, row0, quarter, valid);
             }
             if (!wait_all(&ms.acc_full[n & 1], (n >> 1) & 1)) { ok = false; break; }
             tc_fence_after();
-            uint8_t *dst = reinterpret_cast<uint8_t *>(a.buf.kv + ((int64_t)h * a.buf.padded + row0) * 256);
+            if (g < NT) {
+                uint16_t *dst = a.buf.kv + ((int64_t)h * a.buf.padded + row0 + row) * 256;
 #pragma unroll 1
-            for (int g = 0; g < 4; ++g) {
-                uint32_t r0[32], r1[32];
-                const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + (n & 1) * 256 + g * 64;
-                tmem_ld32(t, r0);
-                tmem_ld32(t + 32, r1);
-                tmem_wait_ld();
-                reg_order32(r0);
-                reg_order32(r1);
-                if (row >= valid) {  // past the context the product saw whatever the slots held
+                for (int q = 0; q < 8; ++q) {  // 32 columns: four of keys, four of values
+                    uint32_t r[32];
+                    tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (n & 1) * 256 + q * 32, r);
+                    tmem_wait_ld();
+                    reg_order32(r);
+                    if (row >= valid) {  // past the context the product saw whatever the slots held
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) r0[j] = r1[j] = 0u;
-                }
-                const bool is_v = g >= 2;
-                if (is_v) {
-                    // clamping changes a value only past the range: compare before and after
-                    bool over = false;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        over |= clamp_f16(r0[j]);
-                        over |= clamp_f16(r1[j]);
+                        for (int j = 0; j < 32; ++j) r[j] = 0u;
                     }
-                    if (over) flag_error(a.err, PKV_DEVERR_VALUE);
-                }
+                    const bool is_v = q >= 4;
+                    if (is_v) {
+                        bool over = false;
 #pragma unroll
-                for (int cc = 0; cc < 8; ++cc) {
-                    const uint32_t *s = cc < 4 ? r0 + 8 * cc : r1 + 8 * (cc - 4);
-                    uint4 x;
-                    x.x = pack_16(is_v, s[0], s[1]);
-                    x.y = pack_16(is_v, s[2], s[3]);
-                    x.z = pack_16(is_v, s[4], s[5]);
-                    x.w = pack_16(is_v, s[6], s[7]);
-                    *reinterpret_cast<uint4 *>(ebuf + lane * 128 + ((cc ^ (lane & 7)) << 4)) = x;
-                }
-                __syncwarp();
+                        for (int j = 0; j < 32; ++j) over |= clamp_f16(r[j]);
+                        if (over) flag_error(a.err, PKV_DEVERR_VALUE);
+                    }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int rr = 4 * k + er;
-                    const uint4 x = *reinterpret_cast<const uint4 *>(ebuf + rr * 128 + ((ec ^ (rr & 7)) << 4));
-                    *reinterpret_cast<uint4 *>(dst + (int64_t)(quarter * 32 + rr) * 512 + g * 128 + ec * 16) = x;
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t x[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = pack_16(is_v, r[16 * k + 2 * j], r[16 * k + 2 * j + 1]);
+                        st_global_32(dst + q * 32 + k * 16, x);
+                    }
                 }
-                __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.acc_free[n & 1]);
+            if (++h == H) { h = 0; ++p; }
         }
         if (!ok) {
             if (lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
             *abort_flag = 1;
         }
     }
+    __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    cluster_barrier();  // the other CTA signals and fills this one's shared memory up to here
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
@@ -332,8 +339,8 @@ static cudaError_t launch_expand(const CUtensorMap &kv_map, const CUtensorMap &w
     static SmemAllowance allowed;
     const cudaError_t e = allow_dynamic_smem(latent_expand_kernel<R>, ExpandSmem<R>::BYTES, allowed);
     if (e != cudaSuccess) return e;
-    return launch_pdl(latent_expand_kernel<R>, dim3(a.grid), dim3(kExpandThreads), ExpandSmem<R>::BYTES, stream,
-                      kv_map, wk_map, wv_map, a);
+    return launch_pdl_cluster(latent_expand_kernel<R>, dim3(a.grid), dim3(kExpandThreads), 2, ExpandSmem<R>::BYTES,
+                              stream, kv_map, wk_map, wv_map, a);
 }
 
 cudaError_t launch_latent_expand(int latent_dim, const CUtensorMap &kv_map, const CUtensorMap &wk_map,

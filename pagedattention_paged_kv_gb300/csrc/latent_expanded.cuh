@@ -27,7 +27,9 @@ struct ExpandArgs {
     const int32_t *query_start_loc;
     const int32_t *block_tables;
     const int32_t *context_lens;
-    int num_seqs, total_q, max_blocks_per_seq, block_shift, num_heads, grid;
+    const __nv_bfloat16 *cache;
+    int num_seqs, total_q, max_blocks_per_seq, block_shift, num_heads;
+    int grid;  // even: clusters of two CTAs
     int64_t num_blocks;
     ExpandedBuffers buf;
     int *err;
@@ -58,7 +60,7 @@ struct ExpandedPlan {
 
 void plan_expanded(int num_seqs, int64_t total_context, int num_heads, int sms, ExpandedPlan *p);
 
-// kv_map: the latent cache in boxes of a block x all chunks; wk_map, wv_map: the weights as rows
+// kv_map: the latent cache in boxes of a block x the latent chunks; wk_map, wv_map: the weights as rows
 // [num_heads * 128][latent_dim] in boxes of 128 rows x 64 columns.
 cudaError_t launch_latent_expand(int latent_dim, const CUtensorMap &kv_map, const CUtensorMap &wk_map,
                                  const CUtensorMap &wv_map, const ExpandArgs &a, cudaStream_t stream);

@@ -78,6 +78,16 @@ __device__ __forceinline__ void umma_commit_warp(uint64_t *bar) {
         : "memory");
 }
 
+// umma_commit_warp that arrives on the barrier at `bar`'s place in every CTA of cta_mask.
+__device__ __forceinline__ void umma_commit_multicast_warp(uint64_t *bar, uint16_t cta_mask) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+        ::"r"(smem_u32(bar)), "h"(cta_mask)
+        : "memory");
+}
+
 // Whole-warp TMEM allocation of `cols` columns; the base address lands in *slot.
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t cols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
