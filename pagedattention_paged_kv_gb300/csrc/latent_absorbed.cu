@@ -14,7 +14,7 @@
 //
 // Layout
 //  * A work item is 64 query rows (row = token * heads + head) of one sequence; its units
-//    are tiles of 64 cached tokens.  A persistent grid takes equal contiguous shares of the
+//    are tiles of 32 cached tokens.  A persistent grid takes equal contiguous shares of the
 //    flat unit list (pkv_split.cuh); items cut by a share boundary leave
 //    parts that latent_merge_kernel joins.
 //  * A tile arrives as one TMA box a block and part (blocks of 8 to 64 tokens, several 64-column
@@ -22,7 +22,7 @@
 //    every 8 tokens of a part are [chunk][8 tokens][128 bytes], 128-byte swizzled, whatever the block
 //    size: the 8-row groups of a tile are a constant distance apart, which is what both operand
 //    descriptors need.
-//  * S = Q K^T runs with the rows on M = 64 and the tile's tokens on N = 64, so a row's scores stay
+//  * S = Q K^T runs with the rows on M = 64 and the tile's tokens on N = 32, so a row's scores stay
 //    in the four threads of a quad.  O^T += C^T P^T runs with the latent columns on M = 128 (R / 128 blocks),
 //    the rows on N and the tokens on K: the tile is read transposed in place (A MN-major) and P
 //    is the K-major B operand.  O^T of 64 rows then takes R / 2 TMEM columns; with the rows
@@ -41,46 +41,49 @@ namespace pkv {
 
 namespace {
 
-constexpr int kMinTilesPerCta = 2;
+constexpr int kMinTilesPerCta = 4;
 
 // A row's reference maximum moves, and O^T is rescaled, only when a tile's maximum exceeds it by
 // this much (log2 units).  bf16 weights and fp32 sums keep their relative precision up to 2^24
 // and far from overflow, and a move is rare enough to be handled off the critical path.
 constexpr float kAbsorbedSlack = 24.0f;
 
+constexpr int kMaxStages = 8;
+
 template <int R>
 struct AbsorbedSmem {
     static constexpr int NCH = R / 64 + 1;                    // 64-column chunks of a row, rotary last
     // A tile's boxes come in PARTS groups of chunks with a barrier each, so that the scores over
     // the first chunks are under way while the last ones are still arriving.
-    static constexpr int PARTS = NCH % 3 == 0 ? 3 : 1;
+    static constexpr int PARTS = 1;
     static constexpr int PCH = NCH / PARTS;                   // chunks of a part
     static constexpr uint32_t GROUP = PCH * 1024;             // 8 tokens, a part's chunks
-    static constexpr uint32_t PART = 8 * GROUP;               // a part of a tile
+    static constexpr uint32_t PART = kLatentTile / 8 * GROUP; // a part of a tile
     static constexpr uint32_t STAGE = PARTS * PART;           // one tile
     static constexpr uint32_t chunk_at(int j) { return (j / PCH) * PART + (j % PCH) * 1024; }
     static constexpr uint32_t Q_CH = kLatentRows * 128;       // 64 rows x 64 columns
     static constexpr uint32_t OFF_Q = 0;
-    static constexpr uint32_t OFF_P = NCH * Q_CH;             // P: 64 rows x 64 tokens, bf16
+    static constexpr uint32_t OFF_P = NCH * Q_CH;             // P: 64 rows x two tiles' 32 tokens, bf16
     static constexpr uint32_t OFF_STAGES = OFF_P + kLatentRows * 128;
     static constexpr uint32_t MISC = 2048;
     static constexpr uint32_t LIMIT = 232448 - 1024 - MISC;
-    static constexpr int NST = (LIMIT - OFF_STAGES) / STAGE > 4 ? 4 : (LIMIT - OFF_STAGES) / STAGE;
+    static constexpr int NST = (LIMIT - OFF_STAGES) / STAGE > kMaxStages ? kMaxStages : (LIMIT - OFF_STAGES) / STAGE;
     static constexpr uint32_t OFF_MISC = OFF_STAGES + NST * STAGE;
     static constexpr uint32_t BYTES = OFF_MISC + MISC + 1024;
-    static constexpr uint32_t COL_O = 128;                    // S: columns 0..63 and 64..127
-    static_assert(NST >= 2, "two tiles in flight at least");
+    static constexpr uint32_t COL_O = 128;                    // S: columns 0..31 and 32..63
+    static_assert(NST >= 4, "four tiles in flight at least");
 };
 
 struct AbsorbedMisc {
-    uint64_t q_full, q_empty, pv_done, p_full, o_free, qk_over, pv_over, group, rescaled;
+    uint64_t q_full, q_empty, o_free, qk_over, pv_over, group, rescaled;
+    uint64_t p_full[2], pv_done[2];
     uint64_t s_full[2], s_free[2];
-    uint64_t kv_full[4][3], kv_empty[4][3];
+    uint64_t kv_full[kMaxStages][3], kv_empty[kMaxStages][3];
     uint32_t tmem_slot;
     int abort_flag;
     int64_t scan[8];
     WalkStart start;
-    int moved[2][4];  // by tile parity and softmax warp: a row's reference maximum moved
+    int moved[4][4];  // by tile % 4 and softmax warp: a row's reference maximum moved
     float alpha[2][kLatentRows];
     float inv[kLatentRows];
 };
@@ -145,8 +148,6 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     if (threadIdx.x == 0) {
         mbar_init(&ms.q_full, 1);
         mbar_init(&ms.q_empty, 1);
-        mbar_init(&ms.pv_done, 1);
-        mbar_init(&ms.p_full, 4);  // one arrival per softmax warp
         mbar_init(&ms.o_free, 4);
         mbar_init(&ms.qk_over, 1);
         mbar_init(&ms.pv_over, 1);
@@ -154,7 +155,9 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         mbar_init(&ms.rescaled, 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms.s_full[i], 1);
-            mbar_init(&ms.s_free[i], 4);
+            mbar_init(&ms.s_free[i], 4);  // one arrival per softmax warp
+            mbar_init(&ms.p_full[i], 4);
+            mbar_init(&ms.pv_done[i], 1);
         }
         for (int i = 0; i < NST; ++i) {
             for (int p = 0; p < L::PARTS; ++p) {
@@ -229,21 +232,22 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         const uint64_t policy = l2_policy_evict_normal();
         uint32_t st = 0, ph = 0, fill = 0;  // ring slot and phase of the next tile; parts issued
         uint32_t qloads = 0;
-        const int per_tile = kLatentTile >> a.block_shift;             // blocks of a tile
-        const int box_bytes = L::GROUP << (a.block_shift - 3);          // a block's share of a part
+        const int bshift = min(a.block_shift, 5);                      // log2 of a box's tokens
+        const int per_tile = kLatentTile >> bshift;                     // boxes of a tile
+        const int box_bytes = L::GROUP << (bshift - 3);                 // a box's share of a part
         bool ok = true;
         for (int64_t f = lo; f < hi && ok;) {
             w.seek(sb, units, f);
             const AbsorbedSegment g = segment_at(a, w.q, w.pre, f, hi);
-            // A window of 32 blocks, one a lane (32 / per_tile tiles); the ids of the next window are
-            // loaded while the current one is issued.
+            // A window of 32 boxes (blocks, or 32 tokens of a larger one), one a lane; the block ids of
+            // the next window are loaded while the current one is issued.
             const int32_t *table = a.block_tables + (int64_t)w.s * a.max_blocks_per_seq;
-            const int64_t block0 = (int64_t)g.kb * per_tile;
-            const int64_t seq_blocks = ((int64_t)w.q.ctx + (1 << a.block_shift) - 1) >> a.block_shift;
-            const int nblocks = (int)(min64(seq_blocks, block0 + (int64_t)g.tiles * per_tile) - block0);
+            const int64_t tok0 = (int64_t)g.kb * kLatentTile;
+            const int64_t tok1 = min64(w.q.ctx, tok0 + (int64_t)g.tiles * kLatentTile);
+            const int nboxes = (int)((tok1 - tok0 + (1 << bshift) - 1) >> bshift);
             auto block_of = [&](int i) -> int {
-                if (i + lane >= nblocks) return -1;
-                const int id = table[block0 + i + lane];
+                if (i + lane >= nboxes) return -1;
+                const int id = table[(tok0 + ((int64_t)(i + lane) << bshift)) >> a.block_shift];
                 if (id >= 0 && id < a.num_blocks) return id;
                 flag_error(a.err, PKV_DEVERR_BLOCK_ID);
                 return -1;  // an out-of-range box is filled with zeros
@@ -264,13 +268,13 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                     bid = bid_next;
                     bid_next = block_of(i0 + 32);
                 }
-                const int boxes = min(per_tile, nblocks - i0);
+                const int boxes = min(per_tile, nboxes - i0);
                 // One lane issues: the copies of several lanes would go out one after the other at
                 // ~90 cycles each, against ~30 for one lane's.
 #pragma unroll
                 for (int p = 0; p < L::PARTS; ++p) {
                     if (lane == 0) {
-                        ok = mbar_poll(&ms.kv_empty[st][p], ph ^ 1, abort_flag, a.wait_ns);
+                        ok = mbar_wait(&ms.kv_empty[st][p], ph ^ 1, abort_flag, a.wait_ns);
                         if (ok) mbar_arrive_expect_tx(&ms.kv_full[st][p], boxes * box_bytes);
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -279,8 +283,9 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
 #pragma unroll 1
                     for (int i = 0; i < boxes; ++i) {
                         const int id = __shfl_sync(0xffffffffu, bid, (i0 + i) & 31);
+                        const int grp = (int)((tok0 + ((int64_t)(i0 + i) << bshift)) & ((1 << a.block_shift) - 1)) >> 3;
                         if (lane == 0)
-                            tma_load_5d(dst + i * box_bytes, &kv_map, &ms.kv_full[st][p], 0, 0, p * L::PCH, 0, id,
+                            tma_load_5d(dst + i * box_bytes, &kv_map, &ms.kv_full[st][p], 0, 0, p * L::PCH, grp, id,
                                         policy);
                     }
                     ++fill;
@@ -307,7 +312,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         // (tcgen05.cuh).  QK and PV have a warp each: a tile that is late holds up no finished
         // one, and the tensor pipe takes from both.
         auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, mbar_poll(bar, parity, abort_flag, a.wait_ns));
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
         };
         constexpr uint32_t IDESC_QK = umma_idesc_bf16(kLatentRows, kLatentTile, 0, 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -355,7 +360,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     } else if (warp == 6) {
         // ------------------------------ PV issuer ------------------------------
         auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, mbar_poll(bar, parity, abort_flag, a.wait_ns));
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
         };
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         // per M block: its two chunks may lie in different parts
@@ -375,8 +380,8 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             const uint32_t idesc_pv = umma_idesc_bf16(128, n, 1, 0);
             if (seg_i > 0) ok = wait_all(&ms.o_free, (seg_i - 1) & 1);
             for (int t = 0; t < tiles && ok; ++t) {
-                if (!wait_all(&ms.p_full, gv & 1)) { ok = false; break; }
-                const volatile int *mv = ms.moved[gv & 1];
+                if (!wait_all(&ms.p_full[gv & 1], (gv >> 1) & 1)) { ok = false; break; }
+                const volatile int *mv = ms.moved[gv & 3];
                 if (__any_sync(0xffffffffu, mv[0] | mv[1] | mv[2] | mv[3])) {
                     if (!wait_all(&ms.rescaled, moves & 1)) { ok = false; break; }
                     ++moves;
@@ -387,14 +392,15 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
 #pragma unroll
                     for (int ks = 0; ks < kLatentTile / 16; ++ks)
                         umma_bf16_warp(tm + L::COL_O + mb * kLatentRows,
-                                       dv0[mb] + ((st * L::STAGE + ks * 2 * L::GROUP) >> 4), dp + ((ks * 32) >> 4),
+                                       dv0[mb] + ((st * L::STAGE + ks * 2 * L::GROUP) >> 4),
+                                       dp + (((gv & 1) * 64 + ks * 32) >> 4),
                                        idesc_pv, t > 0 || ks > 0);
                     // a part is free behind the block that reads its last value chunk
 #pragma unroll
                     for (int p = 0; p < L::PARTS; ++p)
                         if (mb == min((p + 1) * L::PCH - 1, 2 * MB - 1) / 2) umma_commit_warp(&ms.kv_empty[st][p]);
                 }
-                umma_commit_warp(&ms.pv_done);
+                umma_commit_warp(&ms.pv_done[gv & 1]);
                 ++gv;
                 if (++st == NST) st = 0;
             }
@@ -428,7 +434,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         bool ok = true;
         // Waits that the warp leaves together, so that its warp-wide TMEM accesses stay converged.
         auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, mbar_poll(bar, parity, abort_flag, a.wait_ns));
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
         };
         // Meeting of the four warps (a barrier with a limit, unlike bar.sync).
         auto meet = [&]() -> bool {
@@ -439,10 +445,10 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         // O^T, after tile `tile`'s predecessors and before its own PV: every column (= row of the
         // item) times the factor by which its reference maximum moved in that tile.
         auto rescale_if_moved = [&](uint32_t tile, int ncols) -> bool {
-            if (!wait_all(&ms.p_full, tile & 1)) return false;  // every warp's say about the tile
-            const volatile int *mv = ms.moved[tile & 1];
+            if (!wait_all(&ms.p_full[tile & 1], (tile >> 1) & 1)) return false;  // every warp's say about it
+            const volatile int *mv = ms.moved[tile & 3];
             if (!__any_sync(0xffffffffu, mv[0] | mv[1] | mv[2] | mv[3])) return true;
-            if (tile > 0 && !wait_all(&ms.pv_done, (tile - 1) & 1)) return false;
+            if (tile > 0 && !wait_all(&ms.pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1)) return false;
             tc_fence_after();
 #pragma unroll 1
             for (int mb = 0; mb < MB; ++mb)
@@ -481,17 +487,17 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 if (t > 0 && !rescale_if_moved(gt - 1, ncols)) { ok = false; break; }  // its PV may wait for it
                 if (!wait_all(&ms.s_full[gt & 1], (gt >> 1) & 1)) { ok = false; break; }
                 tc_fence_after();
-                uint32_t v[32];
-                tmem_ld_16x64(tl + (gt & 1) * kLatentTile, v);
+                uint32_t v[16];
+                tmem_ld_16x32(tl + (gt & 1) * kLatentTile, v);
                 tmem_wait_ld();
-                reg_order32(v);
+                reg_order16(v);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.s_free[gt & 1]);
                 const int vis0 = (int)min64(lim[0] - key0, kLatentTile), vis1 = (int)min64(lim[1] - key0, kLatentTile);
                 if (!__all_sync(0xffffffffu, vis0 >= kLatentTile && vis1 >= kLatentTile)) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < 16; ++j)
                         if (8 * (j >> 2) + c0 + (j & 1) >= ((j & 2) ? vis1 : vis0)) v[j] = __float_as_uint(-INFINITY);
                 }
                 bool up[2];
@@ -499,7 +505,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 for (int k = 0; k < 2; ++k) {
                     float mx = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
+                    for (int i = 0; i < 4; ++i)
                         mx = fmax3(mx, __uint_as_float(v[4 * i + 2 * k]), __uint_as_float(v[4 * i + 2 * k + 1]));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * sl2;  // scale > 0 keeps the order
@@ -512,16 +518,16 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                     if ((lane & 3) == 0) ms.alpha[gt & 1][ra + 8 * k] = alpha;
                 }
                 const bool moved = __any_sync(0xffffffffu, (up[0] || up[1]) && t > 0);
-                if (lane == 0) ms.moved[gt & 1][quarter] = moved;
+                if (lane == 0) ms.moved[gt & 3][quarter] = moved;
                 // The weights, while the tensor pipe finishes the last tile's PV.  The sum adds them as
                 // rounded, so a row that one key dominates loses nothing to their rounding.
-                uint32_t pk[16];
+                uint32_t pk[8];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const float base = m_ref[k] == -INFINITY ? 0.f : m_ref[k];
                     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         const float e0 = fast_exp2(fmaf(__uint_as_float(v[4 * i + 2 * k]), sl2, -base));
                         const float e1 = fast_exp2(fmaf(__uint_as_float(v[4 * i + 2 * k + 1]), sl2, -base));
                         pk[2 * i + k] = pack_bf16x2(e0, e1);
@@ -530,11 +536,11 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                     }
                     l[k] += s0 + s1;
                 }
-                // P has one place: the last tile's PV comes first
-                if (gt > 0 && !wait_all(&ms.pv_done, (gt - 1) & 1)) { ok = false; break; }
+                // P has two places: PV of two tiles before comes first
+                if (gt >= 2 && !wait_all(&ms.pv_done[gt & 1], ((gt >> 1) - 1) & 1)) { ok = false; break; }
 #pragma unroll
-                for (int i = 0; i < 8; i += 2)  // 16-byte chunks i and i + 1 of the quarter's 16 rows
-                    stmatrix_x4(p_row + (((i + (lane >> 4)) ^ (pr & 7)) << 4), pk[2 * i], pk[2 * i + 1], pk[2 * i + 2],
+                for (int i = 0; i < 4; i += 2)  // 16-byte chunks i and i + 1 of the tile's half of P's rows
+                    stmatrix_x4(p_row + (((4 * (gt & 1) + i + (lane >> 4)) ^ (pr & 7)) << 4), pk[2 * i], pk[2 * i + 1], pk[2 * i + 2],
                                 pk[2 * i + 3]);
                 if (key0 + kLatentTile > ctx) {
                     // Slots past the context may hold NaN, and 0 * NaN would reach O^T: their value
@@ -554,12 +560,12 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.p_full);
+                if (lane == 0) mbar_arrive(&ms.p_full[gt & 1]);
             }
             if (!ok) break;
             if (!rescale_if_moved(gt - 1, ncols)) { ok = false; break; }
             // ---- epilogue: O / l of a whole item, or the part for the merge ----
-            if (!wait_all(&ms.pv_done, (gt - 1) & 1)) { ok = false; break; }
+            if (!wait_all(&ms.pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 2; ++k) {  // the four threads of a row hold its sum in parts

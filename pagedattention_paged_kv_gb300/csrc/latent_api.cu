@@ -41,13 +41,13 @@ int check_latent(int num_seqs, int total_q, int max_blocks_per_seq, int num_head
 }
 
 // The cache as (64 columns, token in group, 64-column chunk, group of 8 tokens, block): a box of
-// one block (at most 64 tokens) x box_chunks chunks lands as [group][chunk][8 tokens][64 columns].
+// one block (at most 32 tokens of it) x box_chunks chunks lands as [group][chunk][8 tokens][64 columns].
 int encode_latent_map(CUtensorMap *map, const void *cache, int64_t num_blocks, int block_size, int row_cols,
                       int box_chunks) {
     const uint64_t row = (uint64_t)row_cols * 2;
     const uint64_t dims[5] = {64, 8, (uint64_t)(row_cols / 64), (uint64_t)(block_size / 8), (uint64_t)num_blocks};
     const uint64_t strides[4] = {row, 128, row * 8, row * block_size};
-    const uint32_t box[5] = {64, 8, (uint32_t)box_chunks, (uint32_t)(block_size / 8), 1};
+    const uint32_t box[5] = {64, 8, (uint32_t)box_chunks, (uint32_t)(block_size < 32 ? block_size / 8 : 4), 1};
     return pkv::encode_tiled(map, 5, cache, dims, strides, box);
 }
 

@@ -182,14 +182,15 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
             const int64_t g = 2 * p + rank;
             if ((f == lo || h == 0) && g < NT) {
                 w.seek(sb, units, g);
-                // the tile's blocks, one a lane (at most 16)
-                const int64_t b0 = (g - w.pre) * kExpTile >> a.block_shift;
-                const int64_t seq_blocks = ((int64_t)w.q.ctx + (1 << a.block_shift) - 1) >> a.block_shift;
-                const int boxes = (int)min64(kExpTile >> a.block_shift, seq_blocks - b0);
-                const int box_bytes = L::GROUP << (a.block_shift - 3);
+                // the tile's boxes (blocks, or 32 tokens of a larger one), one a lane, at most 16
+                const int bshift = min(a.block_shift, 5);
+                const int64_t t0 = (g - w.pre) * kExpTile;
+                const int boxes = (int)((min64(kExpTile, w.q.ctx - t0) + (1 << bshift) - 1) >> bshift);
+                const int box_bytes = L::GROUP << (bshift - 3);
                 int bid = -1;
                 if (lane < boxes) {
-                    bid = a.block_tables[(int64_t)w.s * a.max_blocks_per_seq + b0 + lane];
+                    bid = a.block_tables[(int64_t)w.s * a.max_blocks_per_seq +
+                                         ((t0 + ((int64_t)lane << bshift)) >> a.block_shift)];
                     if (bid < 0 || bid >= a.num_blocks) {
                         flag_error(a.err, PKV_DEVERR_BLOCK_ID);
                         bid = -1;  // an out-of-range box is filled with zeros
@@ -201,7 +202,8 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
 #pragma unroll 1
                 for (int i = 0; i < boxes; ++i) {
                     const int id = __shfl_sync(0xffffffffu, bid, i);
-                    if (lane == 0) tma_load_5d(sA + i * box_bytes, &kv_map, &ms.a_full, 0, 0, 0, 0, id, policy);
+                    const int grp = ((i << bshift) & ((1 << a.block_shift) - 1)) >> 3;  // (a tile starts a block)
+                    if (lane == 0) tma_load_5d(sA + i * box_bytes, &kv_map, &ms.a_full, 0, 0, 0, grp, id, policy);
                 }
                 ++aloads;
             }

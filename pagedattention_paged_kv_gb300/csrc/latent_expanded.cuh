@@ -60,7 +60,7 @@ struct ExpandedPlan {
 
 void plan_expanded(int num_seqs, int64_t total_context, int num_heads, int sms, ExpandedPlan *p);
 
-// kv_map: the latent cache in boxes of a block x the latent chunks; wk_map, wv_map: the weights as rows
+// kv_map: the latent cache in boxes of min(block, 32 tokens) x the latent chunks; wk_map, wv_map: the weights as rows
 // [num_heads * 128][latent_dim] in boxes of 128 rows x 64 columns.
 cudaError_t launch_latent_expand(int latent_dim, const CUtensorMap &kv_map, const CUtensorMap &wk_map,
                                  const CUtensorMap &wv_map, const ExpandArgs &a, cudaStream_t stream);

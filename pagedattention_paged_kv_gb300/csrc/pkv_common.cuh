@@ -96,21 +96,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     }
 }
 
-// The same wait by polling: a failed try_wait may sleep for ~4,000 cycles past the event, a poll
-// costs ~15.  For waits on a kernel's critical path.
-__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                          uint64_t limit_ns) {
-    if (mbar_test(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (mbar_test(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > limit_ns) return false;
-    }
-}
-
 // ---- TMA ---------------------------------------------------------------------
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
