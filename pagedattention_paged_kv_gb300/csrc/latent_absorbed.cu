@@ -14,7 +14,7 @@
 //
 // Layout
 //  * A work item is 64 query rows (row = token * heads + head) of one sequence; its units
-//    are tiles of 32 cached tokens.  A persistent grid takes equal contiguous shares of the
+//    are tiles of 64 cached tokens.  A persistent grid takes equal contiguous shares of the
 //    flat unit list (pkv_split.cuh); items cut by a share boundary leave
 //    parts that latent_merge_kernel joins.
 //  * A tile arrives as one TMA box a block and part (blocks of 8 to 64 tokens, several 64-column
@@ -22,7 +22,7 @@
 //    every 8 tokens of a part are [chunk][8 tokens][128 bytes], 128-byte swizzled, whatever the block
 //    size: the 8-row groups of a tile are a constant distance apart, which is what both operand
 //    descriptors need.
-//  * S = Q K^T runs with the rows on M = 64 and the tile's tokens on N = 32, so a row's scores stay
+//  * S = Q K^T runs with the rows on M = 64 and the tile's tokens on N = 64, so a row's scores stay
 //    in the four threads of a quad.  O^T += C^T P^T runs with the latent columns on M = 128 (R / 128 blocks),
 //    the rows on N and the tokens on K: the tile is read transposed in place (A MN-major) and P
 //    is the K-major B operand.  O^T of 64 rows then takes R / 2 TMEM columns; with the rows
@@ -41,49 +41,44 @@ namespace pkv {
 
 namespace {
 
-constexpr int kMinTilesPerCta = 4;
+constexpr int kMinTilesPerCta = 2;
 
 // A row's reference maximum moves, and O^T is rescaled, only when a tile's maximum exceeds it by
 // this much (log2 units).  bf16 weights and fp32 sums keep their relative precision up to 2^24
 // and far from overflow, and a move is rare enough to be handled off the critical path.
 constexpr float kAbsorbedSlack = 24.0f;
 
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 4;
 
 template <int R>
 struct AbsorbedSmem {
     static constexpr int NCH = R / 64 + 1;                    // 64-column chunks of a row, rotary last
-    // A tile's boxes come in PARTS groups of chunks with a barrier each, so that the scores over
-    // the first chunks are under way while the last ones are still arriving.
-    static constexpr int PARTS = 1;
-    static constexpr int PCH = NCH / PARTS;                   // chunks of a part
-    static constexpr uint32_t GROUP = PCH * 1024;             // 8 tokens, a part's chunks
-    static constexpr uint32_t PART = kLatentTile / 8 * GROUP; // a part of a tile
-    static constexpr uint32_t STAGE = PARTS * PART;           // one tile
-    static constexpr uint32_t chunk_at(int j) { return (j / PCH) * PART + (j % PCH) * 1024; }
+    static constexpr uint32_t GROUP = NCH * 1024;             // 8 tokens, all chunks
+    static constexpr uint32_t HALF = kLatentTile / 16 * GROUP;
+    static constexpr uint32_t STAGE = 2 * HALF;               // one tile
     static constexpr uint32_t Q_CH = kLatentRows * 128;       // 64 rows x 64 columns
     static constexpr uint32_t OFF_Q = 0;
-    static constexpr uint32_t OFF_P = NCH * Q_CH;             // P: 64 rows x two tiles' 32 tokens, bf16
+    static constexpr uint32_t OFF_P = NCH * Q_CH;             // P: 64 rows x 64 tokens, bf16
     static constexpr uint32_t OFF_STAGES = OFF_P + kLatentRows * 128;
     static constexpr uint32_t MISC = 2048;
     static constexpr uint32_t LIMIT = 232448 - 1024 - MISC;
     static constexpr int NST = (LIMIT - OFF_STAGES) / STAGE > kMaxStages ? kMaxStages : (LIMIT - OFF_STAGES) / STAGE;
     static constexpr uint32_t OFF_MISC = OFF_STAGES + NST * STAGE;
     static constexpr uint32_t BYTES = OFF_MISC + MISC + 1024;
-    static constexpr uint32_t COL_O = 128;                    // S: columns 0..31 and 32..63
-    static_assert(NST >= 4, "four tiles in flight at least");
+    static constexpr uint32_t COL_O = 128;                    // S: columns 0..63 and 64..127
+    static_assert(NST >= 2, "two tiles in flight at least");
 };
 
 struct AbsorbedMisc {
     uint64_t q_full, q_empty, o_free, qk_over, pv_over, group, rescaled;
-    uint64_t p_full[2], pv_done[2];
+    uint64_t pv_done, p_full[2];  // p_full: by half of the tile
     uint64_t s_full[2], s_free[2];
-    uint64_t kv_full[kMaxStages][3], kv_empty[kMaxStages][3];
+    uint64_t kv_full[kMaxStages], kv_empty[kMaxStages][2];
     uint32_t tmem_slot;
     int abort_flag;
     int64_t scan[8];
     WalkStart start;
-    int moved[4][4];  // by tile % 4 and softmax warp: a row's reference maximum moved
+    int moved[2][4];  // by tile parity and softmax warp: a row's reference maximum moved
     float alpha[2][kLatentRows];
     float inv[kLatentRows];
 };
@@ -148,6 +143,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     if (threadIdx.x == 0) {
         mbar_init(&ms.q_full, 1);
         mbar_init(&ms.q_empty, 1);
+        mbar_init(&ms.pv_done, 1);
         mbar_init(&ms.o_free, 4);
         mbar_init(&ms.qk_over, 1);
         mbar_init(&ms.pv_over, 1);
@@ -157,13 +153,10 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             mbar_init(&ms.s_full[i], 1);
             mbar_init(&ms.s_free[i], 4);  // one arrival per softmax warp
             mbar_init(&ms.p_full[i], 4);
-            mbar_init(&ms.pv_done[i], 1);
         }
         for (int i = 0; i < NST; ++i) {
-            for (int p = 0; p < L::PARTS; ++p) {
-                mbar_init(&ms.kv_full[i][p], 1);
-                mbar_init(&ms.kv_empty[i][p], 1);
-            }
+            mbar_init(&ms.kv_full[i], 2);  // the tile's halves
+            for (int h = 0; h < 2; ++h) mbar_init(&ms.kv_empty[i][h], 1);
         }
         ms.abort_flag = 0;
         fence_barrier_init();
@@ -230,11 +223,15 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
         const uint64_t policy = l2_policy_evict_normal();
-        uint32_t st = 0, ph = 0, fill = 0;  // ring slot and phase of the next tile; parts issued
+        uint32_t st = 0, ph = 0, fill = 0;  // ring slot and phase of the next tile; halves issued
         uint32_t qloads = 0;
         const int bshift = min(a.block_shift, 5);                      // log2 of a box's tokens
-        const int per_tile = kLatentTile >> bshift;                     // boxes of a tile
-        const int box_bytes = L::GROUP << (bshift - 3);                 // a box's share of a part
+        const int per_half = kLatentTile / 2 >> bshift;                 // boxes of half a tile
+        const int box_bytes = L::GROUP << (bshift - 3);
+        const uint32_t kv0 = smem_u32(sKV);
+        auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
+        };
         bool ok = true;
         for (int64_t f = lo; f < hi && ok;) {
             w.seek(sb, units, f);
@@ -263,34 +260,30 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             ++qloads;
-            for (int t = 0, i0 = 0; t < g.tiles; ++t, i0 += per_tile) {
-                if ((i0 & 31) == 0) {
-                    bid = bid_next;
-                    bid_next = block_of(i0 + 32);
-                }
-                const int boxes = min(per_tile, nboxes - i0);
-                // One lane issues: the copies of several lanes would go out one after the other at
-                // ~90 cycles each, against ~30 for one lane's.
+            int i0 = 0;                                                  // next box
+            int grp = (int)(tok0 & ((1 << a.block_shift) - 1)) >> 3;     // its 8-token group in its block
+            for (int t = 0; t < g.tiles && ok; ++t) {
 #pragma unroll
-                for (int p = 0; p < L::PARTS; ++p) {
-                    if (lane == 0) {
-                        ok = mbar_wait(&ms.kv_empty[st][p], ph ^ 1, abort_flag, a.wait_ns);
-                        if (ok) mbar_arrive_expect_tx(&ms.kv_full[st][p], boxes * box_bytes);
+                for (int h = 0; h < 2; ++h) {
+                    if ((i0 & 31) == 0) {
+                        bid = bid_next;
+                        bid_next = block_of(i0 + 32);
                     }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    ok = wait_all(&ms.kv_empty[st][h], ph ^ 1);
                     if (!ok) break;
-                    uint8_t *dst = sKV + st * L::STAGE + p * L::PART;
+                    const int boxes = max(0, min(per_half, nboxes - i0));
+                    mbar_arrive_expect_tx_warp(&ms.kv_full[st], boxes * box_bytes);
+                    uint32_t dst = kv0 + st * L::STAGE + h * L::HALF;
 #pragma unroll 1
                     for (int i = 0; i < boxes; ++i) {
                         const int id = __shfl_sync(0xffffffffu, bid, (i0 + i) & 31);
-                        const int grp = (int)((tok0 + ((int64_t)(i0 + i) << bshift)) & ((1 << a.block_shift) - 1)) >> 3;
-                        if (lane == 0)
-                            tma_load_5d(dst + i * box_bytes, &kv_map, &ms.kv_full[st][p], 0, 0, p * L::PCH, grp, id,
-                                        policy);
+                        tma_load_5d_warp(dst, &kv_map, &ms.kv_full[st], 0, 0, 0, grp, id, policy);
+                        dst += box_bytes;
+                        if (a.block_shift > 5) grp ^= 4;  // the other 32 tokens of a 64-token block
                     }
+                    i0 += per_half;
                     ++fill;
                 }
-                if (!ok) break;
                 if (++st == NST) { st = 0; ph ^= 1; }
             }
             f += g.tiles;
@@ -299,11 +292,8 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             flag_error(a.err, PKV_DEVERR_TIMEOUT);
             *abort_flag = 1;
             // copies in flight land before the shared memory is given back
-            const uint32_t pending = minu32(fill, NST * L::PARTS);  // fill counts parts
-            for (uint32_t k = fill - pending; k < fill; ++k) {
-                const uint32_t tile = k / L::PARTS;
-                mbar_wait(&ms.kv_full[tile % NST][k % L::PARTS], (tile / NST) & 1, nullptr);
-            }
+            const uint32_t issued = (fill + 1) / 2, pending = minu32(issued, NST);  // fill counts halves
+            for (uint32_t k = issued - pending; k < issued; ++k) mbar_wait(&ms.kv_full[k % NST], (k / NST) & 1, nullptr);
             if (qloads > 0) mbar_wait(&ms.q_full, (qloads - 1) & 1, nullptr);
         }
     } else if (warp == 1) {
@@ -331,17 +321,13 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 // S has two places: the scores of two tiles before have been read
                 if (gq >= 2 && !wait_all(&ms.s_free[gq & 1], ((gq >> 1) - 1) & 1)) { ok = false; break; }
                 const uint32_t tS = tm + (gq & 1) * kLatentTile;
+                if (!wait_all(&ms.kv_full[st], ph)) { ok = false; break; }
+                tc_fence_after();
+                const uint64_t dk = dk0 + st * (L::STAGE >> 4);
 #pragma unroll
-                for (int part = 0; part < L::PARTS; ++part) {
-                    if (!wait_all(&ms.kv_full[st][part], ph)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint64_t dk = dk0 + st * (L::STAGE >> 4);
-#pragma unroll
-                    for (int k = part * L::PCH * 4; k < (part + 1) * L::PCH * 4; ++k)
-                        umma_bf16_warp(tS, dq + (((k / 4) * L::Q_CH + (k % 4) * 32) >> 4),
-                                       dk + ((L::chunk_at(k / 4) + (k % 4) * 32) >> 4), IDESC_QK, k > 0);
-                }
-                if (!ok) break;
+                for (int k = 0; k < NCH * 4; ++k)
+                    umma_bf16_warp(tS, dq + (((k / 4) * L::Q_CH + (k % 4) * 32) >> 4),
+                                   dk + (((k / 4) * 1024 + (k % 4) * 32) >> 4), IDESC_QK, k > 0);
                 umma_commit_warp(&ms.s_full[gq & 1]);
                 ++gq;
                 if (++st == NST) { st = 0; ph ^= 1; }
@@ -363,12 +349,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
         };
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        // per M block: its two chunks may lie in different parts
-        uint64_t dv0[MB];
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-            dv0[mb] = umma_desc_sw128(smem_u32(sKV) + L::chunk_at(2 * mb),
-                                      L::chunk_at(2 * mb + 1) - L::chunk_at(2 * mb), L::GROUP);
+        const uint64_t dv0 = umma_desc_sw128(smem_u32(sKV), 1024, L::GROUP);
         const uint64_t dp = umma_desc_sw128(smem_u32(sP), 16, 1024);
         uint32_t st = 0, gv = 0, seg_i = 0, moves = 0;
         bool ok = true;
@@ -380,27 +361,29 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             const uint32_t idesc_pv = umma_idesc_bf16(128, n, 1, 0);
             if (seg_i > 0) ok = wait_all(&ms.o_free, (seg_i - 1) & 1);
             for (int t = 0; t < tiles && ok; ++t) {
-                if (!wait_all(&ms.p_full[gv & 1], (gv >> 1) & 1)) { ok = false; break; }
-                const volatile int *mv = ms.moved[gv & 3];
-                if (__any_sync(0xffffffffu, mv[0] | mv[1] | mv[2] | mv[3])) {
-                    if (!wait_all(&ms.rescaled, moves & 1)) { ok = false; break; }
-                    ++moves;
+                // in the halves in which the weights come and the stage is given back
+                const uint64_t dv = dv0 + st * (L::STAGE >> 4);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!wait_all(&ms.p_full[h], gv & 1)) { ok = false; break; }
+                    if (h == 0) {
+                        const volatile int *mv = ms.moved[gv & 1];
+                        if (__any_sync(0xffffffffu, mv[0] | mv[1] | mv[2] | mv[3])) {
+                            if (!wait_all(&ms.rescaled, moves & 1)) { ok = false; break; }
+                            ++moves;
+                        }
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                        for (int ks = 2 * h; ks < 2 * h + 2; ++ks)
+                            umma_bf16_warp(tm + L::COL_O + mb * kLatentRows, dv + ((mb * 2048 + ks * 2 * L::GROUP) >> 4),
+                                           dp + ((ks * 32) >> 4), idesc_pv, t > 0 || ks > 0);
+                    umma_commit_warp(&ms.kv_empty[st][h]);
                 }
-                tc_fence_after();
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb) {
-#pragma unroll
-                    for (int ks = 0; ks < kLatentTile / 16; ++ks)
-                        umma_bf16_warp(tm + L::COL_O + mb * kLatentRows,
-                                       dv0[mb] + ((st * L::STAGE + ks * 2 * L::GROUP) >> 4),
-                                       dp + (((gv & 1) * 64 + ks * 32) >> 4),
-                                       idesc_pv, t > 0 || ks > 0);
-                    // a part is free behind the block that reads its last value chunk
-#pragma unroll
-                    for (int p = 0; p < L::PARTS; ++p)
-                        if (mb == min((p + 1) * L::PCH - 1, 2 * MB - 1) / 2) umma_commit_warp(&ms.kv_empty[st][p]);
-                }
-                umma_commit_warp(&ms.pv_done[gv & 1]);
+                if (!ok) break;
+                umma_commit_warp(&ms.pv_done);
                 ++gv;
                 if (++st == NST) st = 0;
             }
@@ -445,10 +428,10 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         // O^T, after tile `tile`'s predecessors and before its own PV: every column (= row of the
         // item) times the factor by which its reference maximum moved in that tile.
         auto rescale_if_moved = [&](uint32_t tile, int ncols) -> bool {
-            if (!wait_all(&ms.p_full[tile & 1], (tile >> 1) & 1)) return false;  // every warp's say about it
-            const volatile int *mv = ms.moved[tile & 3];
+            if (!wait_all(&ms.p_full[0], tile & 1)) return false;  // every warp's say about the tile
+            const volatile int *mv = ms.moved[tile & 1];
             if (!__any_sync(0xffffffffu, mv[0] | mv[1] | mv[2] | mv[3])) return true;
-            if (tile > 0 && !wait_all(&ms.pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1)) return false;
+            if (tile > 0 && !wait_all(&ms.pv_done, (tile - 1) & 1)) return false;
             tc_fence_after();
 #pragma unroll 1
             for (int mb = 0; mb < MB; ++mb)
@@ -487,26 +470,30 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 if (t > 0 && !rescale_if_moved(gt - 1, ncols)) { ok = false; break; }  // its PV may wait for it
                 if (!wait_all(&ms.s_full[gt & 1], (gt >> 1) & 1)) { ok = false; break; }
                 tc_fence_after();
-                uint32_t v[16];
-                tmem_ld_16x32(tl + (gt & 1) * kLatentTile, v);
+                uint32_t v[2][16];  // by half of the tile
+                tmem_ld_16x32(tl + (gt & 1) * kLatentTile, v[0]);
+                tmem_ld_16x32(tl + (gt & 1) * kLatentTile + 32, v[1]);
                 tmem_wait_ld();
-                reg_order16(v);
+                reg_order16(v[0]);
+                reg_order16(v[1]);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.s_free[gt & 1]);
                 const int vis0 = (int)min64(lim[0] - key0, kLatentTile), vis1 = (int)min64(lim[1] - key0, kLatentTile);
                 if (!__all_sync(0xffffffffu, vis0 >= kLatentTile && vis1 >= kLatentTile)) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (8 * (j >> 2) + c0 + (j & 1) >= ((j & 2) ? vis1 : vis0)) v[j] = __float_as_uint(-INFINITY);
+                    for (int j = 0; j < 32; ++j)
+                        if (8 * (j >> 2) + c0 + (j & 1) >= ((j & 2) ? vis1 : vis0))
+                            v[j >> 4][j & 15] = __float_as_uint(-INFINITY);
                 }
                 bool up[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     float mx = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mx = fmax3(mx, __uint_as_float(v[4 * i + 2 * k]), __uint_as_float(v[4 * i + 2 * k + 1]));
+                    for (int i = 0; i < 8; ++i)
+                        mx = fmax3(mx, __uint_as_float(v[i >> 2][4 * (i & 3) + 2 * k]),
+                                   __uint_as_float(v[i >> 2][4 * (i & 3) + 2 * k + 1]));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * sl2;  // scale > 0 keeps the order
                     up[k] = live[k] && mx > m_ref[k] + kAbsorbedSlack;
@@ -518,54 +505,56 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                     if ((lane & 3) == 0) ms.alpha[gt & 1][ra + 8 * k] = alpha;
                 }
                 const bool moved = __any_sync(0xffffffffu, (up[0] || up[1]) && t > 0);
-                if (lane == 0) ms.moved[gt & 3][quarter] = moved;
-                // The weights, while the tensor pipe finishes the last tile's PV.  The sum adds them as
-                // rounded, so a row that one key dominates loses nothing to their rounding.
-                uint32_t pk[8];
+                if (lane == 0) ms.moved[gt & 1][quarter] = moved;
+                // The weights, half a tile at a time, so that PV of the first half runs under the
+                // exponentials of the second.  The sum adds them as rounded, so a row that one key
+                // dominates loses nothing to their rounding.
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float base = m_ref[k] == -INFINITY ? 0.f : m_ref[k];
-                    float s0 = 0.f, s1 = 0.f;
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pk[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float e0 = fast_exp2(fmaf(__uint_as_float(v[4 * i + 2 * k]), sl2, -base));
-                        const float e1 = fast_exp2(fmaf(__uint_as_float(v[4 * i + 2 * k + 1]), sl2, -base));
-                        pk[2 * i + k] = pack_bf16x2(e0, e1);
-                        s0 += bf16_lo(pk[2 * i + k]);
-                        s1 += bf16_hi(pk[2 * i + k]);
+                    for (int k = 0; k < 2; ++k) {
+                        const float base = m_ref[k] == -INFINITY ? 0.f : m_ref[k];
+                        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float e0 = fast_exp2(fmaf(__uint_as_float(v[h][4 * i + 2 * k]), sl2, -base));
+                            const float e1 = fast_exp2(fmaf(__uint_as_float(v[h][4 * i + 2 * k + 1]), sl2, -base));
+                            pk[2 * i + k] = pack_bf16x2(e0, e1);
+                            s0 += bf16_lo(pk[2 * i + k]);
+                            s1 += bf16_hi(pk[2 * i + k]);
+                        }
+                        l[k] += s0 + s1;
                     }
-                    l[k] += s0 + s1;
-                }
-                // P has two places: PV of two tiles before comes first
-                if (gt >= 2 && !wait_all(&ms.pv_done[gt & 1], ((gt >> 1) - 1) & 1)) { ok = false; break; }
+                    // P has one place: the last tile's PV comes first
+                    if (h == 0 && gt > 0 && !wait_all(&ms.pv_done, (gt - 1) & 1)) { ok = false; break; }
 #pragma unroll
-                for (int i = 0; i < 4; i += 2)  // 16-byte chunks i and i + 1 of the tile's half of P's rows
-                    stmatrix_x4(p_row + (((4 * (gt & 1) + i + (lane >> 4)) ^ (pr & 7)) << 4), pk[2 * i], pk[2 * i + 1], pk[2 * i + 2],
-                                pk[2 * i + 3]);
-                if (key0 + kLatentTile > ctx) {
-                    // Slots past the context may hold NaN, and 0 * NaN would reach O^T: their value
-                    // columns are zeroed once the copy has landed.
-                    const uint32_t st = gt % NST;
-                    bool landed = true;
-#pragma unroll
-                    for (int p = 0; p < L::PARTS; ++p) landed = landed && wait_all(&ms.kv_full[st][p], (gt / NST) & 1);
-                    if (!landed) { ok = false; break; }
-                    const int r0 = (int)(ctx - key0), pieces = (kLatentTile - r0) * (R / 8);
-                    for (int i = tid; i < pieces; i += 128) {
-                        const int rr = r0 + i / (R / 8), x = i % (R / 8);
-                        *reinterpret_cast<uint4 *>(sKV + st * L::STAGE + (rr >> 3) * L::GROUP + L::chunk_at(x >> 3) +
-                                                   (rr & 7) * 128 + ((x & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int i = 0; i < 4; i += 2)  // 16-byte chunks i and i + 1 of the half's P rows
+                        stmatrix_x4(p_row + (((4 * h + i + (lane >> 4)) ^ (pr & 7)) << 4), pk[2 * i], pk[2 * i + 1],
+                                    pk[2 * i + 2], pk[2 * i + 3]);
+                    if (h == 0 && key0 + kLatentTile > ctx) {
+                        // Slots past the context may hold NaN, and 0 * NaN would reach O^T: their value
+                        // columns are zeroed once the copy has landed.
+                        const uint32_t st = gt % NST;
+                        if (!wait_all(&ms.kv_full[st], (gt / NST) & 1)) { ok = false; break; }
+                        const int r0 = (int)(ctx - key0), pieces = (kLatentTile - r0) * (R / 8);
+                        for (int i = tid; i < pieces; i += 128) {
+                            const int rr = r0 + i / (R / 8), x = i % (R / 8);
+                            *reinterpret_cast<uint4 *>(sKV + st * L::STAGE + (rr >> 3) * L::GROUP + (x >> 3) * 1024 +
+                                                       (rr & 7) * 128 + ((x & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
+                    fence_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ms.p_full[h]);
                 }
-                fence_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.p_full[gt & 1]);
+                if (!ok) break;
             }
             if (!ok) break;
             if (!rescale_if_moved(gt - 1, ncols)) { ok = false; break; }
             // ---- epilogue: O / l of a whole item, or the part for the merge ----
-            if (!wait_all(&ms.pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1)) { ok = false; break; }
+            if (!wait_all(&ms.pv_done, (gt - 1) & 1)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 2; ++k) {  // the four threads of a row hold its sum in parts
@@ -710,10 +699,6 @@ void plan_absorbed(int latent_dim, int sms, AbsorbedPlan *p) {
     p->off_ml = up(sizeof(AbsorbedJob) * (size_t)p->grid);
     p->off_o = p->off_ml + up(2 * (size_t)p->grid * kLatentRows * sizeof(float2));
     p->ws_bytes = p->off_o + up(2 * (size_t)p->grid * kLatentRows * latent_dim * sizeof(float));
-}
-
-int absorbed_box_chunks(int latent_dim) {
-    return latent_dim == 512 ? AbsorbedSmem<512>::PCH : AbsorbedSmem<256>::PCH;
 }
 
 template <int R>

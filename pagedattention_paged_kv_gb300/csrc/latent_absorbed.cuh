@@ -8,7 +8,7 @@ namespace pkv {
 
 constexpr int kRopeDim = 64;      // rotary columns of a cached latent row
 constexpr int kLatentRows = 64;   // query rows (token x head pairs) of a work item
-constexpr int kLatentTile = 32;   // cached tokens of a tile
+constexpr int kLatentTile = 64;   // cached tokens of a tile
 
 // Warp 0 loads, warp 1 issues QK, warps 2..5 are the softmax warpgroup, warp 6 issues PV.
 constexpr int kAbsorbedThreads = 224;
@@ -51,8 +51,7 @@ void plan_absorbed(int latent_dim, int sms, AbsorbedPlan *p);
 
 // q_map: q as (64 columns, row [total_q * num_heads], chunk) in boxes of 64 rows x all chunks;
 // kv_map: the cache as (64 columns, token in group, chunk, group of 8 tokens, block) in boxes of
-// min(block, 32 tokens) x absorbed_box_chunks(latent_dim) chunks.
-int absorbed_box_chunks(int latent_dim);
+// min(block, 32 tokens) x all chunks.
 
 cudaError_t launch_latent_absorbed(int latent_dim, const CUtensorMap &q_map, const CUtensorMap &kv_map,
                                    const AbsorbedArgs &a, cudaStream_t stream);

@@ -166,7 +166,7 @@ extern "C" int pkv_latent_attention_absorbed(void *out, const void *q, const int
     const uint32_t qbox[3] = {64, (uint32_t)pkv::kLatentRows, (uint32_t)(cols / 64)};
     st = pkv::encode_tiled(&qmap, 3, q, qdims, qstride, qbox);
     if (st == PKV_OK) st = encode_latent_map(&kvmap, latent_cache, num_blocks, block_size, cols,
-                                                 pkv::absorbed_box_chunks(latent_dim));
+                                                 cols / 64);
     if (st != PKV_OK) return st;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     pkv::AbsorbedArgs a;
