@@ -218,7 +218,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         return;
     }
     SeqWalk<AbsorbedUnits> w;
-    w.start(ms.start);
+    w.start(sb, ms.start);
 
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
@@ -242,14 +242,16 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             const int64_t tok0 = (int64_t)g.kb * kLatentTile;
             const int64_t tok1 = min64(w.q.ctx, tok0 + (int64_t)g.tiles * kLatentTile);
             const int nboxes = (int)((tok1 - tok0 + (1 << bshift) - 1) >> bshift);
-            auto block_of = [&](int i) -> int {
-                if (i + lane >= nboxes) return -1;
-                const int id = table[(tok0 + ((int64_t)(i + lane) << bshift)) >> a.block_shift];
+            auto entry = [&](int i) -> int {
+                return i + lane < nboxes ? table[(tok0 + ((int64_t)(i + lane) << bshift)) >> a.block_shift] : 0;
+            };
+            // looked at only when its window begins, so that nothing waits for the load before
+            auto checked = [&](int id) -> int {
                 if (id >= 0 && id < a.num_blocks) return id;
                 flag_error(a.err, PKV_DEVERR_BLOCK_ID);
                 return -1;  // an out-of-range box is filled with zeros
             };
-            int bid = -1, bid_next = block_of(0);  // under way while Q is asked for
+            int bid = 0, next = entry(0);  // under way while Q is asked for
             if (lane == 0) {
                 if (qloads > 0) ok = mbar_wait(&ms.q_empty, (qloads - 1) & 1, abort_flag, a.wait_ns);
                 if (ok) {
@@ -266,8 +268,9 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if ((i0 & 31) == 0) {
-                        bid = bid_next;
-                        bid_next = block_of(i0 + 32);
+                        const int raw = next;
+                        next = entry(i0 + 32);
+                        bid = checked(raw);
                     }
                     ok = wait_all(&ms.kv_empty[st][h], ph ^ 1);
                     if (!ok) break;

@@ -167,7 +167,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
     };
     bool ok = true;
     SeqWalk<ExpandUnits> w;
-    if (g0 < NT) w.start(ms.start);
+    if (works && g0 < NT) w.start(sb, ms.start);  // (ms.start is written for these only)
 
     if (!works) {
         // nothing to do but to meet the other CTA at the end
@@ -223,12 +223,20 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (++h == H) { h = 0; ++p; }
         }
-        if (!ok && lane == 0) {
-            flag_error(a.err, PKV_DEVERR_TIMEOUT);
-            *abort_flag = 1;
-            const uint32_t pending = minu32(fill, NST);  // copies in flight land first
-            for (uint32_t k = fill - pending; k < fill; ++k) mbar_wait(&ms.w_full[k % NST], (k / NST) & 1, nullptr);
-            if (aloads > 0) mbar_wait(&ms.a_full, (aloads - 1) & 1, nullptr);
+        if (lane == 0) {
+            const uint32_t pending = minu32(fill, NST);
+            if (ok) {
+                // the other CTA's last arrivals at this one's barriers come before it ends
+                for (uint32_t k = fill - pending; k < fill && ok; ++k)
+                    ok = mbar_wait(&ms.w_empty[k % NST], (k / NST) & 1, abort_flag, a.wait_ns);
+            }
+            if (!ok) {
+                flag_error(a.err, PKV_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+                // copies in flight land first
+                for (uint32_t k = fill - pending; k < fill; ++k) mbar_wait(&ms.w_full[k % NST], (k / NST) & 1, nullptr);
+                if (aloads > 0) mbar_wait(&ms.a_full, (aloads - 1) & 1, nullptr);
+            }
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------

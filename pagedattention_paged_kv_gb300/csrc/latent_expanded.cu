@@ -212,7 +212,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     tc_fence_after();
     const uint32_t tmem = ms.tmem_slot;
     SeqWalk<ExpandedUnits> w;
-    w.start(ms.start);
+    w.start(sb, ms.start);
     auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
     };

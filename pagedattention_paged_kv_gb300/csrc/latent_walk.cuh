@@ -24,21 +24,31 @@ struct SeqInfo {
     bool dead;
 };
 
-__device__ __forceinline__ SeqInfo read_seq(const SeqBatch &b, int s, bool report) {
+// What memory holds about sequence s; the three loads are independent and nothing waits for them here.
+struct SeqRaw {
+    int32_t q0, q1, ctx;
+};
+__device__ __forceinline__ SeqRaw fetch_seq(const SeqBatch &b, int s) {
+    SeqRaw r;
+    r.q0 = b.query_start_loc ? b.query_start_loc[s] : s;
+    r.q1 = b.query_start_loc ? b.query_start_loc[s + 1] : s + 1;
+    r.ctx = b.context_lens[s];
+    return r;
+}
+
+__device__ __forceinline__ SeqInfo judge_seq(const SeqBatch &b, const SeqRaw &w, bool report) {
     SeqInfo r;
-    const int64_t q0 = b.query_start_loc ? b.query_start_loc[s] : s;
-    const int64_t q1 = b.query_start_loc ? b.query_start_loc[s + 1] : s + 1;
-    r.q0 = (int)q0;
+    r.q0 = w.q0;
     r.q_len = 0;
     r.ctx = 0;
     r.dead = false;
-    if (q0 < 0 || q1 < q0 || q1 > b.total_q) {
+    if (w.q0 < 0 || w.q1 < w.q0 || w.q1 > b.total_q) {
         if (report) flag_error(b.err, PKV_DEVERR_QUERY_LEN);
         return r;
     }
-    if (q1 == q0) return r;
-    r.q_len = (int)(q1 - q0);
-    r.ctx = b.context_lens[s];
+    if (w.q1 == w.q0) return r;
+    r.q_len = w.q1 - w.q0;
+    r.ctx = w.ctx;
     if (r.ctx < 0 || r.ctx > b.max_context) {
         if (report) flag_error(b.err, PKV_DEVERR_CONTEXT_LEN);
         r.dead = true;
@@ -48,6 +58,10 @@ __device__ __forceinline__ SeqInfo read_seq(const SeqBatch &b, int s, bool repor
         r.dead = true;
     }
     return r;
+}
+
+__device__ __forceinline__ SeqInfo read_seq(const SeqBatch &b, int s, bool report) {
+    return judge_seq(b, fetch_seq(b, s), report);
 }
 
 // Units(const SeqInfo &) -> int64_t gives the work units of a live sequence.
@@ -132,23 +146,28 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 // Every call is warp-wide; the current sequence's data is uniform.
 template <typename Units>
 struct SeqWalk {
-    int base;          // sequence of lane 0
     int s;             // current sequence
     int64_t pre;       // units before it
     int64_t units;     // its units (> 0)
     SeqInfo q;
-    SeqInfo mine;      // this lane's sequence
+    int base;          // sequence of lane 0
+    SeqRaw raw;        // this lane's sequence, not looked at yet (fresh) ...
+    bool fresh;
+    SeqInfo mine;      // ... and once it has been
     int64_t my_units;
 
-    __device__ __forceinline__ void load(const SeqBatch &b, const Units &u, int first) {
+    __device__ __forceinline__ void fetch(const SeqBatch &b, int first) {
         base = first;
+        raw.q0 = raw.q1 = raw.ctx = 0;
         const int i = first + (int)(threadIdx.x & 31);
-        my_units = 0;
-        mine.ctx = mine.q0 = mine.q_len = 0;
-        if (i < b.num_seqs) {
-            mine = read_seq(b, i, false);
-            if (mine.q_len > 0 && !mine.dead) my_units = u(mine);
-        }
+        if (i < b.num_seqs) raw = fetch_seq(b, i);
+        fresh = true;
+    }
+    __device__ __forceinline__ void look(const SeqBatch &b, const Units &u) {
+        if (!fresh) return;
+        fresh = false;
+        mine = judge_seq(b, raw, false);
+        my_units = mine.q_len > 0 && !mine.dead ? u(mine) : 0;
     }
     __device__ __forceinline__ void take(int l) {
         s = base + l;
@@ -158,25 +177,26 @@ struct SeqWalk {
         q.dead = false;
         units = __shfl_sync(0xffffffffu, my_units, l);
     }
-    // The sequences behind the first are loaded by the first seek that leaves it.
-    __device__ __forceinline__ void start(const WalkStart &st) {
+    // The loads of the sequences behind the first are under way from here on, and waited for by
+    // the first seek that needs them.
+    __device__ __forceinline__ void start(const SeqBatch &b, const WalkStart &st) {
         s = st.s;
         pre = st.pre;
         units = st.units;
         q = st.q;
-        base = s - 31;  // the last lane's sequence: no lane holds a later one
-        my_units = 0;
+        fetch(b, s);
     }
     // Moves on until the current sequence holds unit f (f >= pre, f below the batch's total).
     __device__ __forceinline__ void seek(const SeqBatch &b, const Units &u, int64_t f) {
         while (f >= pre + units) {
             pre += units;
-            unsigned later = 0;
+            look(b, u);
             const int at = s - base;
-            later = __ballot_sync(0xffffffffu, my_units > 0) & (at >= 31 ? 0u : 0xffffffffu << (at + 1));
+            unsigned later = __ballot_sync(0xffffffffu, my_units > 0) & (at >= 31 ? 0u : 0xffffffffu << (at + 1));
             while (later == 0) {
                 if (base + 32 >= b.num_seqs) return;  // past the last sequence (not reached for f < total)
-                load(b, u, base + 32);
+                fetch(b, base + 32);
+                look(b, u);
                 later = __ballot_sync(0xffffffffu, my_units > 0);
             }
             take(__ffs(later) - 1);
