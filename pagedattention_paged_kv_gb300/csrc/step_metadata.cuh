@@ -5,7 +5,7 @@
 
 namespace pkv {
 
-constexpr int kStepMaxSeqs = 16384;  // three int32 prefix entries a sequence in shared memory
+constexpr int kStepMaxSeqs = 16384;  // 14 bytes a sequence in shared memory
 
 struct StepArgs {
     int32_t *block_tables;     // [num_seqs][max_blocks_per_seq], new entries written
