@@ -16,7 +16,7 @@
 //  * A work item is 64 query rows (row = token * heads + head) of one sequence; its units
 //    are tiles of 64 cached tokens.  A persistent grid takes equal contiguous shares of the
 //    flat unit list (pkv_split.cuh); items cut by a share boundary leave
-//    parts that latent_merge_kernel joins.
+//    parts that a second kernel joins (latent_merge.cuh).
 //  * A tile arrives as one TMA box a block and part (blocks of 8 to 64 tokens, several 64-column
 //    chunks).  In shared memory
 //    every 8 tokens of a part are [chunk][8 tokens][128 bytes], 128-byte swizzled, whatever the block
@@ -33,6 +33,7 @@
 #include "attn_block.cuh"
 #include "fp32x2.cuh"
 #include "latent_absorbed.cuh"
+#include "latent_merge.cuh"
 #include "latent_walk.cuh"
 #include "pkv_split.cuh"
 #include "tcgen05.cuh"
@@ -188,7 +189,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         // The merge job of the boundary before this CTA's share: the item split there, when that
         // is its first split.
         if (threadIdx.x == 64) {
-            AbsorbedJob j{0, 0, 0, -1, -1, 0, 0};
+            LatentJob j{0, 0, 0, -1, -1, 0, 0};
             if (works && c > 0) {
                 const SeqInfo q = ms.start.q;
                 const int64_t nk = (q.ctx + kLatentTile - 1) / kLatentTile;
@@ -196,7 +197,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 if (begin != lo && begin >= quotient((c - 1) * T, ge)) {
                     j.item_begin = begin;
                     j.total_units = T;
-                    j.row0 = (int64_t)q.q0 * a.num_heads + grp * kLatentRows;
+                    j.out_off = ((int64_t)q.q0 * a.num_heads + grp * kLatentRows) * R;
                     j.c0 = c - 1;
                     j.c1 = share_owner(begin + nk - 1, T, ge);
                     j.ge = ge;
@@ -619,87 +620,11 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Log-sum-exp merge of the parts of split items: with part p's reference maximum m_p, sum l_p and
-// unnormalised o_p, out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p, M = max_p m_p.
-//
-// Bound: L2, which holds the parts (128 KiB each at R = 512) just written.  A thread has 4 columns
-// of kMergeRows rows, and the loads of four parts of each are in flight together.
-constexpr int kMergeRows = 2;
-
-template <int R>
-__global__ void __launch_bounds__(256, 3) latent_merge_kernel(const AbsorbedArgs a) {
-    constexpr int CG = R / 4, SETS = 256 / CG;  // threads of a row, rows side by side
-    pdl_wait();
-    const AbsorbedJob j = a.ws_jobs[blockIdx.x];
-    if (j.c0 < 0) return;
-    const int nparts = j.c1 - j.c0 + 1;
-    const int cg = threadIdx.x % CG, row0 = blockIdx.y * (SETS * kMergeRows) + threadIdx.x / CG;
-    float M[kMergeRows], Ls[kMergeRows];
-    float4 acc[kMergeRows];
-#pragma unroll
-    for (int k = 0; k < kMergeRows; ++k) {
-        M[k] = -INFINITY;
-        Ls[k] = 0.f;
-        acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    constexpr int U = 4;
-    for (int p0 = 0; p0 < nparts; p0 += U) {
-        float2 ml[U][kMergeRows];
-        float4 o[U][kMergeRows];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t slot = part_slot(j.c0 + min(p0 + u, nparts - 1), j.item_begin, j.total_units, j.ge);
-#pragma unroll
-            for (int k = 0; k < kMergeRows; ++k) {
-                const int row = row0 + k * SETS;
-                ml[u][k] = make_float2(-INFINITY, 0.f);
-                o[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (p0 + u < nparts && row < j.rows) {
-                    ml[u][k] = __ldcg(a.ws_ml + slot * kLatentRows + row);
-                    o[u][k] = __ldcg(reinterpret_cast<const float4 *>(a.ws_o + (slot * kLatentRows + row) * R) + cg);
-                }
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kMergeRows; ++k) {
-            float mc = M[k];
-#pragma unroll
-            for (int u = 0; u < U; ++u) mc = fmaxf(mc, ml[u][k].x);
-            const float base = mc == -INFINITY ? 0.f : mc;  // a row no part has seen keeps weights 0
-            const float s = fast_exp2(M[k] - base);
-            M[k] = mc;
-            Ls[k] *= s;
-            acc[k].x *= s;
-            acc[k].y *= s;
-            acc[k].z *= s;
-            acc[k].w *= s;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float wgt = fast_exp2(ml[u][k].x - base);
-                Ls[k] = fmaf(wgt, ml[u][k].y, Ls[k]);
-                acc[k].x = fmaf(wgt, o[u][k].x, acc[k].x);
-                acc[k].y = fmaf(wgt, o[u][k].y, acc[k].y);
-                acc[k].z = fmaf(wgt, o[u][k].z, acc[k].z);
-                acc[k].w = fmaf(wgt, o[u][k].w, acc[k].w);
-            }
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < kMergeRows; ++k) {
-        const int row = row0 + k * SETS;
-        if (row >= j.rows) continue;
-        const float inv = Ls[k] > 0.f ? 1.f / Ls[k] : 0.f;
-        const uint2 v = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
-                                   pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
-        reinterpret_cast<uint2 *>(a.out + (j.row0 + row) * R)[cg] = v;
-    }
-}
-
 void plan_absorbed(int latent_dim, int sms, AbsorbedPlan *p) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     p->grid = sms;
     p->off_jobs = 0;
-    p->off_ml = up(sizeof(AbsorbedJob) * (size_t)p->grid);
+    p->off_ml = up(sizeof(LatentJob) * (size_t)p->grid);
     p->off_o = p->off_ml + up(2 * (size_t)p->grid * kLatentRows * sizeof(float2));
     p->ws_bytes = p->off_o + up(2 * (size_t)p->grid * kLatentRows * latent_dim * sizeof(float));
 }
@@ -713,8 +638,7 @@ static cudaError_t launch_absorbed(const CUtensorMap &q_map, const CUtensorMap &
     e = launch_pdl(latent_absorbed_kernel<R>, dim3(a.grid), dim3(kAbsorbedThreads), AbsorbedSmem<R>::BYTES, stream,
                    q_map, kv_map, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(latent_merge_kernel<R>, dim3(a.grid, kLatentRows / kMergeRows * (R / 4) / 256), dim3(256), 0,
-                      stream, a);
+    return launch_latent_merge<R, kLatentRows>(a.ws_jobs, a.ws_ml, a.ws_o, a.out, R, a.grid, stream);
 }
 
 cudaError_t launch_latent_absorbed(int latent_dim, const CUtensorMap &q_map, const CUtensorMap &kv_map,

@@ -2,6 +2,7 @@
 // (latent_absorbed.cu).
 #pragma once
 
+#include "latent_merge.cuh"
 #include "pkv_common.cuh"
 
 namespace pkv {
@@ -12,14 +13,6 @@ constexpr int kLatentTile = 64;   // cached tokens of a tile
 
 // Warp 0 loads, warp 1 issues QK, warps 2..5 are the softmax warpgroup, warp 6 issues PV.
 constexpr int kAbsorbedThreads = 224;
-
-// An item whose tiles lie in the shares of CTAs c0 .. c1 (c0 < 0: none); written by CTA c0 + 1, whose
-// share begins inside it.
-struct AbsorbedJob {
-    int64_t item_begin, total_units;  // first unit; units of the batch
-    int64_t row0;                     // first query row (token * heads + head)
-    int32_t c0, c1, ge, rows;
-};
 
 struct AbsorbedArgs {
     __nv_bfloat16 *out;
@@ -35,7 +28,7 @@ struct AbsorbedArgs {
     bool causal;
     int64_t num_blocks;
     float scale_log2;
-    AbsorbedJob *ws_jobs;            // [grid]
+    LatentJob *ws_jobs;              // [grid]
     float2 *ws_ml;                   // [2 * grid][64]: a part's reference maxima and sums
     float *ws_o;                     // [2 * grid][64][latent_dim]: its unnormalised output
     int *err;

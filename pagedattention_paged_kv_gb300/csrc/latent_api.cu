@@ -131,7 +131,7 @@ extern "C" size_t pkv_latent_workspace_size(int op, int num_seqs, int total_q_to
     if (op == PKV_OP_LATENT_EXPANDED) {
         pkv::ExpandedPlan p;
         pkv::plan_expanded(num_seqs, total_context, num_heads, d.sms, &p);
-        if (p.padded * num_heads > (int64_t)INT32_MAX - 128) return 0;
+        if (p.padded * num_heads > (int64_t)INT32_MAX / 4 - 128) return 0;
         return p.ws_bytes;
     }
     return 0;
@@ -183,7 +183,7 @@ extern "C" int pkv_latent_attention_absorbed(void *out, const void *q, const int
     a.causal = causal != 0;
     a.num_blocks = num_blocks;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.ws_jobs = reinterpret_cast<pkv::AbsorbedJob *>(ws + p.off_jobs);
+    a.ws_jobs = reinterpret_cast<pkv::LatentJob *>(ws + p.off_jobs);
     a.ws_ml = reinterpret_cast<float2 *>(ws + p.off_ml);
     a.ws_o = reinterpret_cast<float *>(ws + p.off_o);
     a.err = d.err;
@@ -219,12 +219,11 @@ extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int
     if (st != PKV_OK) return st;
     pkv::ExpandedPlan p;
     pkv::plan_expanded(num_seqs, total_context, num_heads, d.sms, &p);
-    if (p.padded * num_heads > (int64_t)INT32_MAX - 128) return PKV_ERR_UNSUPPORTED;
+    if (p.padded * num_heads > (int64_t)INT32_MAX / 4 - 128) return PKV_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < p.ws_bytes) return PKV_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned_to(workspace, 256)) return PKV_ERR_INVALID_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     pkv::ExpandedBuffers buf;
-    buf.tile_off = reinterpret_cast<int32_t *>(ws + p.off_tiles);
     buf.rope = reinterpret_cast<__nv_bfloat16 *>(ws + p.off_rope);
     buf.kv = reinterpret_cast<uint16_t *>(ws + p.off_kv);
     buf.padded = p.padded;
@@ -243,8 +242,8 @@ extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int
     if (st == PKV_OK) st = pkv::encode_tiled(&qmap, 4, q, qdims, qstride, qbox);
     // a call whose sequences have no context at all has nothing to expand, but maps must be valid
     const int64_t padded = p.padded > 0 ? p.padded : pkv::kExpTile;
-    const uint64_t kvdims[2] = {2 * pkv::kExpHeadDim, (uint64_t)padded * num_heads};
-    const uint64_t kvstride[1] = {4 * pkv::kExpHeadDim};
+    const uint64_t kvdims[2] = {64, (uint64_t)padded * num_heads * 4};
+    const uint64_t kvstride[1] = {128};
     if (st == PKV_OK) st = pkv::encode_tiled(&kvmap, 2, buf.kv, kvdims, kvstride, rows128);
     const uint64_t rdims[2] = {pkv::kExpRope, (uint64_t)padded};
     const uint64_t rstride[1] = {pkv::kExpRope * 2};
@@ -281,7 +280,7 @@ extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int
     a.causal = causal != 0;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.buf = buf;
-    a.ws_jobs = reinterpret_cast<pkv::MergeJob *>(ws + p.off_jobs);
+    a.ws_jobs = reinterpret_cast<pkv::LatentJob *>(ws + p.off_jobs);
     a.ws_ml = reinterpret_cast<float2 *>(ws + p.off_ml);
     a.ws_o = reinterpret_cast<float *>(ws + p.off_o);
     a.err = d.err;

@@ -144,14 +144,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
     // A batch with more tokens than the caller counted is refused whole; the attention kernel
     // sees the same sum and writes zero rows.
     const int64_t NT = sc.total <= a.buf.padded / kExpTile ? sc.total : 0;
-    if (blockIdx.x == 0) {
-        if (NT != sc.total && threadIdx.x == 0) flag_error(a.err, PKV_DEVERR_CONTEXT_LEN);
-        int64_t run = sc.run;
-        for (int s = sc.beg; s < sc.end; ++s) {
-            a.buf.tile_off[s] = (int32_t)run;
-            run += seq_units_of(sb, units, s, false);
-        }
-    }
+    if (blockIdx.x == 0 && NT != sc.total && threadIdx.x == 0) flag_error(a.err, PKV_DEVERR_CONTEXT_LEN);
     const int64_t T = (NT + 1) / 2 * H;  // (pair, head) units
     const int ge = split_ctas(T, nc, 1);
     const bool works = T > 0 && c < ge;
@@ -299,7 +292,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
             if (!wait_all(&ms.acc_full[n & 1], (n >> 1) & 1)) { ok = false; break; }
             tc_fence_after();
             if (g < NT) {
-                uint16_t *dst = a.buf.kv + ((int64_t)h * a.buf.padded + row0 + row) * 256;
+                uint16_t *dst = a.buf.kv + ((int64_t)h * 4 * a.buf.padded + row0 + row) * 64;
 #pragma unroll 1
                 for (int q = 0; q < 8; ++q) {  // 32 columns: four of keys, four of values
                     uint32_t r[32];
@@ -322,7 +315,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
                         uint32_t x[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) x[j] = pack_16(is_v, r[16 * k + 2 * j], r[16 * k + 2 * j + 1]);
-                        st_global_32(dst + q * 32 + k * 16, x);
+                        st_global_32(dst + (q >> 1) * a.buf.padded * 64 + (q & 1) * 32 + k * 16, x);
                     }
                 }
             }

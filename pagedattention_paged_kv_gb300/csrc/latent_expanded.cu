@@ -9,11 +9,14 @@
 // Layout
 //  * A work tile is 256 query tokens of one head as two 128-row MMA halves; its units are
 //    128-key chunks, causal tiles stop at their last query's position.  A persistent grid
-//    takes equal contiguous shares of the flat unit list; split tiles are merged by
-//    log-sum-exp weights (merge.cuh).
-//  * The producer streams K (three 64-column pieces: two of the head's keys, one rotary) and V
-//    (two pieces) of a chunk; Q takes 96 KiB, so there are two K places and one V place, and
-//    a chunk's V is fetched while its scores are computed.
+//    takes equal contiguous shares of the flat unit list; split tiles are joined by a
+//    second kernel (latent_merge.cuh).
+//  * A chunk is 80 KiB: a pair of 64-column pieces of the head's keys, the rotary piece, and a
+//    pair of its values.  Q takes 96 KiB, so two whole chunks do not fit; the pairs go through
+//    three places and the rotary pieces through two; a place is reused by the pair three on in the
+//    order keys, values, keys, .. .  (With one place for
+//    values their latency was half of a chunk's time: 5,000 cycles for 2,560 of tensor work.)
+//  * A causal tile's first half skips the chunks that only its second half sees.
 //  * Per half TMEM holds S (128 columns, overwritten by the 16-bit weights P) and O (128).  The
 //    issuer runs PV of one half and QK of its next chunk while the other half's warpgroup (one
 //    thread a row) computes its weights, as in the paged prefill.
@@ -39,21 +42,22 @@ constexpr int kExpandedThreads = 384;  // loads, MMAs, two idle warps, two softm
 struct ExpandedSmem {
     static constexpr uint32_t PIECE = 128 * 128;             // 128 rows x 64 columns
     static constexpr uint32_t Q_BYTES = 2 * 3 * PIECE;       // [half][piece]
-    static constexpr uint32_t K_SLOT = 3 * PIECE, V_SLOT = 2 * PIECE;
-    static constexpr uint32_t OFF_K = Q_BYTES;               // two slots
-    static constexpr uint32_t OFF_V = OFF_K + 2 * K_SLOT;    // one slot
-    static constexpr uint32_t OFF_MISC = OFF_V + V_SLOT;
+    static constexpr uint32_t PAIR = 2 * PIECE;
+    static constexpr uint32_t OFF_PAIRS = Q_BYTES;           // three places
+    static constexpr uint32_t OFF_ROPE = OFF_PAIRS + 3 * PAIR;  // two places
+    static constexpr uint32_t OFF_MISC = OFF_ROPE + 2 * PIECE;
     static constexpr uint32_t BYTES = OFF_MISC + 1024 + 1024;
     static constexpr uint32_t HALF_COLS = 256, COL_O = 128;
     static_assert(BYTES <= 232448, "fits one CTA");
 };
 
 struct ExpandedMisc {
-    uint64_t q_full, q_empty, v_full, v_empty, mma_done;
-    uint64_t k_full[2], k_empty[2];
+    uint64_t q_full, q_empty, mma_done;
+    uint64_t full[3], empty[3], rope_full[2], rope_empty[2];
     uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
     int64_t scan[16];
     WalkStart start;
+    int64_t start_tiles;
     uint32_t tmem_slot;
     int abort_flag;
 };
@@ -107,6 +111,7 @@ struct ExpandedSegment {
     int64_t qt;          // tile
     int kb, chunks;      // first chunk of the segment, chunks in it
     int tokens;          // query tokens of the tile
+    int first_half;      // chunks of the segment that the tile's first half sees
     bool whole;
 };
 
@@ -124,7 +129,14 @@ __device__ __forceinline__ ExpandedSegment expanded_segment(const SeqInfo &q, bo
     g.chunks = (int)min64(n - g.kb, hi - f);
     g.tokens = (int)min64(kExpQTile, q.q_len - g.qt * kExpQTile);
     g.whole = g.kb == 0 && g.chunks == n;
+    const int64_t last0 = q.ctx - q.q_len + g.qt * kExpQTile + min(g.tokens, 128);  // keys its last token sees
+    g.first_half = causal && g.tokens > 128 ? (int)max64(0, min64(g.chunks, (last0 + kExpTile - 1) / kExpTile - g.kb)) : g.chunks;
     return g;
+}
+
+// Chunks of a segment that half h has to do with.
+__device__ __forceinline__ int half_chunks(const ExpandedSegment &g, int h) {
+    return h == 0 ? g.first_half : g.tokens > 128 ? g.chunks : 0;
 }
 
 }  // namespace
@@ -135,7 +147,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     using L = ExpandedSmem;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sQ = smem, *sK = smem + L::OFF_K, *sV = smem + L::OFF_V;
+    uint8_t *sQ = smem, *sPairs = smem + L::OFF_PAIRS, *sRope = smem + L::OFF_ROPE;
     ExpandedMisc &ms = *reinterpret_cast<ExpandedMisc *>(smem + L::OFF_MISC);
     volatile int *abort_flag = &ms.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -144,12 +156,14 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     if (threadIdx.x == 0) {
         mbar_init(&ms.q_full, 1);
         mbar_init(&ms.q_empty, 1);
-        mbar_init(&ms.v_full, 1);
-        mbar_init(&ms.v_empty, 1);
         mbar_init(&ms.mma_done, 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&ms.full[i], 1);
+            mbar_init(&ms.empty[i], 1);
+        }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&ms.k_full[i], 1);
-            mbar_init(&ms.k_empty[i], 1);
+            mbar_init(&ms.rope_full[i], 1);
+            mbar_init(&ms.rope_empty[i], 1);
             mbar_init(&ms.s_full[i], 1);
             mbar_init(&ms.p_full[i], 4);  // one arrival per softmax warp of the half
             mbar_init(&ms.pv_done[i], 1);
@@ -163,48 +177,56 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         tma_prefetch_desc(&kv_map);
         tma_prefetch_desc(&rope_map);
     }
-    pdl_wait();
+    // The expansion's CTAs let this kernel start once everything before them is complete, so all
+    // inputs of the call may be read here; only what the expansion writes has to be waited for, and
+    // only by the producer (CTAs without work wait too, so that this grid ends behind the last).
     pdl_trigger();
     const SeqBatch sb{a.query_start_loc, a.context_lens, a.num_seqs, a.total_q, a.max_context, a.err};
     const ExpandedUnits units{a.num_heads, a.causal};
     // (the expansion kernel has reported bad sequences already)
-    const bool fits = scan_batch(sb, TokenTiles{}, ms.scan, false).total <= a.buf.padded / kExpTile;
+    const BatchScan st = scan_batch(sb, TokenTiles{}, ms.scan, false);
+    const bool fits = st.total <= a.buf.padded / kExpTile;
     const BatchScan sc = scan_batch(sb, units, ms.scan, false);
     const int64_t T = fits ? sc.total : 0;
     const int ge = split_ctas(T, a.grid, 1);
     const bool works = T > 0 && c < ge;
-    const int64_t lo = works ? share_begin(c, T, ge) : 0, hi = works ? share_begin(c + 1, T, ge) : 0;
-    if (works) find_unit(sb, units, sc, lo, &ms.start);
+    const int64_t lo = works ? quotient(c * T, ge) : 0, hi = works ? quotient((c + 1) * T, ge) : 0;
+    if (works && lo >= sc.run && lo < sc.run + sc.local) {
+        find_unit(sb, units, sc, lo, &ms.start);
+        int64_t tiles = st.run;  // expansion tiles before the sequence
+        for (int s = st.beg; s < ms.start.s; ++s) tiles += seq_units_of(sb, TokenTiles{}, s, false);
+        ms.start_tiles = tiles;
+    }
     __syncthreads();
 
     // The merge job of the boundary before this CTA's share (see latent_absorbed.cu).
     if (threadIdx.x == 0) {
-        MergeJob j;
-        no_job(j);
+        LatentJob j{0, 0, 0, -1, -1, 0, 0};
         if (works && c > 0) {
             const SeqInfo q = ms.start.q;
             const ExpandedSegment g = expanded_segment(q, a.causal, ms.start.pre, lo, hi);
             if (g.kb != 0 && g.tile_begin >= share_begin(c - 1, T, ge)) {
                 j.item_begin = g.tile_begin;
                 j.total_units = T;
-                j.out_row0 = q.q0 + g.qt * kExpQTile;
+                j.out_off = ((q.q0 + g.qt * kExpQTile) * a.num_heads + g.h) * kExpHeadDim;
                 j.c0 = c - 1;
                 j.c1 = share_owner(g.tile_begin + ExpandedTiles(q, a.causal).chunks(g.qt) - 1, T, ge);
                 j.ge = ge;
                 j.rows = g.tokens;
-                j.rows_per_token = 1;
-                j.head0 = g.h;
             }
         }
         if (c > 0) a.ws_jobs[c - 1] = j;
         if (c == a.grid - 1) {
-            no_job(j);
+            j.c0 = -1;
             a.ws_jobs[c] = j;
         }
     }
     zero_dead_rows(sb, c, a.grid, a.out, (int64_t)a.num_heads * kExpHeadDim, warp,
                    kExpandedThreads / 32, !fits);
-    if (!works) return;
+    if (!works) {
+        pdl_wait();
+        return;
+    }
 
     if (warp == 1) tmem_alloc(&ms.tmem_slot, 512);
     tc_fence_before();
@@ -220,124 +242,171 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
 
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
+        // The warp runs it together on uniform values; one elected lane issues.
         const uint64_t policy = l2_policy_evict_normal();
-        uint32_t n = 0, segs = 0;  // chunks and tiles issued
-        bool v_pending = false;
+        const uint32_t pairs0 = smem_u32(sPairs), rope0 = smem_u32(sRope);
+        uint32_t n = 0, segs = 0;  // chunks (keys) and tiles issued
+        // pair i = 2 chunk (keys) or 2 chunk + 1 (values) of the CTA
+        const int pitch = (int)a.buf.padded;  // rows from a piece to the next
+        auto load_pair = [&](uint32_t i, int row) -> bool {
+            const uint32_t at = i % 3, times = i / 3;
+            if (times > 0 && !wait_all(&ms.empty[at], (times - 1) & 1)) return false;
+            mbar_arrive_expect_tx_warp(&ms.full[at], L::PAIR);
+            tma_load_2d_warp(pairs0 + at * L::PAIR, &kv_map, &ms.full[at], 0, row, policy);
+            tma_load_2d_warp(pairs0 + at * L::PAIR + L::PIECE, &kv_map, &ms.full[at], 0, row + pitch, policy);
+            return true;
+        };
+        int64_t tiles = ms.start_tiles;
+        int seq = ms.start.s, ctx = ms.start.q.ctx;
+        bool waited = false;
         for (int64_t f = lo; f < hi && ok;) {
             w.seek(sb, units, f);
             const ExpandedSegment g = expanded_segment(w.q, a.causal, w.pre, f, hi);
-            const int64_t tok = (int64_t)a.buf.tile_off[w.s] * kExpTile;
-            if (lane == 0) {
-                auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, a.wait_ns); };
-                if (segs > 0) ok = wait(&ms.q_empty, (segs - 1) & 1);
-                if (ok) {
-                    const int nh = g.tokens > 128 ? 2 : 1;
-                    mbar_arrive_expect_tx(&ms.q_full, nh * 3 * L::PIECE);
-                    for (int h = 0; h < nh; ++h)
-                        for (int p = 0; p < 3; ++p)
-                            tma_load_4d(sQ + (h * 3 + p) * L::PIECE, &q_map, &ms.q_full, 0, p, g.h,
-                                        (int)(w.q.q0 + g.qt * kExpQTile) + h * 128, policy);
-                    ++segs;
-                }
-                for (int ch = 0; ch < g.chunks && ok; ++ch, ++n) {
-                    const int64_t key0 = tok + (int64_t)(g.kb + ch) * kExpTile;
-                    const int row = (int)(g.h * a.buf.padded + key0);
-                    uint8_t *k = sK + (n & 1) * L::K_SLOT;
-                    ok = n < 2 || wait(&ms.k_empty[n & 1], ((n >> 1) - 1) & 1);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&ms.k_full[n & 1], L::K_SLOT);
-                    tma_load_2d(k, &kv_map, &ms.k_full[n & 1], 0, row, policy);
-                    tma_load_2d(k + L::PIECE, &kv_map, &ms.k_full[n & 1], 64, row, policy);
-                    tma_load_2d(k + 2 * L::PIECE, &rope_map, &ms.k_full[n & 1], 0, (int)key0, policy);
-                    v_pending = true;
-                    ok = n < 1 || wait(&ms.v_empty, (n - 1) & 1);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&ms.v_full, L::V_SLOT);
-                    tma_load_2d(sV, &kv_map, &ms.v_full, 128, row, policy);
-                    tma_load_2d(sV + L::PIECE, &kv_map, &ms.v_full, 192, row, policy);
-                    v_pending = false;
-                }
+            if (w.s != seq) {  // the next live sequence
+                tiles += (ctx + kExpTile - 1) / kExpTile;
+                seq = w.s;
+                ctx = w.q.ctx;
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            int key = __shfl_sync(0xffffffffu, (int)(tiles + g.kb) * kExpTile, 0);
+            int row = __shfl_sync(0xffffffffu, (int)(4 * g.h * a.buf.padded) + key, 0);
+            const int chunks = __shfl_sync(0xffffffffu, g.chunks, 0);
+            if (segs > 0) ok = wait_all(&ms.q_empty, (segs - 1) & 1);
+            if (!ok) break;
+            const int nh = g.tokens > 128 ? 2 : 1;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&ms.q_full, nh * 3 * L::PIECE);
+                for (int h = 0; h < nh; ++h)
+                    for (int p = 0; p < 3; ++p)
+                        tma_load_4d(sQ + (h * 3 + p) * L::PIECE, &q_map, &ms.q_full, 0, p, g.h,
+                                    (int)(w.q.q0 + g.qt * kExpQTile) + h * 128, policy);
+            }
+            __syncwarp();
+            ++segs;
+            if (!waited) pdl_wait();  // from here on the expansion's output is read
+            waited = true;
+            for (int ch = 0; ch < chunks; ++ch) {
+                if (!load_pair(2 * n, row)) { ok = false; break; }
+                if (n >= 2 && !wait_all(&ms.rope_empty[n & 1], ((n >> 1) - 1) & 1)) { ok = false; break; }
+                mbar_arrive_expect_tx_warp(&ms.rope_full[n & 1], L::PIECE);
+                tma_load_2d_warp(rope0 + (n & 1) * L::PIECE, &rope_map, &ms.rope_full[n & 1], 0, key, policy);
+                if (!load_pair(2 * n + 1, row + 2 * pitch)) { ok = false; break; }
+                key += kExpTile;
+                row += kExpTile;
+                ++n;
+            }
             f += g.chunks;
         }
+        if (!waited) pdl_wait();
         if (!ok && lane == 0) {
             flag_error(a.err, PKV_DEVERR_TIMEOUT);
             *abort_flag = 1;
             // copies in flight land first
-            const uint32_t nk = n + (v_pending ? 1 : 0);
-            for (uint32_t k = nk > 2 ? nk - 2 : 0; k < nk; ++k) mbar_wait(&ms.k_full[k & 1], (k >> 1) & 1, nullptr);
-            if (n > 0) mbar_wait(&ms.v_full, (n - 1) & 1, nullptr);
+            for (uint32_t k = n > 2 ? n - 2 : 0; k < n; ++k) {
+                mbar_wait(&ms.full[2 * k % 3], (2 * k / 3) & 1, nullptr);
+                mbar_wait(&ms.full[(2 * k + 1) % 3], ((2 * k + 1) / 3) & 1, nullptr);
+                mbar_wait(&ms.rope_full[k & 1], (k >> 1) & 1, nullptr);
+            }
             if (segs > 0) mbar_wait(&ms.q_full, (segs - 1) & 1, nullptr);
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
-        // PV_h(c), then QK_h(c + 1) over the same S columns; the halves alternate.
+        // PV_h(c), then QK_h(c + 1) over the same S columns; the halves alternate.  The last half to
+        // use a place gives it back.  (An issuer a half was slower: without turns the halves fall
+        // into step, weights and MMAs of both at the same time; with turns a step waits for keys that
+        // the other half's step makes room for.)
         constexpr uint32_t IDESC_QK = umma_idesc_bf16(128, kExpTile, 0, 0);
         constexpr uint32_t IDESC_PV = umma_idesc_f16(128, kExpHeadDim, 0, 1);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t dq0 = umma_desc_sw128(smem_u32(sQ), 16, 1024);
-        const uint64_t dk0 = umma_desc_sw128(smem_u32(sK), 16, 1024);
-        const uint64_t dv = umma_desc_sw128(smem_u32(sV), L::PIECE, 1024);
-        uint32_t n = 0;             // chunk whose V is next
+        const uint64_t dk0 = umma_desc_sw128(smem_u32(sPairs), 16, 1024);
+        const uint64_t dr0 = umma_desc_sw128(smem_u32(sRope), 16, 1024);
+        const uint64_t dv0 = umma_desc_sw128(smem_u32(sPairs), L::PIECE, 1024);
+        uint32_t n = 0;             // chunks whose PV is behind
+        uint32_t kp = 0, kq = 0;    // place and parity of the next chunk's keys
+        uint32_t vp = 1, vq = 0;    // and of the current one's values
         uint32_t gh[2] = {0, 0};    // chunks each half has processed
         uint32_t segh[2] = {0, 0};  // tiles each half has processed
         uint32_t segs = 0;
-        auto issue_qk = [&](int h, uint32_t chunk) {
-            const uint64_t dk = dk0 + (chunk & 1) * (L::K_SLOT >> 4);
-            const uint64_t dq = dq0 + h * (3 * L::PIECE >> 4);
-#pragma unroll
-            for (int ks = 0; ks < 12; ++ks) {
-                const uint32_t off = ((ks / 4) * L::PIECE + (ks % 4) * 32) >> 4;
-                umma_bf16_warp(tm + h * L::HALF_COLS, dq + off, dk + off, IDESC_QK, ks > 0);
+        auto next2 = [&](uint32_t &place, uint32_t &parity) {  // two pairs on
+            place += 2;
+            if (place >= 3) {
+                place -= 3;
+                parity ^= 1;
             }
+        };
+        // QK of chunk `chunk` (its keys at kp, kq)
+        auto issue_qk = [&](int h, uint32_t chunk, bool last) -> bool {
+            if (!wait_all(&ms.full[kp], kq)) return false;
+            tc_fence_after();
+            const uint64_t dk = umma_desc_at(dk0, kp * L::PAIR), dr = umma_desc_at(dr0, (chunk & 1) * L::PIECE);
+            const uint64_t dq = dq0 + h * (3 * L::PIECE >> 4);
+            const uint32_t tS = tm + h * L::HALF_COLS;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint32_t off = ((ks / 4) * L::PIECE + (ks % 4) * 32) >> 4;
+                umma_bf16_warp(tS, dq + off, dk + off, IDESC_QK, ks > 0);
+            }
+            if (last) umma_commit_warp(&ms.empty[kp]);
+            if (!wait_all(&ms.rope_full[chunk & 1], (chunk >> 1) & 1)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+                umma_bf16_warp(tS, dq + ((2 * L::PIECE + ks * 32) >> 4), dr + (ks * 32 >> 4), IDESC_QK, true);
             umma_commit_warp(&ms.s_full[h]);
+            if (last) {
+                umma_commit_warp(&ms.rope_empty[chunk & 1]);
+                next2(kp, kq);
+            }
+            return true;
+        };
+        auto issue_pv = [&](int h, bool first, bool last) -> bool {
+            if (!wait_all(&ms.full[vp], vq)) return false;
+            tc_fence_after();
+            const uint64_t dv = umma_desc_at(dv0, vp * L::PAIR);
+            const uint32_t tP = tm + h * L::HALF_COLS;
+#pragma unroll
+            for (int ks = 0; ks < kExpTile / 16; ++ks)
+                umma_bf16_tmem_a_warp(tP + L::COL_O, tP + ks * 8, dv + (ks * 2048 >> 4), IDESC_PV, !first || ks > 0);
+            umma_commit_warp(&ms.pv_done[h]);
+            if (last) {
+                umma_commit_warp(&ms.empty[vp]);
+                next2(vp, vq);
+            }
+            return true;
         };
         for (int64_t f = lo; f < hi && ok;) {
             w.seek(sb, units, f);
             const ExpandedSegment g = expanded_segment(w.q, a.causal, w.pre, f, hi);
             const int chunks = __shfl_sync(0xffffffffu, g.chunks, 0);
-            const int nh = __shfl_sync(0xffffffffu, g.tokens > 128 ? 2 : 1, 0);
-            if (!wait_all(&ms.q_full, segs & 1) || !wait_all(&ms.k_full[n & 1], (n >> 1) & 1)) { ok = false; break; }
-            tc_fence_after();
+            const int cnt[2] = {__shfl_sync(0xffffffffu, half_chunks(g, 0), 0),
+                                __shfl_sync(0xffffffffu, half_chunks(g, 1), 0)};
+            const int last = cnt[1] > 0 ? 1 : 0;  // the second half, where there is one, sees every chunk
+            if (!wait_all(&ms.q_full, segs & 1)) { ok = false; break; }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (h < nh) issue_qk(h, n);
-            umma_commit_warp(&ms.k_empty[n & 1]);
+                if (cnt[h] > 0 && ok) ok = issue_qk(h, n, h == last);
+            if (!ok) break;
             if (chunks == 1) umma_commit_warp(&ms.q_empty);
-            for (int ch = 0; ch < chunks && ok; ++ch, ++n) {
-                const bool more = ch + 1 < chunks;
-                if (!wait_all(&ms.v_full, n & 1)) { ok = false; break; }
+            for (int ch = 0; ch < chunks && ok; ++ch) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (h >= nh) break;
+                    if (ch >= cnt[h]) continue;
                     if (ch == 0 && segh[h] > 0 && !wait_all(&ms.o_free[h], (segh[h] - 1) & 1)) { ok = false; break; }
                     if (!wait_all(&ms.p_full[h], (gh[h] + ch) & 1)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t tP = tm + h * L::HALF_COLS;
-#pragma unroll
-                    for (int ks = 0; ks < kExpTile / 16; ++ks)
-                        umma_bf16_tmem_a_warp(tP + L::COL_O, tP + ks * 8, dv + ((ks * 2048) >> 4), IDESC_PV,
-                                              ch > 0 || ks > 0);
-                    umma_commit_warp(&ms.pv_done[h]);
-                    if (h == nh - 1) umma_commit_warp(&ms.v_empty);
-                    if (more) {
-                        if (h == 0 && !wait_all(&ms.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1)) { ok = false; break; }
-                        tc_fence_after();
-                        issue_qk(h, n + 1);
-                        if (h == nh - 1) {
-                            umma_commit_warp(&ms.k_empty[(n + 1) & 1]);
-                            if (ch + 2 == chunks) umma_commit_warp(&ms.q_empty);
-                        }
+                    if (!issue_pv(h, ch == 0, h == last)) { ok = false; break; }
+                    if (ch + 1 < cnt[h]) {
+                        if (!issue_qk(h, n + ch + 1, h == last)) { ok = false; break; }
+                        if (h == last && ch + 2 == chunks) umma_commit_warp(&ms.q_empty);
                     }
                 }
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (h < nh) {
-                    gh[h] += chunks;
+                if (cnt[h] > 0) {
+                    gh[h] += cnt[h];
                     segh[h] += 1;
                 }
+            n += chunks;
             f += g.chunks;
             ++segs;
         }
@@ -361,7 +430,12 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         for (int64_t f = lo; f < hi && ok;) {
             w.seek(sb, units, f);
             const ExpandedSegment g = expanded_segment(w.q, a.causal, w.pre, f, hi);
-            if (h == 1 && g.tokens <= 128) {  // this half has no query rows here
+            const int mine = half_chunks(g, h);
+            if (mine == 0) {  // this half has no query rows here, or they see none of the segment's keys
+                if (h == 0) {
+                    const int slot = part_slot(c, g.tile_begin, T, ge);
+                    a.ws_ml[(int64_t)slot * kExpQTile + row] = make_float2(-INFINITY, 0.f);
+                }
                 f += g.chunks;
                 continue;
             }
@@ -370,7 +444,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             const int64_t pos = (int64_t)(ctx - w.q.q_len) + g.qt * kExpQTile + min(tok, g.tokens - 1);
             const int64_t lim = a.causal ? pos + 1 : ctx;
             float m_ref = -INFINITY, l = 0.f;
-            for (int ch = 0; ch < g.chunks; ++ch, ++gh) {
+            for (int ch = 0; ch < mine; ++ch, ++gh) {
                 if (!wait_all(&ms.s_full[h], gh & 1)) { ok = false; break; }
                 tc_fence_after();
                 const int vis = (int)max64(0, min64(lim - (int64_t)(g.kb + ch) * kExpTile, kExpTile));
@@ -528,14 +602,13 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
 
 void plan_expanded(int num_seqs, int64_t total_context, int num_heads, int sms, ExpandedPlan *p) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    p->grid = sms < kMergeMaxParts ? sms : kMergeMaxParts;
+    p->grid = sms;
     // each sequence is padded to whole tiles
     p->padded = (total_context + (int64_t)num_seqs * (kExpTile - 1)) / kExpTile * kExpTile;
-    p->off_tiles = 0;
-    p->off_rope = up(sizeof(int32_t) * (size_t)num_seqs);
+    p->off_rope = 0;
     p->off_kv = p->off_rope + up((size_t)p->padded * kExpRope * 2);
     p->off_jobs = p->off_kv + up((size_t)num_heads * p->padded * 2 * kExpHeadDim * 2);
-    p->off_ml = p->off_jobs + up(sizeof(MergeJob) * (size_t)p->grid);
+    p->off_ml = p->off_jobs + up(sizeof(LatentJob) * (size_t)p->grid);
     p->off_o = p->off_ml + up(2 * (size_t)p->grid * kExpQTile * sizeof(float2));
     p->ws_bytes = p->off_o + up(2 * (size_t)p->grid * kExpQTile * kExpHeadDim * sizeof(float));
 }
@@ -548,8 +621,8 @@ cudaError_t launch_latent_expanded(const CUtensorMap &q_map, const CUtensorMap &
     e = launch_pdl(latent_expanded_kernel, dim3(a.grid), dim3(kExpandedThreads), ExpandedSmem::BYTES, stream, q_map,
                    kv_map, rope_map, a);
     if (e != cudaSuccess) return e;
-    const MergeArgs m{a.ws_jobs, a.ws_ml, a.ws_o, a.out, kExpQTile, a.num_heads};
-    return launch_merge<kExpHeadDim>(m, a.grid, stream);
+    return launch_latent_merge<kExpHeadDim, kExpQTile>(a.ws_jobs, a.ws_ml, a.ws_o, a.out,
+                                                       (int64_t)a.num_heads * kExpHeadDim, a.grid, stream);
 }
 
 }  // namespace pkv

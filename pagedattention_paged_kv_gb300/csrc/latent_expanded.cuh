@@ -3,7 +3,7 @@
 // attention over them (latent_expanded.cu).
 #pragma once
 
-#include "merge.cuh"
+#include "latent_merge.cuh"
 #include "pkv_common.cuh"
 
 namespace pkv {
@@ -13,13 +13,13 @@ constexpr int kExpRope = 64;
 constexpr int kExpTile = 128;     // cached tokens of an expansion tile, keys of an attention chunk
 constexpr int kExpQTile = 256;    // query tokens of an attention tile (two MMA halves)
 
-// The expanded keys and values of a call: for head h and padded token i (each sequence starts
-// on a multiple of 128, tile_off[s] tiles in), row h * padded + i of kv is [128 key columns |
-// 128 value columns]; rope row i is the token's rotary key part.  Rows past a context are zero.
+// The expanded keys and values of a call, for head h and padded token i (each sequence with query
+// rows starts on the next multiple of 128): piece p (64 key columns, the next 64, 64 value columns,
+// the next 64) is row (4 h + p) * padded + i of kv, so the 128 rows of a box are contiguous; rope
+// row i is the token's rotary key part.  Rows past a context are zero.
 struct ExpandedBuffers {
-    int32_t *tile_off;    // [num_seqs]
     __nv_bfloat16 *rope;  // [padded][64]
-    uint16_t *kv;         // [num_heads][padded][256]: bf16 keys, fp16 values
+    uint16_t *kv;         // [num_heads][4][padded][64]: bf16 keys, fp16 values
     int64_t padded;       // tokens, a multiple of 128
 };
 
@@ -45,7 +45,7 @@ struct ExpandedArgs {
     bool causal;
     float scale_log2;
     ExpandedBuffers buf;
-    MergeJob *ws_jobs;   // [grid]
+    LatentJob *ws_jobs;  // [grid]
     float2 *ws_ml;       // [2 * grid][256]
     float *ws_o;         // [2 * grid][256][128]
     int *err;
@@ -55,7 +55,7 @@ struct ExpandedArgs {
 struct ExpandedPlan {
     int grid;
     int64_t padded;
-    size_t off_tiles, off_rope, off_kv, off_jobs, off_ml, off_o, ws_bytes;
+    size_t off_rope, off_kv, off_jobs, off_ml, off_o, ws_bytes;
 };
 
 void plan_expanded(int num_seqs, int64_t total_context, int num_heads, int sms, ExpandedPlan *p);

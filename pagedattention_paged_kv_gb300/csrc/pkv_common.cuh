@@ -180,6 +180,16 @@ __device__ __forceinline__ void tma_load_5d_warp(uint32_t dst, const CUtensorMap
         "l"(cache_policy)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_2d_warp(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1,
+                                                 uint64_t cache_policy) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar)), "l"(cache_policy)
+        : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_expect_tx_warp(uint64_t *bar, uint32_t bytes) {
     asm volatile(
         "{\n\t.reg .pred e;\n\t"

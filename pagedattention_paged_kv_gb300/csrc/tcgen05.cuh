@@ -88,6 +88,13 @@ __device__ __forceinline__ void umma_commit_multicast_warp(uint64_t *bar, uint16
         : "memory");
 }
 
+// A descriptor moved by `bytes`, passed through a shuffle: the compiler then holds it in uniform
+// registers, where an offset worked out per thread costs each MMA of a warp-wide issuer some 40 cycles.
+__device__ __forceinline__ uint64_t umma_desc_at(uint64_t base, uint32_t bytes) {
+    const uint32_t lo = __shfl_sync(0xffffffffu, (uint32_t)base + (bytes >> 4), 0);
+    return (base & 0xffffffff00000000ull) | lo;
+}
+
 // Whole-warp TMEM allocation of `cols` columns; the base address lands in *slot.
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t cols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
