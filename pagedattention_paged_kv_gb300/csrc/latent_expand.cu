@@ -10,14 +10,17 @@
 // Bound: tensor.  2 * 256 * R operations against 512 bytes written a (token, head): 512
 // operations a byte at R = 512.  What feeds the tensor pipe is the question: a CTA keeps 128
 // tokens (all of R) in shared memory and streams the weights of one head after the other past
-// them, 64 bytes a cycle at the full rate, about twice what the L2 gives each of 152 SMs at
-// once.  So two CTAs with a token tile each form a cluster that walks the heads in step: each
-// loads half of every weight chunk and multicasts it to both.  The accumulator (128 tokens x
-// 256 columns, half of TMEM) is double-buffered, so the stores of one head run under the
+// them, 64 bytes a cycle at the full rate, about as much as an SM takes in, with three 32 KiB
+// stages of room.  So two CTAs with a token tile each form a pair (cta_group::2): one MMA
+// multiplies 256 tokens, each CTA holds one half of every weight chunk (its keys' rows or its
+// values' rows) for both, and the same room makes six stages.  The accumulator (128 tokens x 256
+// columns a CTA, half of TMEM) is double-buffered, so the stores of one head run under the
 // products of the next.  Units are (pair of token tiles, head), cut into equal contiguous
-// shares, so a cluster reloads its tokens only when its share crosses a pair.
-// Waits are bounded in time.  The CTAs of a cluster (always resident together) wait for each
-// other's weight halves; no cluster waits for another.
+// shares, so a pair reloads its tokens only when its share crosses tiles.
+// Measured at 16,896 tokens x 64 heads, R = 512 (283 GFLOP): 292 us for single CTAs, 228 with
+// every chunk's halves multicast to both CTAs of a cluster.
+// Waits are bounded in time.  The CTAs of a pair (always resident together) wait for each other;
+// no pair waits for another.
 #include "attn_block.cuh"
 #include "latent_expanded.cuh"
 #include "latent_walk.cuh"
@@ -35,9 +38,8 @@ struct ExpandSmem {
     static constexpr int KCH = R / 64;
     static constexpr uint32_t GROUP = KCH * 1024;         // 8 tokens, all latent chunks
     static constexpr uint32_t A_BYTES = (kExpTile / 8) * GROUP;
-    static constexpr uint32_t W_HALF = 128 * 128;         // 128 weight rows x 64 columns
-    static constexpr uint32_t W_STAGE = 2 * W_HALF;       // keys' rows, values' rows
-    static constexpr int NST = R == 512 ? 3 : 4;
+    static constexpr uint32_t W_STAGE = 128 * 128;        // this CTA's 128 weight rows x 64 columns
+    static constexpr int NST = 6;
     static constexpr uint32_t OFF_W = A_BYTES;
     static constexpr uint32_t OFF_MISC = OFF_W + NST * W_STAGE;
     static constexpr uint32_t BYTES = OFF_MISC + 1024 + 1024;
@@ -46,7 +48,7 @@ struct ExpandSmem {
 
 struct ExpandMisc {
     uint64_t a_full, a_empty, mma_done;
-    uint64_t w_full[4], w_empty[4];
+    uint64_t w_full[6], w_empty[6];
     uint64_t acc_full[2], acc_free[2];
     int64_t scan[8];
     WalkStart start;
@@ -115,16 +117,18 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
     const int rank = (int)cluster_rank(), c = blockIdx.x >> 1, nc = a.grid >> 1;  // cluster, clusters
 
     if (threadIdx.x == 0) {
-        mbar_init(&ms.a_full, 1);
+        // Those the issuer waits for (a_full, w_full, acc_free) are used in the even CTA only and
+        // signalled by both; the others are signalled by the issuer in both.
+        mbar_init(&ms.a_full, 2);
         mbar_init(&ms.a_empty, 1);
         mbar_init(&ms.mma_done, 1);
         for (int i = 0; i < NST; ++i) {
             mbar_init(&ms.w_full[i], 1);
-            mbar_init(&ms.w_empty[i], 2);  // both CTAs' products have read the stage
+            mbar_init(&ms.w_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms.acc_full[i], 1);
-            mbar_init(&ms.acc_free[i], 4);
+            mbar_init(&ms.acc_free[i], 8);
         }
         ms.abort_flag = 0;
         fence_barrier_init();
@@ -134,7 +138,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
         tma_prefetch_desc(&wk_map);
         tma_prefetch_desc(&wv_map);
     }
-    if (warp == 1) tmem_alloc(&ms.tmem_slot, 512);
+    if (warp == 1) tmem_alloc_pair(&ms.tmem_slot, 512);
     pdl_wait();
     pdl_trigger();
     const SeqBatch sb{a.query_start_loc, a.context_lens, a.num_seqs, a.total_q,
@@ -168,35 +172,42 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
         // ------------------------------ TMA producer ------------------------------
         const uint64_t policy = l2_policy_evict_normal();
         const CUtensorMap *w_map = rank == 0 ? &wk_map : &wv_map;
+        const uint32_t a_full = smem_of_cta(&ms.a_full, 0), w_full0 = smem_of_cta(&ms.w_full[0], 0);
         uint32_t st = 0, ph = 0, fill = 0, aloads = 0;
         int64_t p = quotient(lo, H);
         int h = (int)(lo - p * H);
         for (int64_t f = lo; f < hi && ok; ++f) {
             const int64_t g = 2 * p + rank;
-            if ((f == lo || h == 0) && g < NT) {
-                w.seek(sb, units, g);
-                // the tile's boxes (blocks, or 32 tokens of a larger one), one a lane, at most 16
-                const int bshift = min(a.block_shift, 5);
-                const int64_t t0 = (g - w.pre) * kExpTile;
-                const int boxes = (int)((min64(kExpTile, w.q.ctx - t0) + (1 << bshift) - 1) >> bshift);
-                const int box_bytes = L::GROUP << (bshift - 3);
-                int bid = -1;
-                if (lane < boxes) {
-                    bid = a.block_tables[(int64_t)w.s * a.max_blocks_per_seq +
-                                         ((t0 + ((int64_t)lane << bshift)) >> a.block_shift)];
-                    if (bid < 0 || bid >= a.num_blocks) {
-                        flag_error(a.err, PKV_DEVERR_BLOCK_ID);
-                        bid = -1;  // an out-of-range box is filled with zeros
-                    }
-                }
+            if (f == lo || h == 0) {
                 ok = aloads == 0 || wait_all(&ms.a_empty, (aloads - 1) & 1);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&ms.a_full, boxes * box_bytes);
+                int boxes = 0;
+                if (g < NT) {
+                    w.seek(sb, units, g);
+                    // the tile's boxes (blocks, or 32 tokens of a larger one), one a lane, at most 16
+                    const int bshift = min(a.block_shift, 5);
+                    const int64_t t0 = (g - w.pre) * kExpTile;
+                    boxes = (int)((min64(kExpTile, w.q.ctx - t0) + (1 << bshift) - 1) >> bshift);
+                    const int box_bytes = L::GROUP << (bshift - 3);
+                    int bid = -1;
+                    if (lane < boxes) {
+                        bid = a.block_tables[(int64_t)w.s * a.max_blocks_per_seq +
+                                             ((t0 + ((int64_t)lane << bshift)) >> a.block_shift)];
+                        if (bid < 0 || bid >= a.num_blocks) {
+                            flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+                            bid = -1;  // an out-of-range box is filled with zeros
+                        }
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx_cluster(a_full, boxes * box_bytes);
 #pragma unroll 1
-                for (int i = 0; i < boxes; ++i) {
-                    const int id = __shfl_sync(0xffffffffu, bid, i);
-                    const int grp = ((i << bshift) & ((1 << a.block_shift) - 1)) >> 3;  // (a tile starts a block)
-                    if (lane == 0) tma_load_5d(sA + i * box_bytes, &kv_map, &ms.a_full, 0, 0, 0, grp, id, policy);
+                    for (int i = 0; i < boxes; ++i) {
+                        const int id = __shfl_sync(0xffffffffu, bid, i);
+                        const int grp = ((i << bshift) & ((1 << a.block_shift) - 1)) >> 3;  // (a tile starts a block)
+                        if (lane == 0)
+                            tma_load_5d_pair(smem_u32(sA) + i * box_bytes, &kv_map, a_full, 0, 0, 0, grp, id, policy);
+                    }
+                } else if (lane == 0) {
+                    mbar_arrive_cluster(a_full);  // no tile of its own: nothing to load
                 }
                 ++aloads;
             }
@@ -205,10 +216,9 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
                 for (int kc = 0; kc < KCH; ++kc) {
                     ok = mbar_wait(&ms.w_empty[st], ph ^ 1, abort_flag, a.wait_ns);
                     if (!ok) break;
-                    // both halves land here: this CTA's own and the other one's
-                    mbar_arrive_expect_tx(&ms.w_full[st], L::W_STAGE);
-                    tma_load_2d_multicast(sW + st * L::W_STAGE + rank * L::W_HALF, w_map, &ms.w_full[st], kc * 64,
-                                          h * kExpHeadDim, 3, policy);
+                    if (rank == 0) mbar_arrive_expect_tx(&ms.w_full[st], 2 * L::W_STAGE);  // both CTAs' halves
+                    tma_load_2d_pair(smem_u32(sW) + st * L::W_STAGE, w_map, w_full0 + st * 8, kc * 64, h * kExpHeadDim,
+                                     policy);
                     ++fill;
                     if (++st == NST) { st = 0; ph ^= 1; }
                 }
@@ -218,32 +228,40 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
         }
         if (lane == 0) {
             const uint32_t pending = minu32(fill, NST);
-            if (ok) {
-                // the other CTA's last arrivals at this one's barriers come before it ends
-                for (uint32_t k = fill - pending; k < fill && ok; ++k)
-                    ok = mbar_wait(&ms.w_empty[k % NST], (k / NST) & 1, abort_flag, a.wait_ns);
-            }
+            // The issuer's last arrivals at this CTA's barriers come before it ends; with them the copies
+            // have landed, for the products read them.
+            for (uint32_t k = fill - pending; k < fill && ok; ++k)
+                ok = mbar_wait(&ms.w_empty[k % NST], (k / NST) & 1, abort_flag, a.wait_ns);
+            if (ok && aloads > 0) ok = mbar_wait(&ms.a_empty, (aloads - 1) & 1, abort_flag, a.wait_ns);
             if (!ok) {
                 flag_error(a.err, PKV_DEVERR_TIMEOUT);
                 *abort_flag = 1;
-                // copies in flight land first
-                for (uint32_t k = fill - pending; k < fill; ++k) mbar_wait(&ms.w_full[k % NST], (k / NST) & 1, nullptr);
-                if (aloads > 0) mbar_wait(&ms.a_full, (aloads - 1) & 1, nullptr);
+                // copies in flight land first; their barriers are in the even CTA
+                if (rank == 0) {
+                    for (uint32_t k = fill - pending; k < fill; ++k)
+                        mbar_wait(&ms.w_full[k % NST], (k / NST) & 1, nullptr);
+                    if (aloads > 0) mbar_wait(&ms.a_full, (aloads - 1) & 1, nullptr);
+                } else {
+                    const uint64_t t0 = globaltimer_ns();
+                    while (globaltimer_ns() - t0 < 1000000) {
+                    }
+                }
             }
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
-        // A CTA without a tile of its own (the last pair of an odd count) multiplies whatever its
-        // shared memory holds, so that the stages go on in step; nothing of it is stored.
-        constexpr uint32_t IDESC = umma_idesc_bf16(kExpTile, 256, 0, 0);
+        // The even CTA issues for both.  Where the odd one has no tile of its own (the last pair of
+        // an odd count) the products run over whatever its shared memory holds; nothing of them is
+        // stored.
+        constexpr uint32_t IDESC = umma_idesc_bf16(2 * kExpTile, 256, 0, 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t da = umma_desc_sw128(smem_u32(sA), 16, L::GROUP);
         const uint64_t dw0 = umma_desc_sw128(smem_u32(sW), 16, 1024);
         uint32_t st = 0, ph = 0, n = 0, atiles = 0;
         int64_t p = quotient(lo, H);
         int h = (int)(lo - p * H);
-        for (int64_t f = lo; f < hi && ok; ++f, ++n) {
-            if ((f == lo || h == 0) && 2 * p + rank < NT) {
+        for (int64_t f = lo; f < hi && ok && rank == 0; ++f, ++n) {
+            if (f == lo || h == 0) {
                 if (!wait_all(&ms.a_full, atiles & 1)) { ok = false; break; }
                 ++atiles;
             }
@@ -254,15 +272,15 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
                 const uint64_t dw = dw0 + st * (L::W_STAGE >> 4);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    umma_bf16_warp(tm + (n & 1) * 256, da + ((kc * 1024 + ks * 32) >> 4), dw + ((ks * 32) >> 4), IDESC,
+                    umma2_bf16_warp(tm + (n & 1) * 256, da + ((kc * 1024 + ks * 32) >> 4), dw + ((ks * 32) >> 4), IDESC,
                                    kc > 0 || ks > 0);
-                umma_commit_multicast_warp(&ms.w_empty[st], 3);
+                umma2_commit_warp(&ms.w_empty[st], 3);
                 if (++st == NST) { st = 0; ph ^= 1; }
             }
             if (!ok) break;
-            umma_commit_warp(&ms.acc_full[n & 1]);
-            if (++h == H) {
-                umma_commit_warp(&ms.a_empty);
+            umma2_commit_warp(&ms.acc_full[n & 1], 3);
+            if (++h == H || f + 1 == hi) umma2_commit_warp(&ms.a_empty, 3);
+            if (h == H) {
                 h = 0;
                 ++p;
             }
@@ -271,13 +289,16 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
             if (lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
             *abort_flag = 1;
         }
-        umma_commit_warp(&ms.mma_done);  // every MMA is done before TMEM is released
-        mbar_wait(&ms.mma_done, 0, nullptr);
+        if (rank == 0) {  // every MMA is done before TMEM is released
+            umma2_commit_warp(&ms.mma_done, 1);
+            mbar_wait(&ms.mma_done, 0, nullptr);
+        }
         __syncwarp();
     } else {
         // ------------- epilogue: one token a thread, 32 bytes a store -------------
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
+        const uint32_t acc_free0 = smem_of_cta(&ms.acc_free[0], 0);
         uint32_t n = 0;
         int64_t p = quotient(lo, H);
         int h = (int)(lo - p * H);
@@ -321,7 +342,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ms.acc_free[n & 1]);
+            if (lane == 0) mbar_arrive_cluster(acc_free0 + (n & 1) * 8);
             if (++h == H) { h = 0; ++p; }
         }
         if (!ok) {
@@ -333,7 +354,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
     tc_fence_before();
     cluster_barrier();  // the other CTA signals and fills this one's shared memory up to here
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 512);
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
 template <int R>

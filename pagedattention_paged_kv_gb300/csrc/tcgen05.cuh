@@ -78,21 +78,53 @@ __device__ __forceinline__ void umma_commit_warp(uint64_t *bar) {
         : "memory");
 }
 
-// umma_commit_warp that arrives on the barrier at `bar`'s place in every CTA of cta_mask.
-__device__ __forceinline__ void umma_commit_multicast_warp(uint64_t *bar, uint16_t cta_mask) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
-        ::"r"(smem_u32(bar)), "h"(cta_mask)
-        : "memory");
-}
-
 // A descriptor moved by `bytes`, passed through a shuffle: the compiler then holds it in uniform
 // registers, where an offset worked out per thread costs each MMA of a warp-wide issuer some 40 cycles.
 __device__ __forceinline__ uint64_t umma_desc_at(uint64_t base, uint32_t bytes) {
     const uint32_t lo = __shfl_sync(0xffffffffu, (uint32_t)base + (bytes >> 4), 0);
     return (base & 0xffffffff00000000ull) | lo;
+}
+
+// The CTA pair's forms (cta_group::2; the CTAs of a cluster of two).  One MMA works on both CTAs' shared
+// memory and TMEM: M = 256 puts A's and D's first 128 rows on the even CTA and the others on the
+// odd one, and each holds half of B's N rows; descriptors and TMEM addresses are offsets common to
+// both.  The even CTA issues; commits arrive on the barrier's place in every CTA of cta_mask.
+__device__ __forceinline__ void umma2_bf16_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma2_bf16_tmem_a_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                       uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma2_commit_warp(uint64_t *bar, uint16_t cta_mask) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+        ::"r"(smem_u32(bar)), "h"(cta_mask)
+        : "memory");
+}
+// Both CTAs' allocating warps call these.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t base, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
 }
 
 // Whole-warp TMEM allocation of `cols` columns; the base address lands in *slot.
