@@ -189,18 +189,16 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         // The merge job of the boundary before this CTA's share: the item split there, when that
         // is its first split.
         if (threadIdx.x == 64) {
-            LatentJob j{0, 0, 0, -1, -1, 0, 0};
+            LatentJob j{0, -1, -1, 0, 0};
             if (works && c > 0) {
                 const SeqInfo q = ms.start.q;
                 const int64_t nk = (q.ctx + kLatentTile - 1) / kLatentTile;
                 const int64_t grp = quotient(lo - ms.start.pre, nk), begin = ms.start.pre + grp * nk;
                 if (begin != lo && begin >= quotient((c - 1) * T, ge)) {
-                    j.item_begin = begin;
-                    j.total_units = T;
                     j.out_off = ((int64_t)q.q0 * a.num_heads + grp * kLatentRows) * R;
                     j.c0 = c - 1;
                     j.c1 = share_owner(begin + nk - 1, T, ge);
-                    j.ge = ge;
+                    j.first = part_slot(c - 1, begin, T, ge);
                     j.rows = (int)min64(kLatentRows, (int64_t)q.q_len * a.num_heads - grp * kLatentRows);
                 }
             }
@@ -638,7 +636,7 @@ static cudaError_t launch_absorbed(const CUtensorMap &q_map, const CUtensorMap &
     e = launch_pdl(latent_absorbed_kernel<R>, dim3(a.grid), dim3(kAbsorbedThreads), AbsorbedSmem<R>::BYTES, stream,
                    q_map, kv_map, a);
     if (e != cudaSuccess) return e;
-    return launch_latent_merge<R, kLatentRows>(a.ws_jobs, a.ws_ml, a.ws_o, a.out, R, a.grid, stream);
+    return launch_latent_merge<R, kLatentRows, false>(a.ws_jobs, a.ws_ml, a.ws_o, a.out, R, a.grid, stream);
 }
 
 cudaError_t launch_latent_absorbed(int latent_dim, const CUtensorMap &q_map, const CUtensorMap &kv_map,

@@ -201,17 +201,15 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
 
     // The merge job of the boundary before this CTA's share (see latent_absorbed.cu).
     if (threadIdx.x == 0) {
-        LatentJob j{0, 0, 0, -1, -1, 0, 0};
+        LatentJob j{0, -1, -1, 0, 0};
         if (works && c > 0) {
             const SeqInfo q = ms.start.q;
             const ExpandedSegment g = expanded_segment(q, a.causal, ms.start.pre, lo, hi);
             if (g.kb != 0 && g.tile_begin >= share_begin(c - 1, T, ge)) {
-                j.item_begin = g.tile_begin;
-                j.total_units = T;
                 j.out_off = ((q.q0 + g.qt * kExpQTile) * a.num_heads + g.h) * kExpHeadDim;
                 j.c0 = c - 1;
                 j.c1 = share_owner(g.tile_begin + ExpandedTiles(q, a.causal).chunks(g.qt) - 1, T, ge);
-                j.ge = ge;
+                j.first = part_slot(c - 1, g.tile_begin, T, ge);
                 j.rows = g.tokens;
             }
         }
@@ -621,7 +619,7 @@ cudaError_t launch_latent_expanded(const CUtensorMap &q_map, const CUtensorMap &
     e = launch_pdl(latent_expanded_kernel, dim3(a.grid), dim3(kExpandedThreads), ExpandedSmem::BYTES, stream, q_map,
                    kv_map, rope_map, a);
     if (e != cudaSuccess) return e;
-    return launch_latent_merge<kExpHeadDim, kExpQTile>(a.ws_jobs, a.ws_ml, a.ws_o, a.out,
+    return launch_latent_merge<kExpHeadDim, kExpQTile, true>(a.ws_jobs, a.ws_ml, a.ws_o, a.out,
                                                        (int64_t)a.num_heads * kExpHeadDim, a.grid, stream);
 }
 

@@ -12,22 +12,23 @@
 #pragma once
 
 #include "attn_block.cuh"
-#include "pkv_split.cuh"
 
 namespace pkv {
 
 // An item whose units lie in the shares of CTAs c0 .. c1 (c0 < 0: none); written by CTA c0 + 1,
 // whose share begins inside it.
 struct LatentJob {
-    int64_t item_begin, total_units;  // first unit; units of the batch
-    int64_t out_off;                  // element of out at which the item's first row begins
-    int32_t c0, c1, ge, rows;
+    int64_t out_off;  // element of out at which the item's first row begins
+    int32_t c0, c1;
+    int32_t first;    // slot of c0's part; CTAs c > c0 begin inside the item, their parts are in slots 2 c
+    int32_t rows;
 };
 
 constexpr int kJoinRows = 2;
 
-// Parts lie as [2 * grid][SLOT_ROWS] (m, l) and [2 * grid][SLOT_ROWS][D] o.
-template <int D, int SLOT_ROWS>
+// Parts lie as [2 * grid][SLOT_ROWS] (m, l) and [2 * grid][SLOT_ROWS][D] o.  BARE: a part that
+// saw nothing of a row (m = -inf) need not have left an output there.
+template <int D, int SLOT_ROWS, bool BARE>
 __global__ void __launch_bounds__(256, 3)
 latent_merge_kernel(const LatentJob *jobs, const float2 *ws_ml, const float *ws_o, __nv_bfloat16 *out,
                     int64_t out_stride) {
@@ -51,7 +52,8 @@ latent_merge_kernel(const LatentJob *jobs, const float2 *ws_ml, const float *ws_
         float4 o[U][kJoinRows];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t slot = part_slot(j.c0 + min(p0 + u, nparts - 1), j.item_begin, j.total_units, j.ge);
+            const int p = min(p0 + u, nparts - 1);
+            const int64_t slot = p == 0 ? j.first : 2 * (j.c0 + p);
 #pragma unroll
             for (int k = 0; k < kJoinRows; ++k) {
                 const int row = row0 + k * SETS;
@@ -60,8 +62,7 @@ latent_merge_kernel(const LatentJob *jobs, const float2 *ws_ml, const float *ws_
                 if (p0 + u < nparts && row < j.rows) {
                     ml[u][k] = __ldcg(ws_ml + slot * SLOT_ROWS + row);
                     o[u][k] = __ldcg(reinterpret_cast<const float4 *>(ws_o + (slot * SLOT_ROWS + row) * D) + cg);
-                    // a part that saw nothing of the row need not have left an output
-                    if (ml[u][k].x == -INFINITY) o[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (BARE && ml[u][k].x == -INFINITY) o[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 }
             }
         }
@@ -100,11 +101,11 @@ latent_merge_kernel(const LatentJob *jobs, const float2 *ws_ml, const float *ws_
     }
 }
 
-template <int D, int SLOT_ROWS>
+template <int D, int SLOT_ROWS, bool BARE>
 cudaError_t launch_latent_merge(const LatentJob *jobs, const float2 *ws_ml, const float *ws_o, __nv_bfloat16 *out,
                                 int64_t out_stride, int grid, cudaStream_t stream) {
     constexpr int per = 256 / (D / 4) * kJoinRows;
-    return launch_pdl(latent_merge_kernel<D, SLOT_ROWS>, dim3(grid, SLOT_ROWS / per), dim3(256), 0, stream, jobs,
+    return launch_pdl(latent_merge_kernel<D, SLOT_ROWS, BARE>, dim3(grid, SLOT_ROWS / per), dim3(256), 0, stream, jobs,
                       ws_ml, ws_o, out, out_stride);
 }
 
