@@ -353,7 +353,8 @@ int pkv_step_metadata(int32_t *block_tables, int32_t *context_lens, int32_t *que
  * slot becomes [latent[t] ; rope[t]] (latent [num_tokens, latent_dim], rope [num_tokens,
  * rope_dim], bf16).  Bit-exact; negative slots are skipped, slots outside the pool skipped and
  * flagged PKV_DEVERR_SLOT; two tokens with the same slot race.
- * Supported: dtype PKV_DTYPE_BF16, latent_dim and rope_dim multiples of 8, at most 65536.
+ * Supported: dtype PKV_DTYPE_BF16, latent_dim and rope_dim multiples of 8, at most 65536,
+ * num_blocks < 2^31.
  */
 int pkv_latent_cache_write(void *latent_cache, const void *latent, const void *rope,
                            const int64_t *slot_mapping, int64_t num_tokens, int64_t num_blocks, int block_size,
@@ -370,8 +371,9 @@ int pkv_latent_cache_write(void *latent_cache, const void *latent, const void *r
  * 0 gives a zero row.  Otherwise sequence s owns rows query_start_loc[s] ..
  * query_start_loc[s + 1] - 1, its last q_len positions (verification of drafted tokens, short
  * chunks), masked as in pkv_paged_attention_varlen; a sequence whose metadata is bad gets zero
- * rows, and rows behind query_start_loc[num_seqs] are left as they were.  Cache rows at or past
- * a context are never read as values.  The softmax weights are rounded to bf16 for the product
+ * rows, and rows behind query_start_loc[num_seqs] are left as they were.  What the cache holds
+ * at or past a context has no effect; a row inside the context that is not finite makes every
+ * row of that sequence not finite, also those the causal mask hides it from.  The softmax weights are rounded to bf16 for the product
  * with the latents; sums are fp32.
  * Supported: dtype PKV_DTYPE_BF16, latent_dim 256 or 512, rope_dim 64, block_size 8, 16, 32 or
  * 64, any num_heads with total_q_tokens * num_heads < 2^31 - 128, 0 < scale < infinity.

@@ -295,8 +295,9 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             *abort_flag = 1;
             // copies in flight land before the shared memory is given back
             const uint32_t issued = (fill + 1) / 2, pending = minu32(issued, NST);  // fill counts halves
-            for (uint32_t k = issued - pending; k < issued; ++k) mbar_wait(&ms.kv_full[k % NST], (k / NST) & 1, nullptr);
-            if (qloads > 0) mbar_wait(&ms.q_full, (qloads - 1) & 1, nullptr);
+            for (uint32_t k = issued - pending; k < issued; ++k)
+                mbar_wait(&ms.kv_full[k % NST], (k / NST) & 1, nullptr, kCopyLandsNs);
+            if (qloads > 0) mbar_wait(&ms.q_full, (qloads - 1) & 1, nullptr, kCopyLandsNs);
         }
     } else if (warp == 1) {
         // ------------------------------ QK issuer ------------------------------
@@ -405,7 +406,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         const int tid = threadIdx.x - 64;
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t tO = tl + L::COL_O;
-        // S is read 16 lanes at a time over all 32 threads (tmem_ld_16x64): this thread has rows
+        // S is read 16 lanes at a time over all 32 threads (tmem_ld_16x32): this thread has rows
         // ra and ra + 8, a quarter of the columns of each.
         const int ra = quarter * 16 + (lane >> 2);
         const int c0 = 2 * (lane & 3);

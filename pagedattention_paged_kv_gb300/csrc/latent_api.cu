@@ -40,6 +40,12 @@ int check_latent(int num_seqs, int total_q, int max_blocks_per_seq, int num_head
     return PKV_OK;
 }
 
+// Whether the expanded rows of a batch can be addressed.
+bool expanded_fits(int num_seqs, int64_t total_context, int num_heads) {
+    return total_context <= INT32_MAX &&
+           total_context + (int64_t)num_seqs * (pkv::kExpTile - 1) <= ((int64_t)INT32_MAX / 4 - 128) / num_heads;
+}
+
 // The cache as (64 columns, token in group, 64-column chunk, group of 8 tokens, block): a box of
 // one block (at most 32 tokens of it) x box_chunks chunks lands as [group][chunk][8 tokens][64 columns].
 int encode_latent_map(CUtensorMap *map, const void *cache, int64_t num_blocks, int block_size, int row_cols,
@@ -99,7 +105,7 @@ extern "C" int pkv_latent_cache_write(void *latent_cache, const void *latent, co
     if (num_tokens < 0 || num_blocks < 0 || block_size <= 0 || latent_dim <= 0 || rope_dim <= 0)
         return PKV_ERR_INVALID_ARG;
     if (dtype != PKV_DTYPE_BF16 || latent_dim % 8 != 0 || rope_dim % 8 != 0 || latent_dim > 65536 ||
-        rope_dim > 65536)
+        rope_dim > 65536 || num_blocks > INT32_MAX)
         return PKV_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PKV_OK;
     if (!latent_cache || !latent || !rope || !slot_mapping) return PKV_ERR_INVALID_ARG;
@@ -121,6 +127,7 @@ extern "C" size_t pkv_latent_workspace_size(int op, int num_seqs, int total_q_to
     if (check_latent(num_seqs, total_q_tokens, 0, num_heads, latent_dim, rope_dim, 16, 0, PKV_DTYPE_BF16) != PKV_OK ||
         total_context < 0)
         return 0;
+    if (op == PKV_OP_LATENT_EXPANDED && !expanded_fits(num_seqs, total_context, num_heads)) return 0;
     pkv::DeviceFacts d;
     if (pkv::current_device(&d) != PKV_OK) return 0;
     if (op == PKV_OP_LATENT_ABSORBED) {
@@ -131,7 +138,6 @@ extern "C" size_t pkv_latent_workspace_size(int op, int num_seqs, int total_q_to
     if (op == PKV_OP_LATENT_EXPANDED) {
         pkv::ExpandedPlan p;
         pkv::plan_expanded(num_seqs, total_context, num_heads, d.sms, &p);
-        if (p.padded * num_heads > (int64_t)INT32_MAX / 4 - 128) return 0;
         return p.ws_bytes;
     }
     return 0;
@@ -206,7 +212,9 @@ extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int
     if (st != PKV_OK) return st;
     if (total_context < 0 || nope_dim <= 0 || v_dim <= 0 || !(scale > 0.f) || scale == INFINITY)
         return PKV_ERR_INVALID_ARG;
-    if (nope_dim != pkv::kExpHeadDim || v_dim != pkv::kExpHeadDim) return PKV_ERR_UNSUPPORTED;
+    if (nope_dim != pkv::kExpHeadDim || v_dim != pkv::kExpHeadDim ||
+        !expanded_fits(num_seqs, total_context, num_heads))
+        return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0 || total_q_tokens == 0) return PKV_OK;
     if (!out || !q || !query_start_loc || !latent_cache || !block_tables || !context_lens || !w_k || !w_v)
         return PKV_ERR_INVALID_ARG;
@@ -219,7 +227,6 @@ extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int
     if (st != PKV_OK) return st;
     pkv::ExpandedPlan p;
     pkv::plan_expanded(num_seqs, total_context, num_heads, d.sms, &p);
-    if (p.padded * num_heads > (int64_t)INT32_MAX / 4 - 128) return PKV_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < p.ws_bytes) return PKV_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned_to(workspace, 256)) return PKV_ERR_INVALID_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);

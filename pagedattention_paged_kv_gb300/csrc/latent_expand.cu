@@ -239,11 +239,11 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
                 // copies in flight land first; their barriers are in the even CTA
                 if (rank == 0) {
                     for (uint32_t k = fill - pending; k < fill; ++k)
-                        mbar_wait(&ms.w_full[k % NST], (k / NST) & 1, nullptr);
-                    if (aloads > 0) mbar_wait(&ms.a_full, (aloads - 1) & 1, nullptr);
+                        mbar_wait(&ms.w_full[k % NST], (k / NST) & 1, nullptr, kCopyLandsNs);
+                    if (aloads > 0) mbar_wait(&ms.a_full, (aloads - 1) & 1, nullptr, kCopyLandsNs);
                 } else {
                     const uint64_t t0 = globaltimer_ns();
-                    while (globaltimer_ns() - t0 < 1000000) {
+                    while (globaltimer_ns() - t0 < kCopyLandsNs) {
                     }
                 }
             }

@@ -243,7 +243,8 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         // The warp runs it together on uniform values; one elected lane issues.
         const uint64_t policy = l2_policy_evict_normal();
         const uint32_t pairs0 = smem_u32(sPairs), rope0 = smem_u32(sRope);
-        uint32_t n = 0, segs = 0;  // chunks (keys) and tiles issued
+        uint32_t n = 0, segs = 0;   // chunks and tiles issued
+        uint32_t np = 0, nr = 0;    // pairs and rotary pieces issued
         // pair i = 2 chunk (keys) or 2 chunk + 1 (values) of the CTA
         const int pitch = (int)a.buf.padded;  // rows from a piece to the next
         auto load_pair = [&](uint32_t i, int row) -> bool {
@@ -252,6 +253,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             mbar_arrive_expect_tx_warp(&ms.full[at], L::PAIR);
             tma_load_2d_warp(pairs0 + at * L::PAIR, &kv_map, &ms.full[at], 0, row, policy);
             tma_load_2d_warp(pairs0 + at * L::PAIR + L::PIECE, &kv_map, &ms.full[at], 0, row + pitch, policy);
+            ++np;
             return true;
         };
         int64_t tiles = ms.start_tiles;
@@ -287,6 +289,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 if (n >= 2 && !wait_all(&ms.rope_empty[n & 1], ((n >> 1) - 1) & 1)) { ok = false; break; }
                 mbar_arrive_expect_tx_warp(&ms.rope_full[n & 1], L::PIECE);
                 tma_load_2d_warp(rope0 + (n & 1) * L::PIECE, &rope_map, &ms.rope_full[n & 1], 0, key, policy);
+                ++nr;
                 if (!load_pair(2 * n + 1, row + 2 * pitch)) { ok = false; break; }
                 key += kExpTile;
                 row += kExpTile;
@@ -299,12 +302,11 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             flag_error(a.err, PKV_DEVERR_TIMEOUT);
             *abort_flag = 1;
             // copies in flight land first
-            for (uint32_t k = n > 2 ? n - 2 : 0; k < n; ++k) {
-                mbar_wait(&ms.full[2 * k % 3], (2 * k / 3) & 1, nullptr);
-                mbar_wait(&ms.full[(2 * k + 1) % 3], ((2 * k + 1) / 3) & 1, nullptr);
-                mbar_wait(&ms.rope_full[k & 1], (k >> 1) & 1, nullptr);
-            }
-            if (segs > 0) mbar_wait(&ms.q_full, (segs - 1) & 1, nullptr);
+            for (uint32_t i = np > 3 ? np - 3 : 0; i < np; ++i)
+                mbar_wait(&ms.full[i % 3], (i / 3) & 1, nullptr, kCopyLandsNs);
+            for (uint32_t i = nr > 2 ? nr - 2 : 0; i < nr; ++i)
+                mbar_wait(&ms.rope_full[i & 1], (i >> 1) & 1, nullptr, kCopyLandsNs);
+            if (segs > 0) mbar_wait(&ms.q_full, (segs - 1) & 1, nullptr, kCopyLandsNs);
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
