@@ -175,12 +175,12 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     const SeqBatch sb{a.query_start_loc, a.context_lens, a.num_seqs, a.total_q,
                       (int64_t)a.max_blocks_per_seq << a.block_shift, a.err};
     const AbsorbedUnits units{a.num_heads};
-    const BatchScan sc = scan_batch(sb, units, ms.scan, c == 0);
-    const int64_t T = sc.total;
+    const auto sc = scan_batch<kAbsorbedThreads>(sb, ms.scan, c == 0, units);
+    const int64_t T = sc.total[0];
     const int ge = split_ctas(T, a.grid, kMinTilesPerCta);
     const bool works = T > 0 && c < ge;
     const int64_t lo = works ? quotient(c * T, ge) : 0, hi = works ? quotient((c + 1) * T, ge) : 0;
-    if (works) find_unit(sb, units, sc, lo, &ms.start);
+    if (works) find_unit(sb, units, sc, 0, lo, &ms.start);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -217,7 +217,8 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         return;
     }
     SeqWalk<AbsorbedUnits> w;
-    w.start(sb, ms.start);
+    w.start(ms.start);
+    if (warp != 0) w.ahead(sb);  // the producer is on the critical path
 
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
@@ -287,6 +288,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                     ++fill;
                 }
                 if (++st == NST) { st = 0; ph ^= 1; }
+                w.ahead(sb);
             }
             f += g.tiles;
         }

@@ -144,17 +144,17 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
     const SeqBatch sb{a.query_start_loc, a.context_lens, a.num_seqs, a.total_q,
                       (int64_t)a.max_blocks_per_seq << a.block_shift, a.err};
     const ExpandUnits units{};
-    const BatchScan sc = scan_batch(sb, units, ms.scan, blockIdx.x == 0);
+    const auto sc = scan_batch<kExpandThreads>(sb, ms.scan, blockIdx.x == 0, units);
     // A batch with more tokens than the caller counted is refused whole; the attention kernel
     // sees the same sum and writes zero rows.
-    const int64_t NT = sc.total <= a.buf.padded / kExpTile ? sc.total : 0;
-    if (blockIdx.x == 0 && NT != sc.total && threadIdx.x == 0) flag_error(a.err, PKV_DEVERR_CONTEXT_LEN);
+    const int64_t NT = sc.total[0] <= a.buf.padded / kExpTile ? sc.total[0] : 0;
+    if (blockIdx.x == 0 && NT != sc.total[0] && threadIdx.x == 0) flag_error(a.err, PKV_DEVERR_CONTEXT_LEN);
     const int64_t T = (NT + 1) / 2 * H;  // (pair, head) units
     const int ge = split_ctas(T, nc, 1);
     const bool works = T > 0 && c < ge;
     const int64_t lo = works ? quotient(c * T, ge) : 0, hi = works ? quotient((c + 1) * T, ge) : 0;
     const int64_t g0 = 2 * quotient(lo, H) + rank;  // this CTA's first token tile
-    if (works) find_unit(sb, units, sc, g0, &ms.start);
+    if (works) find_unit(sb, units, sc, 0, g0, &ms.start);
     tc_fence_before();
     cluster_barrier();  // the barriers of both CTAs are there before either is signalled
     tc_fence_after();
@@ -164,7 +164,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
     };
     bool ok = true;
     SeqWalk<ExpandUnits> w;
-    if (works && g0 < NT) w.start(sb, ms.start);  // (ms.start is written for these only)
+    if (works && g0 < NT) w.start(ms.start);  // (ms.start is written for these only)
 
     if (!works) {
         // nothing to do but to meet the other CTA at the end
@@ -224,6 +224,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (g < NT) w.ahead(sb);
             if (++h == H) { h = 0; ++p; }
         }
         if (lane == 0) {

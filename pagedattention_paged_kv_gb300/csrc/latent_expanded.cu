@@ -55,7 +55,7 @@ struct ExpandedMisc {
     uint64_t q_full, q_empty, mma_done;
     uint64_t full[3], empty[3], rope_full[2], rope_empty[2];
     uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
-    int64_t scan[16];
+    int64_t scan[2 * kExpandedThreads / 32];
     WalkStart start;
     int64_t start_tiles;
     uint32_t tmem_slot;
@@ -120,7 +120,7 @@ __device__ __forceinline__ ExpandedSegment expanded_segment(const SeqInfo &q, bo
     ExpandedSegment g;
     const ExpandedTiles t(q, causal);
     const int64_t ph = t.per_head(), o = f - pre;
-    g.h = (int)(o / ph);
+    g.h = (int)quotient(o, ph);
     const int64_t o1 = o - g.h * ph;
     g.qt = t.tile_of(o1);
     g.kb = (int)(o1 - t.before(g.qt));
@@ -181,58 +181,62 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     // inputs of the call may be read here; only what the expansion writes has to be waited for, and
     // only by the producer (CTAs without work wait too, so that this grid ends behind the last).
     pdl_trigger();
+    // A CTA of this kernel has the SM's shared memory, so no other holder of TMEM is there.
+    if (warp == 1) tmem_alloc(&ms.tmem_slot, 512);
     const SeqBatch sb{a.query_start_loc, a.context_lens, a.num_seqs, a.total_q, a.max_context, a.err};
     const ExpandedUnits units{a.num_heads, a.causal};
     // (the expansion kernel has reported bad sequences already)
-    const BatchScan st = scan_batch(sb, TokenTiles{}, ms.scan, false);
-    const bool fits = st.total <= a.buf.padded / kExpTile;
-    const BatchScan sc = scan_batch(sb, units, ms.scan, false);
-    const int64_t T = fits ? sc.total : 0;
+    const auto sc = scan_batch<kExpandedThreads>(sb, ms.scan, false, units, TokenTiles{});
+    const bool fits = sc.total[1] <= a.buf.padded / kExpTile;
+    const int64_t T = fits ? sc.total[0] : 0;
     const int ge = split_ctas(T, a.grid, 1);
     const bool works = T > 0 && c < ge;
     const int64_t lo = works ? quotient(c * T, ge) : 0, hi = works ? quotient((c + 1) * T, ge) : 0;
-    if (works && lo >= sc.run && lo < sc.run + sc.local) {
-        find_unit(sb, units, sc, lo, &ms.start);
-        int64_t tiles = st.run;  // expansion tiles before the sequence
-        for (int s = st.beg; s < ms.start.s; ++s) tiles += seq_units_of(sb, TokenTiles{}, s, false);
+    if (works && find_unit(sb, units, sc, 0, lo, &ms.start)) {
+        int64_t tiles = sc.run[1];  // expansion tiles before the sequence
+        SeqInfo q = sc.first;
+        for (int s = sc.beg; s < ms.start.s; q = read_seq(sb, ++s, false)) tiles += units_of(q, TokenTiles{});
         ms.start_tiles = tiles;
     }
-    __syncthreads();
-
-    // The merge job of the boundary before this CTA's share (see latent_absorbed.cu).
-    if (threadIdx.x == 0) {
-        LatentJob j{0, -1, -1, 0, 0};
-        if (works && c > 0) {
-            const SeqInfo q = ms.start.q;
-            const ExpandedSegment g = expanded_segment(q, a.causal, ms.start.pre, lo, hi);
-            if (g.kb != 0 && g.tile_begin >= share_begin(c - 1, T, ge)) {
-                j.out_off = ((q.q0 + g.qt * kExpQTile) * a.num_heads + g.h) * kExpHeadDim;
-                j.c0 = c - 1;
-                j.c1 = share_owner(g.tile_begin + ExpandedTiles(q, a.causal).chunks(g.qt) - 1, T, ge);
-                j.first = part_slot(c - 1, g.tile_begin, T, ge);
-                j.rows = g.tokens;
-            }
-        }
-        if (c > 0) a.ws_jobs[c - 1] = j;
-        if (c == a.grid - 1) {
-            j.c0 = -1;
-            a.ws_jobs[c] = j;
-        }
-    }
-    zero_dead_rows(sb, c, a.grid, a.out, (int64_t)a.num_heads * kExpHeadDim, warp,
-                   kExpandedThreads / 32, !fits);
-    if (!works) {
-        pdl_wait();
-        return;
-    }
-
-    if (warp == 1) tmem_alloc(&ms.tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ms.tmem_slot;
+
+    if (warp == 2 || warp == 3) {  // (these have nothing else to do)
+        // The merge job of the boundary before this CTA's share (see latent_absorbed.cu).
+        if (threadIdx.x == 64) {
+            LatentJob j{0, -1, -1, 0, 0};
+            if (works && c > 0) {
+                const SeqInfo q = ms.start.q;
+                const ExpandedSegment g = expanded_segment(q, a.causal, ms.start.pre, lo, hi);
+                if (g.kb != 0 && g.tile_begin >= share_begin(c - 1, T, ge)) {
+                    j.out_off = ((q.q0 + g.qt * kExpQTile) * a.num_heads + g.h) * kExpHeadDim;
+                    j.c0 = c - 1;
+                    j.c1 = share_owner(g.tile_begin + ExpandedTiles(q, a.causal).chunks(g.qt) - 1, T, ge);
+                    j.first = part_slot(c - 1, g.tile_begin, T, ge);
+                    j.rows = g.tokens;
+                }
+            }
+            if (c > 0) a.ws_jobs[c - 1] = j;
+            if (c == a.grid - 1) {
+                j.c0 = -1;
+                a.ws_jobs[c] = j;
+            }
+        }
+        __syncwarp();
+        zero_dead_rows(sb, c, a.grid, a.out, (int64_t)a.num_heads * kExpHeadDim, warp - 2, 2, !fits);
+    }
+    if (!works) {
+        __syncwarp();
+        if (warp == 1) tmem_dealloc(tmem, 512);
+        pdl_wait();
+        return;
+    }
+
     SeqWalk<ExpandedUnits> w;
-    w.start(sb, ms.start);
+    w.start(ms.start);
+    if (warp != 0) w.ahead(sb);  // the producer is on the critical path
     auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
     };
@@ -294,6 +298,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 key += kExpTile;
                 row += kExpTile;
                 ++n;
+                w.ahead(sb);
             }
             f += g.chunks;
         }

@@ -66,46 +66,69 @@ __device__ __forceinline__ SeqInfo read_seq(const SeqBatch &b, int s, bool repor
 
 // Units(const SeqInfo &) -> int64_t gives the work units of a live sequence.
 template <typename Units>
-__device__ __forceinline__ int64_t seq_units_of(const SeqBatch &b, const Units &units, int s, bool report) {
-    const SeqInfo q = read_seq(b, s, report);
+__device__ __forceinline__ int64_t units_of(const SeqInfo &q, const Units &units) {
     return q.q_len == 0 || q.dead ? 0 : units(q);
 }
 
-// The threads of a block take equal runs of consecutive sequences; run = units before this
-// thread's first one.
+// The threads of a block take equal runs of consecutive sequences; for each of K counts of units
+// run = units before this thread's first one.
+template <int K>
 struct BatchScan {
     int beg, end;
-    int64_t run, local, total;
+    SeqInfo first;  // of sequence beg, where there is one
+    int64_t run[K], local[K], total[K];
 };
 
-// Whole block; tmp holds one entry per warp.  Ends with __syncthreads.
-template <typename Units>
-__device__ __forceinline__ BatchScan scan_batch(const SeqBatch &b, const Units &units, int64_t *tmp,
-                                                bool report) {
-    BatchScan r;
-    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-    const int per = (b.num_seqs + nt - 1) / nt;
+// Whole block of NT threads; tmp holds NT / 32 entries a count and is not to be written again before
+// the next __syncthreads.  (Every CTA of a launch starts with it, and what the block's size, the
+// number of counts and the loads' independence leave to the compiler halved its time to 1,000 cycles.)
+template <int NT, typename... Units>
+__device__ __forceinline__ BatchScan<sizeof...(Units)> scan_batch(const SeqBatch &b, int64_t *tmp, bool report,
+                                                                  const Units &...units) {
+    constexpr int K = sizeof...(Units), NW = NT / 32;
+    BatchScan<K> r;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (b.num_seqs + NT - 1) / NT;
     r.beg = min(b.num_seqs, tid * per);
     r.end = min(b.num_seqs, r.beg + per);
-    r.local = 0;
-    for (int s = r.beg; s < r.end; ++s) r.local += seq_units_of(b, units, s, report);
-    int64_t x = r.local;
+    r.first.ctx = r.first.q0 = r.first.q_len = 0;
+    r.first.dead = false;
+    int64_t x[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) r.local[k] = 0;
+    for (int s = r.beg; s < r.end; ++s) {
+        const SeqInfo q = read_seq(b, s, report);
+        if (s == r.beg) r.first = q;
+        const int64_t u[K] = {units_of(q, units)...};
+#pragma unroll
+        for (int k = 0; k < K; ++k) r.local[k] += u[k];
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = r.local[k];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x[k], o);
+            if (lane >= o) x[k] += y;
+        }
     }
-    if (lane == 31) tmp[warp] = x;
+    if (lane == 31)
+#pragma unroll
+        for (int k = 0; k < K; ++k) tmp[k * NW + warp] = x[k];
     __syncthreads();
-    int64_t before = 0, total = 0;
-    for (int i = 0; i < nw; ++i) {
-        const int64_t v = tmp[i];
-        if (i < warp) before += v;
-        total += v;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        int64_t before = 0, total = 0;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            const int64_t v = tmp[k * NW + i];
+            if (i < warp) before += v;
+            total += v;
+        }
+        r.run[k] = before + x[k] - r.local[k];
+        r.total[k] = total;
     }
-    r.run = before + x - r.local;
-    r.total = total;
-    __syncthreads();
     return r;
 }
 
@@ -116,23 +139,25 @@ struct WalkStart {
     int s;
 };
 
-// The one thread whose run holds unit f writes *start.  Callers synchronise afterwards.
-template <typename Units>
-__device__ __forceinline__ void find_unit(const SeqBatch &b, const Units &units, const BatchScan &sc, int64_t f,
-                                          WalkStart *start) {
-    if (f < sc.run || f >= sc.run + sc.local) return;
-    int64_t run = sc.run;
-    for (int s = sc.beg; s < sc.end; ++s) {
-        const SeqInfo q = read_seq(b, s, false);
-        const int64_t u = q.q_len == 0 || q.dead ? 0 : units(q);
+// The one thread whose run holds unit f (of count k) writes *start.  Callers synchronise afterwards.
+template <int K, typename Units>
+__device__ __forceinline__ bool find_unit(const SeqBatch &b, const Units &units, const BatchScan<K> &sc, int k,
+                                          int64_t f, WalkStart *start) {
+    if (f < sc.run[k] || f >= sc.run[k] + sc.local[k]) return false;
+    int64_t run = sc.run[k];
+    SeqInfo q = sc.first;
+    for (int s = sc.beg;;) {
+        const int64_t u = units_of(q, units);
         if (f < run + u) {
             start->pre = run;
             start->units = u;
             start->q = q;
             start->s = s;
-            return;
+            return true;
         }
         run += u;
+        if (++s >= sc.end) return false;  // (not reached: the run's units are `local`)
+        q = read_seq(b, s, false);
     }
 }
 
@@ -150,7 +175,7 @@ struct SeqWalk {
     int64_t pre;       // units before it
     int64_t units;     // its units (> 0)
     SeqInfo q;
-    int base;          // sequence of lane 0
+    int base;          // sequence of lane 0 (below 0: nothing fetched yet)
     SeqRaw raw;        // this lane's sequence, not looked at yet (fresh) ...
     bool fresh;
     SeqInfo mine;      // ... and once it has been
@@ -177,19 +202,25 @@ struct SeqWalk {
         q.dead = false;
         units = __shfl_sync(0xffffffffu, my_units, l);
     }
-    // The loads of the sequences behind the first are under way from here on, and waited for by
-    // the first seek that needs them.
-    __device__ __forceinline__ void start(const SeqBatch &b, const WalkStart &st) {
+    __device__ __forceinline__ void start(const WalkStart &st) {
         s = st.s;
         pre = st.pre;
         units = st.units;
         q = st.q;
-        fetch(b, s);
+        base = -1;
+        fresh = false;
+        my_units = 0;
+    }
+    // The loads of the sequences behind the first are under way from here on.  (Not from start on:
+    // registers that a load fills are moved, and so waited for, before the first seek is over.)
+    __device__ __forceinline__ void ahead(const SeqBatch &b) {
+        if (base < 0) fetch(b, s);
     }
     // Moves on until the current sequence holds unit f (f >= pre, f below the batch's total).
     __device__ __forceinline__ void seek(const SeqBatch &b, const Units &u, int64_t f) {
         while (f >= pre + units) {
             pre += units;
+            ahead(b);
             look(b, u);
             const int at = s - base;
             unsigned later = __ballot_sync(0xffffffffu, my_units > 0) & (at >= 31 ? 0u : 0xffffffffu << (at + 1));
