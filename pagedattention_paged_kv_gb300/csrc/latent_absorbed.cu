@@ -42,7 +42,10 @@ namespace pkv {
 
 namespace {
 
-constexpr int kMinTilesPerCta = 2;
+// A small batch is spread until a CTA has one tile: its time is that of the longest chain, and a
+// second item's loads, products and output one behind the other cost more than a join (four
+// requests of up to 100 tokens, 16 heads: 9.2 us; with two tiles at least 15.9).
+constexpr int kMinTilesPerCta = 1;
 
 // A row's reference maximum moves, and O^T is rescaled, only when a tile's maximum exceeds it by
 // this much (log2 units).  bf16 weights and fp32 sums keep their relative precision up to 2^24
