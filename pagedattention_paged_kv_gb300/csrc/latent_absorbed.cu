@@ -103,7 +103,6 @@ struct AbsorbedUnits {
 
 // The part of one item that lies in the CTA's share.
 struct AbsorbedSegment {
-    int64_t item_begin;  // the item's first unit
     int64_t row0;        // its first query row (token * heads + head)
     int row_in_seq;      // the same, counted inside the sequence
     int rows;            // live rows, <= 64
@@ -118,7 +117,6 @@ __device__ __forceinline__ AbsorbedSegment segment_at(const AbsorbedArgs &a, con
     const int64_t o = f - pre;
     const int64_t grp = quotient(o, nk);
     g.kb = (int)(o - grp * nk);
-    g.item_begin = f - g.kb;
     g.tiles = (int)min64(nk - g.kb, hi - f);
     g.row_in_seq = (int)(grp * kLatentRows);
     g.row0 = (int64_t)q.q0 * a.num_heads + g.row_in_seq;
@@ -192,7 +190,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         // The merge job of the boundary before this CTA's share: the item split there, when that
         // is its first split.
         if (threadIdx.x == 64) {
-            LatentJob j{0, -1, -1, 0, 0};
+            LatentJob j{0, -1, -1, 0};
             if (works && c > 0) {
                 const SeqInfo q = ms.start.q;
                 const int64_t nk = (q.ctx + kLatentTile - 1) / kLatentTile;
@@ -201,7 +199,6 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                     j.out_off = ((int64_t)q.q0 * a.num_heads + grp * kLatentRows) * R;
                     j.c0 = c - 1;
                     j.c1 = share_owner(begin + nk - 1, T, ge);
-                    j.first = part_slot(c - 1, begin, T, ge);
                     j.rows = (int)min64(kLatentRows, (int64_t)q.q_len * a.num_heads - grp * kLatentRows);
                 }
             }
@@ -571,7 +568,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 if ((lane & 3) == 0) ms.inv[ra + 8 * k] = l[k] > 0.f ? 1.f / l[k] : 0.f;
             }
             if (!meet()) { ok = false; break; }
-            const int slot = g.whole ? 0 : part_slot(c, g.item_begin, T, ge);
+            const int slot = g.whole ? 0 : latent_slot(c, g.kb == 0);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
                 if (!g.whole && live[k] && (lane & 3) == 0)

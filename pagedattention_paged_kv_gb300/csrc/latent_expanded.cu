@@ -37,6 +37,8 @@ namespace pkv {
 
 namespace {
 
+constexpr int kSnap = 1;
+
 constexpr int kExpandedThreads = 384;  // loads, MMAs, two idle warps, two softmax warpgroups
 
 struct ExpandedSmem {
@@ -57,7 +59,7 @@ struct ExpandedMisc {
     uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
     int64_t scan[2 * kExpandedThreads / 32];
     WalkStart start;
-    int64_t start_tiles;
+    int64_t start_tiles, lo, hi;
     uint32_t tmem_slot;
     int abort_flag;
 };
@@ -134,6 +136,16 @@ __device__ __forceinline__ ExpandedSegment expanded_segment(const SeqInfo &q, bo
     return g;
 }
 
+// Where a share that would begin at unit f begins: the tile's begin or end if that is near, so that
+// short tiles are not cut.  (The sequence that holds f is given.)
+__device__ __forceinline__ int64_t snapped(const WalkStart &at, bool causal, int64_t f) {
+    const ExpandedTiles t(at.q, causal);
+    const int64_t ph = t.per_head(), o = f - at.pre;
+    const int64_t o1 = o - quotient(o, ph) * ph, qt = t.tile_of(o1);
+    const int64_t kb = o1 - t.before(qt), left = t.chunks(qt) - kb;
+    return kb <= kSnap ? f - kb : left <= kSnap ? f + left : f;
+}
+
 // Chunks of a segment that half h has to do with.
 __device__ __forceinline__ int half_chunks(const ExpandedSegment &g, int h) {
     return h == 0 ? g.first_half : g.tokens > 128 ? g.chunks : 0;
@@ -191,30 +203,36 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     const int64_t T = fits ? sc.total[0] : 0;
     const int ge = split_ctas(T, a.grid, 1);
     const bool works = T > 0 && c < ge;
-    const int64_t lo = works ? quotient(c * T, ge) : 0, hi = works ? quotient((c + 1) * T, ge) : 0;
-    if (works && find_unit(sb, units, sc, 0, lo, &ms.start)) {
+    const int64_t lo0 = quotient(c * T, ge), hi0 = quotient((c + 1) * T, ge);
+    if (works && find_unit(sb, units, sc, 0, lo0, &ms.start)) {
+        ms.lo = snapped(ms.start, a.causal, lo0);
         int64_t tiles = sc.run[1];  // expansion tiles before the sequence
         SeqInfo q = sc.first;
         for (int s = sc.beg; s < ms.start.s; q = read_seq(sb, ++s, false)) tiles += units_of(q, TokenTiles{});
         ms.start_tiles = tiles;
     }
+    WalkStart next;
+    if (works && hi0 < T && find_unit(sb, units, sc, 0, hi0, &next)) ms.hi = snapped(next, a.causal, hi0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ms.tmem_slot;
+    const int64_t lo = works ? ms.lo : 0, hi = !works ? 0 : hi0 < T ? ms.hi : T;
 
     if (warp == 2 || warp == 3) {  // (these have nothing else to do)
         // The merge job of the boundary before this CTA's share (see latent_absorbed.cu).
         if (threadIdx.x == 64) {
-            LatentJob j{0, -1, -1, 0, 0};
-            if (works && c > 0) {
+            LatentJob j{0, -1, -1, 0};
+            if (works && c > 0 && lo == lo0) {  // (else it begins with a tile)
                 const SeqInfo q = ms.start.q;
                 const ExpandedSegment g = expanded_segment(q, a.causal, ms.start.pre, lo, hi);
-                if (g.kb != 0 && g.tile_begin >= share_begin(c - 1, T, ge)) {
+                const int64_t end = g.tile_begin + ExpandedTiles(q, a.causal).chunks(g.qt);
+                // (a cut tile has more than 2 kSnap + 1 chunks; its first part is the last share's that
+                // begins before it or snapped to its begin)
+                if (g.kb != 0 && share_owner(g.tile_begin + kSnap, T, ge) == c - 1) {
                     j.out_off = ((q.q0 + g.qt * kExpQTile) * a.num_heads + g.h) * kExpHeadDim;
                     j.c0 = c - 1;
-                    j.c1 = share_owner(g.tile_begin + ExpandedTiles(q, a.causal).chunks(g.qt) - 1, T, ge);
-                    j.first = part_slot(c - 1, g.tile_begin, T, ge);
+                    j.c1 = share_owner(end - kSnap - 1, T, ge);
                     j.rows = g.tokens;
                 }
             }
@@ -438,7 +456,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             const int mine = half_chunks(g, h);
             if (mine == 0) {  // this half has no query rows here, or they see none of the segment's keys
                 if (h == 0) {
-                    const int slot = part_slot(c, g.tile_begin, T, ge);
+                    const int slot = latent_slot(c, g.kb == 0);
                     a.ws_ml[(int64_t)slot * kExpQTile + row] = make_float2(-INFINITY, 0.f);
                 }
                 f += g.chunks;
@@ -562,7 +580,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             if (!wait_all(&ms.pv_done[h], (gh - 1) & 1)) { ok = false; break; }
             tc_fence_after();
             const float inv = g.whole ? 1.f / l : 1.f;
-            const int slot = g.whole ? 0 : part_slot(c, g.tile_begin, T, ge);
+            const int slot = g.whole ? 0 : latent_slot(c, g.kb == 0);
             const bool live = tok < g.tokens;
 #pragma unroll 1
             for (int q = 0; q < kExpHeadDim / 32; ++q) {

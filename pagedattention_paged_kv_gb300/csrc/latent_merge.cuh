@@ -19,12 +19,13 @@ namespace pkv {
 // whose share begins inside it.
 struct LatentJob {
     int64_t out_off;  // element of out at which the item's first row begins
-    int32_t c0, c1;
-    int32_t first;    // slot of c0's part; CTAs c > c0 begin inside the item, their parts are in slots 2 c
-    int32_t rows;
+    int32_t c0, c1, rows;
 };
 
 constexpr int kJoinRows = 2;
+
+// A CTA has at most one part that begins inside its item, and one that begins with it.
+__device__ __forceinline__ int latent_slot(int c, bool begins) { return 2 * c + begins; }
 
 // Parts lie as [2 * grid][SLOT_ROWS] (m, l) and [2 * grid][SLOT_ROWS][D] o.  BARE: a part that
 // saw nothing of a row (m = -inf) need not have left an output there.
@@ -53,7 +54,7 @@ latent_merge_kernel(const LatentJob *jobs, const float2 *ws_ml, const float *ws_
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int p = min(p0 + u, nparts - 1);
-            const int64_t slot = p == 0 ? j.first : 2 * (j.c0 + p);
+            const int64_t slot = latent_slot(j.c0 + p, p == 0);
 #pragma unroll
             for (int k = 0; k < kJoinRows; ++k) {
                 const int row = row0 + k * SETS;
