@@ -53,22 +53,10 @@ struct ExpandedSmem {
     static_assert(BYTES <= 232448, "fits one CTA");
 };
 
-struct ExpandedMisc {
-    uint64_t q_full, q_empty, mma_done;
-    uint64_t full[3], empty[3], rope_full[2], rope_empty[2];
-    uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
-    int64_t scan[2 * kExpandedThreads / 32];
-    WalkStart start;
-    int64_t start_tiles, lo, hi;
-    uint32_t tmem_slot;
-    int abort_flag;
-};
-static_assert(sizeof(ExpandedMisc) <= 1024, "fits its place");
-
 // Closed forms for the tiles of one (sequence, head).  Causal: full tile qt visits
 // A + 2 (qt + 1) chunks, A = ceil((ctx - q_len) / 128); the last, partial one all of them.
 struct ExpandedTiles {
-    int64_t A, nfull, rem, nk;
+    int A, nfull, rem, nk;
     bool causal;
     __device__ __forceinline__ ExpandedTiles(const SeqInfo &q, bool causal_) : causal(causal_) {
         A = (q.ctx - q.q_len + kExpTile - 1) / kExpTile;
@@ -76,18 +64,17 @@ struct ExpandedTiles {
         rem = q.q_len % kExpQTile;
         nk = (q.ctx + kExpTile - 1) / kExpTile;
     }
-    __device__ __forceinline__ int64_t before(int64_t qt) const {  // chunks before tile qt <= nfull
-        return causal ? qt * A + qt * (qt + 1) : qt * nk;
+    __device__ __forceinline__ int count() const { return nfull + (rem > 0); }
+    __device__ __forceinline__ int64_t before(int qt) const {  // chunks before tile qt <= nfull
+        return (int64_t)qt * (causal ? A + qt + 1 : nk);
     }
-    __device__ __forceinline__ int64_t chunks(int64_t qt) const {
-        return !causal || qt >= nfull ? nk : A + 2 * (qt + 1);
-    }
+    __device__ __forceinline__ int chunks(int qt) const { return !causal || qt >= nfull ? nk : A + 2 * (qt + 1); }
     __device__ __forceinline__ int64_t per_head() const { return before(nfull) + (rem > 0 ? nk : 0); }
-    __device__ __forceinline__ int64_t tile_of(int64_t o) const {  // tile that holds chunk o
+    __device__ __forceinline__ int tile_of(int64_t o) const {  // tile that holds chunk o
         if (o >= before(nfull)) return nfull;
-        int64_t lo = 0, hi = nfull;
+        int lo = 0, hi = nfull;
         while (hi - lo > 1) {
-            const int64_t mid = (lo + hi) >> 1;
+            const int mid = (lo + hi) >> 1;
             if (before(mid) <= o) lo = mid; else hi = mid;
         }
         return lo;
@@ -108,43 +95,91 @@ struct TokenTiles {
 };
 
 struct ExpandedSegment {
-    int h;
-    int64_t tile_begin;  // first unit of the tile
-    int64_t qt;          // tile
+    int h, qt;           // head, tile
     int kb, chunks;      // first chunk of the segment, chunks in it
     int tokens;          // query tokens of the tile
     int first_half;      // chunks of the segment that the tile's first half sees
     bool whole;
 };
 
-__device__ __forceinline__ ExpandedSegment expanded_segment(const SeqInfo &q, bool causal, int64_t pre, int64_t f,
-                                                            int64_t hi) {
-    ExpandedSegment g;
-    const ExpandedTiles t(q, causal);
-    const int64_t ph = t.per_head(), o = f - pre;
-    g.h = (int)quotient(o, ph);
-    const int64_t o1 = o - g.h * ph;
-    g.qt = t.tile_of(o1);
-    g.kb = (int)(o1 - t.before(g.qt));
-    g.tile_begin = f - g.kb;
-    const int64_t n = t.chunks(g.qt);
-    g.chunks = (int)min64(n - g.kb, hi - f);
-    g.tokens = (int)min64(kExpQTile, q.q_len - g.qt * kExpQTile);
-    g.whole = g.kb == 0 && g.chunks == n;
-    const int64_t last0 = q.ctx - q.q_len + g.qt * kExpQTile + min(g.tokens, 128);  // keys its last token sees
-    g.first_half = causal && g.tokens > 128 ? (int)max64(0, min64(g.chunks, (last0 + kExpTile - 1) / kExpTile - g.kb)) : g.chunks;
-    return g;
+// Where a share begins: tile qt of head h of the sequence in `seq`, chunk kb (kb = the tile's chunks:
+// behind it).
+struct ExpandedStart {
+    WalkStart seq;
+    int64_t tiles;  // expansion tiles before the sequence
+    int64_t unit;
+    int h, qt, kb;
+};
+
+// The start nearest unit f of the sequence in st->seq: where the tile that holds it begins or
+// ends if that is at most kSnap chunks away, so that short tiles are not cut.
+__device__ __forceinline__ void snap_start(ExpandedStart *st, bool causal, int64_t f) {
+    const ExpandedTiles t(st->seq.q, causal);
+    const int64_t ph = t.per_head(), o = f - st->seq.pre, h = quotient(o, ph), o1 = o - h * ph;
+    const int qt = t.tile_of(o1), at = (int)(o1 - t.before(qt)), n = t.chunks(qt);
+    const int kb = at <= kSnap ? 0 : n - at <= kSnap ? n : at;
+    st->h = (int)h;
+    st->qt = qt;
+    st->kb = kb;
+    st->unit = f + (kb - at);
 }
 
-// Where a share that would begin at unit f begins: the tile's begin or end if that is near, so that
-// short tiles are not cut.  (The sequence that holds f is given.)
-__device__ __forceinline__ int64_t snapped(const WalkStart &at, bool causal, int64_t f) {
-    const ExpandedTiles t(at.q, causal);
-    const int64_t ph = t.per_head(), o = f - at.pre;
-    const int64_t o1 = o - quotient(o, ph) * ph, qt = t.tile_of(o1);
-    const int64_t kb = o1 - t.before(qt), left = t.chunks(qt) - kb;
-    return kb <= kSnap ? f - kb : left <= kSnap ? f + left : f;
-}
+// A warp's walk over the tiles of its CTA's share: steps, no division.  (The first pass through
+// any code waits for its instructions, so what every role runs before its first tile is kept short:
+// finding the tile of a unit anew for every segment put 9,000 cycles before the first load.)
+struct TileWalk {
+    SeqWalk<ExpandedUnits> w;
+    ExpandedTiles t;
+    int64_t left;  // units of the share from here on
+    int h, qt, kb;
+    bool causal;
+    int heads;
+    __device__ __forceinline__ TileWalk(const SeqBatch &sb, const ExpandedUnits &u, const ExpandedStart &st, int64_t hi)
+        : t(st.seq.q, u.causal), left(hi - st.unit), h(st.h), qt(st.qt), kb(st.kb), causal(u.causal),
+          heads(u.num_heads) {
+        w.start(st.seq);
+        if (left > 0 && kb == t.chunks(qt)) next(sb, u);
+    }
+    __device__ __forceinline__ void next(const SeqBatch &sb, const ExpandedUnits &u) {
+        kb = 0;
+        if (++qt < t.count()) return;
+        qt = 0;
+        if (++h < heads) return;
+        h = 0;
+        w.seek(sb, u, w.pre + w.units);
+        t = ExpandedTiles(w.q, causal);
+    }
+    __device__ __forceinline__ ExpandedSegment segment() const {
+        ExpandedSegment g;
+        g.h = h;
+        g.qt = qt;
+        g.kb = kb;
+        const int n = t.chunks(qt);
+        g.chunks = (int)min64(n - kb, left);
+        g.tokens = min(kExpQTile, w.q.q_len - qt * kExpQTile);
+        g.whole = g.chunks == n;
+        const int last0 = w.q.ctx - w.q.q_len + qt * kExpQTile + min(g.tokens, 128);  // keys its last token sees
+        g.first_half = causal && g.tokens > 128
+                           ? max(0, min(g.chunks, (last0 + kExpTile - 1) / kExpTile - kb)) : g.chunks;
+        return g;
+    }
+    // past the segment
+    __device__ __forceinline__ void advance(const SeqBatch &sb, const ExpandedUnits &u, const ExpandedSegment &g) {
+        left -= g.chunks;
+        if (left > 0) next(sb, u);
+    }
+};
+
+struct ExpandedMisc {
+    uint64_t q_full, q_empty, mma_done;
+    uint64_t full[3], empty[3], rope_full[2], rope_empty[2];
+    uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+    int64_t scan[2 * kExpandedThreads / 32];
+    ExpandedStart start[2];  // of this share and the next
+    uint32_t tmem_slot;
+    int abort_flag;
+};
+static_assert(sizeof(ExpandedMisc) <= 1024, "fits its place");
 
 // Chunks of a segment that half h has to do with.
 __device__ __forceinline__ int half_chunks(const ExpandedSegment &g, int h) {
@@ -203,37 +238,39 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     const int64_t T = fits ? sc.total[0] : 0;
     const int ge = split_ctas(T, a.grid, 1);
     const bool works = T > 0 && c < ge;
-    const int64_t lo0 = quotient(c * T, ge), hi0 = quotient((c + 1) * T, ge);
-    if (works && find_unit(sb, units, sc, 0, lo0, &ms.start)) {
-        ms.lo = snapped(ms.start, a.causal, lo0);
-        int64_t tiles = sc.run[1];  // expansion tiles before the sequence
-        SeqInfo q = sc.first;
-        for (int s = sc.beg; s < ms.start.s; q = read_seq(sb, ++s, false)) tiles += units_of(q, TokenTiles{});
-        ms.start_tiles = tiles;
+    // This share's begin and the next one's, each found by the thread whose sequences hold it.
+#pragma unroll 1
+    for (int i = 0; i < 2 && works; ++i) {
+        const int64_t f = quotient((c + i) * T, ge);
+        ExpandedStart *st = &ms.start[i];
+        if (f < T && find_unit(sb, units, sc, 0, f, &st->seq)) {
+            snap_start(st, a.causal, f);
+            st->tiles = sc.run[1];
+            SeqInfo q = sc.first;
+            for (int s = sc.beg; s < st->seq.s; q = read_seq(sb, ++s, false)) st->tiles += units_of(q, TokenTiles{});
+        }
     }
-    WalkStart next;
-    if (works && hi0 < T && find_unit(sb, units, sc, 0, hi0, &next)) ms.hi = snapped(next, a.causal, hi0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ms.tmem_slot;
-    const int64_t lo = works ? ms.lo : 0, hi = !works ? 0 : hi0 < T ? ms.hi : T;
+    const int64_t hi = !works ? 0 : c + 1 < ge ? ms.start[1].unit : T;
 
     if (warp == 2 || warp == 3) {  // (these have nothing else to do)
         // The merge job of the boundary before this CTA's share (see latent_absorbed.cu).
         if (threadIdx.x == 64) {
             LatentJob j{0, -1, -1, 0};
-            if (works && c > 0 && lo == lo0) {  // (else it begins with a tile)
-                const SeqInfo q = ms.start.q;
-                const ExpandedSegment g = expanded_segment(q, a.causal, ms.start.pre, lo, hi);
-                const int64_t end = g.tile_begin + ExpandedTiles(q, a.causal).chunks(g.qt);
-                // (a cut tile has more than 2 kSnap + 1 chunks; its first part is the last share's that
-                // begins before it or snapped to its begin)
-                if (g.kb != 0 && share_owner(g.tile_begin + kSnap, T, ge) == c - 1) {
-                    j.out_off = ((q.q0 + g.qt * kExpQTile) * a.num_heads + g.h) * kExpHeadDim;
+            if (works && c > 0) {
+                const ExpandedStart st = ms.start[0];
+                const int n = ExpandedTiles(st.seq.q, a.causal).chunks(st.qt);
+                const int64_t begin = st.unit - st.kb;
+                // a cut tile has more than 2 kSnap + 1 chunks; its first part is that of the last share
+                // that begins before it or snapped to its begin
+                if (st.kb > 0 && st.kb < n && share_owner(begin + kSnap, T, ge) == c - 1) {
+                    j.out_off = ((int64_t)(st.seq.q.q0 + st.qt * kExpQTile) * a.num_heads + st.h) * kExpHeadDim;
                     j.c0 = c - 1;
-                    j.c1 = share_owner(end - kSnap - 1, T, ge);
-                    j.rows = g.tokens;
+                    j.c1 = share_owner(begin + n - kSnap - 1, T, ge);
+                    j.rows = min(kExpQTile, st.seq.q.q_len - st.qt * kExpQTile);
                 }
             }
             if (c > 0) a.ws_jobs[c - 1] = j;
@@ -252,8 +289,8 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         return;
     }
 
-    SeqWalk<ExpandedUnits> w;
-    w.start(ms.start);
+    TileWalk tw(sb, units, ms.start[0], hi);
+    SeqWalk<ExpandedUnits> &w = tw.w;
     if (warp != 0) w.ahead(sb);  // the producer is on the critical path
     auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
@@ -278,12 +315,11 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             ++np;
             return true;
         };
-        int64_t tiles = ms.start_tiles;
-        int seq = ms.start.s, ctx = ms.start.q.ctx;
+        int64_t tiles = ms.start[0].tiles;
+        int seq = ms.start[0].seq.s, ctx = ms.start[0].seq.q.ctx;
         bool waited = false;
-        for (int64_t f = lo; f < hi && ok;) {
-            w.seek(sb, units, f);
-            const ExpandedSegment g = expanded_segment(w.q, a.causal, w.pre, f, hi);
+        while (tw.left > 0 && ok) {
+            const ExpandedSegment g = tw.segment();
             if (w.s != seq) {  // the next live sequence
                 tiles += (ctx + kExpTile - 1) / kExpTile;
                 seq = w.s;
@@ -318,7 +354,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 ++n;
                 w.ahead(sb);
             }
-            f += g.chunks;
+            tw.advance(sb, units, g);
         }
         if (!waited) pdl_wait();
         if (!ok && lane == 0) {
@@ -397,9 +433,8 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             }
             return true;
         };
-        for (int64_t f = lo; f < hi && ok;) {
-            w.seek(sb, units, f);
-            const ExpandedSegment g = expanded_segment(w.q, a.causal, w.pre, f, hi);
+        while (tw.left > 0 && ok) {
+            const ExpandedSegment g = tw.segment();
             const int chunks = __shfl_sync(0xffffffffu, g.chunks, 0);
             const int cnt[2] = {__shfl_sync(0xffffffffu, half_chunks(g, 0), 0),
                                 __shfl_sync(0xffffffffu, half_chunks(g, 1), 0)};
@@ -430,7 +465,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                     segh[h] += 1;
                 }
             n += chunks;
-            f += g.chunks;
+            tw.advance(sb, units, g);
             ++segs;
         }
         if (!ok) {
@@ -450,16 +485,15 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         const float sl2 = a.scale_log2;
         const uint64_t sc2 = f2_pack(sl2, sl2);
         uint32_t gh = 0;  // chunks this half has processed
-        for (int64_t f = lo; f < hi && ok;) {
-            w.seek(sb, units, f);
-            const ExpandedSegment g = expanded_segment(w.q, a.causal, w.pre, f, hi);
+        while (tw.left > 0 && ok) {
+            const ExpandedSegment g = tw.segment();
             const int mine = half_chunks(g, h);
             if (mine == 0) {  // this half has no query rows here, or they see none of the segment's keys
                 if (h == 0) {
                     const int slot = latent_slot(c, g.kb == 0);
                     a.ws_ml[(int64_t)slot * kExpQTile + row] = make_float2(-INFINITY, 0.f);
                 }
-                f += g.chunks;
+                tw.advance(sb, units, g);
                 continue;
             }
             const int ctx = w.q.ctx;
@@ -589,7 +623,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 tmem_wait_ld();
                 reg_order32(r);
                 if (live && g.whole) {
-                    __nv_bfloat16 *o = a.out + ((w.q.q0 + g.qt * kExpQTile + tok) * a.num_heads + g.h) * kExpHeadDim + q * 32;
+                    __nv_bfloat16 *o = a.out + ((int64_t)(w.q.q0 + g.qt * kExpQTile + tok) * a.num_heads + g.h) * kExpHeadDim + q * 32;
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         uint32_t x[8];
@@ -610,7 +644,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.o_free[h]);
-            f += g.chunks;
+            tw.advance(sb, units, g);
         }
         if (!ok) {
             if (lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
