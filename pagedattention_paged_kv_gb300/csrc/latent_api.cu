@@ -237,11 +237,15 @@ extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int
 
     CUtensorMap latmap, wkmap, wvmap, qmap, kvmap, ropemap;
     st = encode_latent_map(&latmap, latent_cache, num_blocks, block_size, latent_dim + rope_dim, latent_dim / 64);
-    const uint64_t wdims[2] = {(uint64_t)latent_dim, (uint64_t)num_heads * pkv::kExpHeadDim};
-    const uint64_t wstride[1] = {(uint64_t)latent_dim * 2};
+    // A weight's rows in the order in which the expansion's epilogue has its columns: row
+    // 16 j + 2 i + e of 64 goes to place 8 i + 2 j + e.
+    const uint64_t wrow = (uint64_t)latent_dim * 2;
+    const uint64_t wdims[5] = {(uint64_t)latent_dim, 2, 4, 8, (uint64_t)num_heads * (pkv::kExpHeadDim / 64)};
+    const uint64_t wstride[4] = {wrow, 16 * wrow, 2 * wrow, 64 * wrow};
+    const uint32_t wbox[5] = {64, 2, 4, 8, pkv::kExpHeadDim / 64};
+    if (st == PKV_OK) st = pkv::encode_tiled(&wkmap, 5, w_k, wdims, wstride, wbox);
+    if (st == PKV_OK) st = pkv::encode_tiled(&wvmap, 5, w_v, wdims, wstride, wbox);
     const uint32_t rows128[2] = {64, 128};
-    if (st == PKV_OK) st = pkv::encode_tiled(&wkmap, 2, w_k, wdims, wstride, rows128);
-    if (st == PKV_OK) st = pkv::encode_tiled(&wvmap, 2, w_v, wdims, wstride, rows128);
     const uint64_t qcols = (uint64_t)nope_dim + rope_dim;
     const uint64_t qdims[4] = {64, qcols / 64, (uint64_t)num_heads, (uint64_t)total_q_tokens};
     const uint64_t qstride[3] = {128, qcols * 2, qcols * 2 * num_heads};

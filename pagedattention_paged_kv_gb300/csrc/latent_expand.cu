@@ -22,6 +22,7 @@
 // Waits are bounded in time.  The CTAs of a pair (always resident together) wait for each other;
 // no pair waits for another.
 #include "attn_block.cuh"
+#include "fp32x2.cuh"
 #include "latent_expanded.cuh"
 #include "latent_walk.cuh"
 #include "pkv_split.cuh"
@@ -217,8 +218,8 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
                     ok = mbar_wait(&ms.w_empty[st], ph ^ 1, abort_flag, a.wait_ns);
                     if (!ok) break;
                     if (rank == 0) mbar_arrive_expect_tx(&ms.w_full[st], 2 * L::W_STAGE);  // both CTAs' halves
-                    tma_load_2d_pair(smem_u32(sW) + st * L::W_STAGE, w_map, w_full0 + st * 8, kc * 64, h * kExpHeadDim,
-                                     policy);
+                    tma_load_5d_pair(smem_u32(sW) + st * L::W_STAGE, w_map, w_full0 + st * 8, kc * 64, 0, 0, 0,
+                                     h * (kExpHeadDim / 64), policy);
                     ++fill;
                     if (++st == NST) { st = 0; ph ^= 1; }
                 }
@@ -296,12 +297,15 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
         }
         __syncwarp();
     } else {
-        // ------------- epilogue: one token a thread, 32 bytes a store -------------
-        // Four warps write the keys, four the values: one set of four took 6,000 cycles a unit, its
-        // products 4,100.
+        // ------------- epilogue -------------
+        // Four warps write the keys, four the values.  The accumulator is read so that a row's 64
+        // columns lie in four threads, 16 each in the pattern of tmem_ld_16x32; the weight map puts
+        // weight rows 16 j .. 16 j + 15 of a piece there for thread j, so a thread has 32 bytes that
+        // belong together and four threads a whole line.  (With a row a thread, 32 lines a store, a
+        // unit's stores took 5,500 cycles, its products 4,100.)
         const int quarter = warp & 3;
         const bool is_v = warp >= 6;
-        const int row = quarter * 32 + lane;
+        const int row = quarter * 32 + (lane >> 2), part = lane & 3;
         const uint32_t acc_free0 = smem_of_cta(&ms.acc_free[0], 0);
         uint32_t n = 0;
         int64_t p = quotient(lo, H);
@@ -317,29 +321,38 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
             if (!wait_all(&ms.acc_full[n & 1], (n >> 1) & 1)) { ok = false; break; }
             tc_fence_after();
             if (g < NT) {
-                uint16_t *dst = a.buf.kv + ((int64_t)(h * 4 + 2 * is_v) * a.buf.padded + row0 + row) * 64;
+                uint16_t *dst = a.buf.kv + ((int64_t)(h * 4 + 2 * is_v) * a.buf.padded + row0) * 64 + part * 16;
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {  // 32 columns
+                for (int i = 0; i < 4; ++i) {  // a 64-column piece, 16 of the warp's rows
+                    const int q = i >> 1, r0 = row + (i & 1) * 16;
                     uint32_t r[32];
-                    tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (n & 1) * 256 + is_v * 128 + q * 32, r);
+                    tmem_ld_16x64(tmem + ((uint32_t)(quarter * 32 + (i & 1) * 16) << 16) + (n & 1) * 256 + is_v * 128 +
+                                      q * 64, r);
                     tmem_wait_ld();
                     reg_order32(r);
-                    if (row >= valid) {  // past the context the product saw whatever the slots held
+                    if (valid < kExpTile) {  // past the context the product saw whatever the slots held
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) r[j] = 0u;
+                        for (int j = 0; j < 32; ++j)
+                            if (r0 + (j & 2) * 4 >= valid) r[j] = 0u;
                     }
                     if (is_v) {
-                        bool over = false;
+                        float top = 0.f;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) over |= clamp_f16(r[j]);
-                        if (over) flag_error(a.err, PKV_DEVERR_VALUE);
+                        for (int j = 0; j < 32; j += 2)
+                            top = fmax3(top, fabsf(__uint_as_float(r[j])), fabsf(__uint_as_float(r[j + 1])));
+                        if (__any_sync(0xffffffffu, top > 65504.f)) {
+                            bool over = false;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) over |= clamp_f16(r[j]);
+                            if (over) flag_error(a.err, PKV_DEVERR_VALUE);
+                        }
                     }
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                    for (int k = 0; k < 2; ++k) {  // rows r0 and r0 + 8
                         uint32_t x[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) x[j] = pack_16(is_v, r[16 * k + 2 * j], r[16 * k + 2 * j + 1]);
-                        st_global_32(dst + (q >> 1) * a.buf.padded * 64 + (q & 1) * 32 + k * 16, x);
+                        for (int j = 0; j < 8; ++j) x[j] = pack_16(is_v, r[4 * j + 2 * k], r[4 * j + 2 * k + 1]);
+                        st_global_32(dst + (int64_t)q * a.buf.padded * 64 + (r0 + 8 * k) * 64, x);
                     }
                 }
             }
