@@ -237,14 +237,18 @@ extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int
 
     CUtensorMap latmap, wkmap, wvmap, qmap, kvmap, ropemap;
     st = encode_latent_map(&latmap, latent_cache, num_blocks, block_size, latent_dim + rope_dim, latent_dim / 64);
-    // A weight's rows in the order in which the expansion's epilogue has its columns: row
-    // 16 j + 2 i + e of 64 goes to place 8 i + 2 j + e.
-    const uint64_t wrow = (uint64_t)latent_dim * 2;
-    const uint64_t wdims[5] = {(uint64_t)latent_dim, 2, 4, 8, (uint64_t)num_heads * (pkv::kExpHeadDim / 64)};
-    const uint64_t wstride[4] = {wrow, 16 * wrow, 2 * wrow, 64 * wrow};
-    const uint32_t wbox[5] = {64, 2, 4, 8, pkv::kExpHeadDim / 64};
-    if (st == PKV_OK) st = pkv::encode_tiled(&wkmap, 5, w_k, wdims, wstride, wbox);
-    if (st == PKV_OK) st = pkv::encode_tiled(&wvmap, 5, w_v, wdims, wstride, wbox);
+    // The weights' rows in the order in which the epilogues have the columns (tmem_ld_16x64 gives
+    // thread j of four columns 8 i + 2 j + e, which it stores as its 16 j + 2 i + e): the keys' so that
+    // they are stored in their own order, the values' so that the attention's output is.
+    const uint64_t wrow = (uint64_t)latent_dim * 2, pieces = (uint64_t)num_heads * (pkv::kExpHeadDim / 64);
+    const uint64_t kdims[5] = {(uint64_t)latent_dim, 2, 4, 8, pieces};
+    const uint64_t kstride[4] = {wrow, 16 * wrow, 2 * wrow, 64 * wrow};
+    const uint32_t kbox[5] = {64, 2, 4, 8, pkv::kExpHeadDim / 64};
+    const uint64_t vdims[5] = {(uint64_t)latent_dim, 2, 16, 2, pieces};
+    const uint64_t vstride[4] = {wrow, 4 * wrow, 2 * wrow, 64 * wrow};
+    const uint32_t vbox[5] = {64, 2, 16, 2, pkv::kExpHeadDim / 64};
+    if (st == PKV_OK) st = pkv::encode_tiled(&wkmap, 5, w_k, kdims, kstride, kbox);
+    if (st == PKV_OK) st = pkv::encode_tiled(&wvmap, 5, w_v, vdims, vstride, vbox);
     const uint32_t rows128[2] = {64, 128};
     const uint64_t qcols = (uint64_t)nope_dim + rope_dim;
     const uint64_t qdims[4] = {64, qcols / 64, (uint64_t)num_heads, (uint64_t)total_q_tokens};

@@ -299,9 +299,9 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
     } else {
         // ------------- epilogue -------------
         // Four warps write the keys, four the values.  The accumulator is read so that a row's 64
-        // columns lie in four threads, 16 each in the pattern of tmem_ld_16x32; the weight map puts
-        // weight rows 16 j .. 16 j + 15 of a piece there for thread j, so a thread has 32 bytes that
-        // belong together and four threads a whole line.  (With a row a thread, 32 lines a store, a
+        // columns lie in four threads, 16 each (tmem_ld_16x64), which are 32 bytes of the stored row:
+        // four threads store a whole line.  What order the stored columns have follows from the order
+        // in which the weight maps load the weights' rows.  (With a row a thread, 32 lines a store, a
         // unit's stores took 5,500 cycles, its products 4,100.)
         const int quarter = warp & 3;
         const bool is_v = warp >= 6;

@@ -349,6 +349,10 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 tma_load_2d_warp(rope0 + (n & 1) * L::PIECE, &rope_map, &ms.rope_full[n & 1], 0, key, policy);
                 ++nr;
                 if (!load_pair(2 * n + 1, row + 2 * pitch)) { ok = false; break; }
+                // The next chunk's pieces into L2, while their places are still in use.
+                if (ch + 1 < chunks && lane < 4)
+                    l2_prefetch(a.buf.kv + ((int64_t)row + kExpTile + (int64_t)lane * pitch) * 64, L::PIECE);
+                __syncwarp();
                 key += kExpTile;
                 row += kExpTile;
                 ++n;
@@ -615,32 +619,44 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             tc_fence_after();
             const float inv = g.whole ? 1.f / l : 1.f;
             const int slot = g.whole ? 0 : latent_slot(c, g.kb == 0);
-            const bool live = tok < g.tokens;
+            // 16 rows x 64 columns at a time: four threads have a row's 64 columns, in the order in which
+            // the values are stored 16 that belong together each, so a store writes whole lines (with a
+            // row a thread the epilogue took twice as long).
+            const int part = lane & 3;
 #pragma unroll 1
-            for (int q = 0; q < kExpHeadDim / 32; ++q) {
+            for (int i = 0; i < 4; ++i) {
+                const int q = i >> 1, r0 = (i & 1) * 16 + (lane >> 2);  // rows r0, r0 + 8 of the warp's 32
                 uint32_t r[32];
-                tmem_ld32(tO + q * 32, r);
+                tmem_ld_16x64(tO + ((uint32_t)((i & 1) * 16) << 16) + q * 64, r);
                 tmem_wait_ld();
                 reg_order32(r);
-                if (live && g.whole) {
-                    __nv_bfloat16 *o = a.out + ((int64_t)(w.q.q0 + g.qt * kExpQTile + tok) * a.num_heads + g.h) * kExpHeadDim + q * 32;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < 2; ++k) {
+                    const float f = __shfl_sync(0xffffffffu, inv, r0 + 8 * k);
+                    const int t = h * 128 + quarter * 32 + r0 + 8 * k;  // token inside the tile
+                    if (t >= g.tokens) continue;
+                    if (g.whole) {
                         uint32_t x[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            x[j] = pack_bf16x2(__uint_as_float(r[16 * k + 2 * j]) * inv,
-                                               __uint_as_float(r[16 * k + 2 * j + 1]) * inv);
-                        st_global_32(o + 16 * k, x);
-                    }
-                } else if (live) {
-                    float *o = a.ws_o + ((int64_t)slot * kExpQTile + tok) * kExpHeadDim + q * 32;
+                            x[j] = pack_bf16x2(__uint_as_float(r[4 * j + 2 * k]) * f,
+                                               __uint_as_float(r[4 * j + 2 * k + 1]) * f);
+                        st_global_32(a.out + ((int64_t)(w.q.q0 + g.qt * kExpQTile + t) * a.num_heads + g.h) * kExpHeadDim +
+                                         q * 64 + part * 16, x);
+                    } else {
+                        float *o = a.ws_o + ((int64_t)slot * kExpQTile + t) * kExpHeadDim + q * 64 + part * 16;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) st_global_32(o + 8 * k, reinterpret_cast<const uint32_t(&)[8]>(r[8 * k]));
+                        for (int m = 0; m < 2; ++m) {
+                            uint32_t x[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) x[j] = r[4 * (4 * m + j / 2) + 2 * k + j % 2];
+                            st_global_32(o + 8 * m, x);
+                        }
+                    }
                 }
                 __syncwarp();
             }
-            if (!g.whole && live) a.ws_ml[(int64_t)slot * kExpQTile + tok] = make_float2(m_ref, l);
+            if (!g.whole && tok < g.tokens) a.ws_ml[(int64_t)slot * kExpQTile + tok] = make_float2(m_ref, l);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.o_free[h]);

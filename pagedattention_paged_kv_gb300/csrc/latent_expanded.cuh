@@ -16,7 +16,8 @@ constexpr int kExpQTile = 256;    // query tokens of an attention tile (two MMA 
 // The expanded keys and values of a call, for head h and padded token i (each sequence with query
 // rows starts on the next multiple of 128): piece p (64 key columns, the next 64, 64 value columns,
 // the next 64) is row (4 h + p) * padded + i of kv, so the 128 rows of a box are contiguous; rope
-// row i is the token's rotary key part.  Rows past a context are zero.
+// row i is the token's rotary key part.  Rows past a context are zero.  Value column 16 j + 2 i + e of
+// 64 (e < 2, i < 8) is stored as column 8 i + 2 j + e.
 struct ExpandedBuffers {
     __nv_bfloat16 *rope;  // [padded][64]
     uint16_t *kv;         // [num_heads][4][padded][64]: bf16 keys, fp16 values
@@ -60,8 +61,8 @@ struct ExpandedPlan {
 
 void plan_expanded(int num_seqs, int64_t total_context, int num_heads, int sms, ExpandedPlan *p);
 
-// kv_map: the latent cache in boxes of min(block, 32 tokens) x the latent chunks; wk_map, wv_map: the weights as rows
-// [num_heads * 128][latent_dim] in boxes of 128 rows x 64 columns.
+// kv_map: the latent cache in boxes of min(block, 32 tokens) x the latent chunks; wk_map, wv_map: 64
+// columns of a head's 128 weight rows, in the order that the epilogues want.
 cudaError_t launch_latent_expand(int latent_dim, const CUtensorMap &kv_map, const CUtensorMap &wk_map,
                                  const CUtensorMap &wv_map, const ExpandArgs &a, cudaStream_t stream);
 

@@ -90,6 +90,11 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// Asks for `bytes` (a multiple of 16, from a 16-byte boundary) in L2.
+__device__ __forceinline__ void l2_prefetch(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // ---- CTA pairs (clusters of two) ---------------------------------------------
 // Address, in the cluster's shared-memory window, of `p`'s place in CTA `rank`.
 __device__ __forceinline__ uint32_t smem_of_cta(const void *p, uint32_t rank) {
