@@ -387,8 +387,8 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         uint32_t n = 0;             // chunks whose PV is behind
         uint32_t kp = 0, kq = 0;    // place and parity of the next chunk's keys
         uint32_t vp = 1, vq = 0;    // and of the current one's values
-        uint32_t gh[2] = {0, 0};    // chunks each half has processed
-        uint32_t segh[2] = {0, 0};  // tiles each half has processed
+        uint32_t pq = 0;            // by half, a bit each: parity of its next weights,
+        uint32_t oq = 0, used = 0;  // parity of its next accumulator's release, whether it had one
         uint32_t segs = 0;
         auto next2 = [&](uint32_t &place, uint32_t &parity) {  // two pairs on
             place += 2;
@@ -440,34 +440,31 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         while (tw.left > 0 && ok) {
             const ExpandedSegment g = tw.segment();
             const int chunks = __shfl_sync(0xffffffffu, g.chunks, 0);
-            const int cnt[2] = {__shfl_sync(0xffffffffu, half_chunks(g, 0), 0),
-                                __shfl_sync(0xffffffffu, half_chunks(g, 1), 0)};
-            const int last = cnt[1] > 0 ? 1 : 0;  // the second half, where there is one, sees every chunk
+            const int cnt0 = __shfl_sync(0xffffffffu, half_chunks(g, 0), 0);
+            const int cnt1 = __shfl_sync(0xffffffffu, half_chunks(g, 1), 0);
+            const int last = cnt1 > 0 ? 1 : 0;  // the second half, where there is one, sees every chunk
             if (!wait_all(&ms.q_full, segs & 1)) { ok = false; break; }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (cnt[h] > 0 && ok) ok = issue_qk(h, n, h == last);
-            if (!ok) break;
-            if (chunks == 1) umma_commit_warp(&ms.q_empty);
-            for (int ch = 0; ch < chunks && ok; ++ch) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (ch >= cnt[h]) continue;
-                    if (ch == 0 && segh[h] > 0 && !wait_all(&ms.o_free[h], (segh[h] - 1) & 1)) { ok = false; break; }
-                    if (!wait_all(&ms.p_full[h], (gh[h] + ch) & 1)) { ok = false; break; }
-                    if (!issue_pv(h, ch == 0, h == last)) { ok = false; break; }
-                    if (ch + 1 < cnt[h]) {
-                        if (!issue_qk(h, n + ch + 1, h == last)) { ok = false; break; }
-                        if (h == last && ch + 2 == chunks) umma_commit_warp(&ms.q_empty);
+            // One copy of the code for both halves and for the first scores: every line of it waits
+            // for its instructions once, 2,000 cycles a copy.
+#pragma unroll 1
+            for (int step = -2; step < 2 * chunks && ok; ++step) {
+                const int ch = step >> 1, h = step & 1, cnt = h ? cnt1 : cnt0;
+                if (ch >= 0 && ch < cnt) {
+                    if (ch == 0) {
+                        if ((used >> h & 1) && !wait_all(&ms.o_free[h], oq >> h & 1)) { ok = false; break; }
+                        oq ^= (used >> h & 1) << h;
+                        used |= 1u << h;
                     }
+                    if (!wait_all(&ms.p_full[h], pq >> h & 1)) { ok = false; break; }
+                    pq ^= 1u << h;
+                    if (!issue_pv(h, ch == 0, h == last)) { ok = false; break; }
+                }
+                if (ch + 1 < cnt) {
+                    if (!issue_qk(h, n + ch + 1, h == last)) { ok = false; break; }
+                    if (h == last && ch + 2 == chunks) umma_commit_warp(&ms.q_empty);
                 }
             }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (cnt[h] > 0) {
-                    gh[h] += cnt[h];
-                    segh[h] += 1;
-                }
+            if (!ok) break;
             n += chunks;
             tw.advance(sb, units, g);
             ++segs;
