@@ -268,6 +268,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
                 ++atiles;
             }
             if (n >= 2 && !wait_all(&ms.acc_free[n & 1], ((n >> 1) - 1) & 1)) { ok = false; break; }
+#pragma unroll 1
             for (int kc = 0; kc < KCH; ++kc) {
                 if (!wait_all(&ms.w_full[st], ph)) { ok = false; break; }
                 tc_fence_after();
