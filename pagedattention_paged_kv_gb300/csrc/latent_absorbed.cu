@@ -73,6 +73,12 @@ struct AbsorbedSmem {
     static_assert(NST >= 2, "two tiles in flight at least");
 };
 
+// Where a share begins: 64-row group grp of the sequence, tile kb.
+struct AbsorbedStart {
+    WalkStart seq;
+    int grp, kb;
+};
+
 struct AbsorbedMisc {
     uint64_t q_full, q_empty, o_free, qk_over, pv_over, group, rescaled;
     uint64_t pv_done, p_full[2];  // p_full: by half of the tile
@@ -81,7 +87,7 @@ struct AbsorbedMisc {
     uint32_t tmem_slot;
     int abort_flag;
     int64_t scan[8];
-    WalkStart start;
+    AbsorbedStart start;
     int moved[2][4];  // by tile parity and softmax warp: a row's reference maximum moved
     float alpha[2][kLatentRows];
     float inv[kLatentRows];
@@ -103,27 +109,43 @@ struct AbsorbedUnits {
 
 // The part of one item that lies in the CTA's share.
 struct AbsorbedSegment {
-    int64_t row0;        // its first query row (token * heads + head)
+    int64_t row0;        // the item's first query row (token * heads + head)
     int row_in_seq;      // the same, counted inside the sequence
     int rows;            // live rows, <= 64
     int kb, tiles;       // first tile of the segment, tiles in it
     bool whole;          // the segment is the whole item
 };
 
-__device__ __forceinline__ AbsorbedSegment segment_at(const AbsorbedArgs &a, const SeqInfo &q, int64_t pre,
-                                                      int64_t f, int64_t hi) {
-    AbsorbedSegment g;
-    const int nk = (q.ctx + kLatentTile - 1) / kLatentTile;
-    const int64_t o = f - pre;
-    const int64_t grp = quotient(o, nk);
-    g.kb = (int)(o - grp * nk);
-    g.tiles = (int)min64(nk - g.kb, hi - f);
-    g.row_in_seq = (int)(grp * kLatentRows);
-    g.row0 = (int64_t)q.q0 * a.num_heads + g.row_in_seq;
-    g.rows = (int)min64(kLatentRows, (int64_t)q.q_len * a.num_heads - g.row_in_seq);
-    g.whole = g.kb == 0 && g.tiles == nk;
-    return g;
-}
+// A warp's walk over the items of its CTA's share: steps from the start, which one thread found,
+// without a division.  (The first pass through any code waits for its instructions: what every role
+// runs before its first tile is kept short.)
+struct ItemWalk {
+    SeqWalk<AbsorbedUnits> w;
+    int64_t left;  // units of the share from here on
+    int grp, kb;   // 64-row group of the sequence, its tile
+    __device__ __forceinline__ ItemWalk(const AbsorbedStart &st, int64_t units) : left(units), grp(st.grp), kb(st.kb) {
+        w.start(st.seq);
+    }
+    __device__ __forceinline__ AbsorbedSegment segment(int num_heads) const {
+        AbsorbedSegment g;
+        const int nk = (w.q.ctx + kLatentTile - 1) / kLatentTile;
+        g.kb = kb;
+        g.tiles = (int)min64(nk - kb, left);
+        g.row_in_seq = grp * kLatentRows;
+        g.row0 = (int64_t)w.q.q0 * num_heads + g.row_in_seq;
+        g.rows = min(kLatentRows, w.q.q_len * num_heads - g.row_in_seq);
+        g.whole = g.tiles == nk;
+        return g;
+    }
+    // past the segment
+    __device__ __forceinline__ void advance(const SeqBatch &sb, const AbsorbedUnits &u, const AbsorbedSegment &g) {
+        left -= g.tiles;
+        kb = 0;
+        if (++grp * kLatentRows < w.q.q_len * u.num_heads || left <= 0) return;
+        grp = 0;
+        w.seek(sb, u, w.pre + w.units);
+    }
+};
 
 }  // namespace
 
@@ -181,7 +203,11 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     const int ge = split_ctas(T, a.grid, kMinTilesPerCta);
     const bool works = T > 0 && c < ge;
     const int64_t lo = works ? quotient(c * T, ge) : 0, hi = works ? quotient((c + 1) * T, ge) : 0;
-    if (works) find_unit(sb, units, sc, 0, lo, &ms.start);
+    if (works && find_unit(sb, units, sc, 0, lo, &ms.start.seq)) {
+        const int64_t nk = (ms.start.seq.q.ctx + kLatentTile - 1) / kLatentTile, o = lo - ms.start.seq.pre;
+        ms.start.grp = (int)quotient(o, nk);
+        ms.start.kb = (int)(o - ms.start.grp * nk);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -192,14 +218,14 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         if (threadIdx.x == 64) {
             LatentJob j{0, -1, -1, 0};
             if (works && c > 0) {
-                const SeqInfo q = ms.start.q;
-                const int64_t nk = (q.ctx + kLatentTile - 1) / kLatentTile;
-                const int64_t grp = quotient(lo - ms.start.pre, nk), begin = ms.start.pre + grp * nk;
+                const SeqInfo q = ms.start.seq.q;
+                const int grp = ms.start.grp, nk = (q.ctx + kLatentTile - 1) / kLatentTile;
+                const int64_t begin = lo - ms.start.kb;
                 if (begin != lo && begin >= quotient((c - 1) * T, ge)) {
                     j.out_off = ((int64_t)q.q0 * a.num_heads + grp * kLatentRows) * R;
                     j.c0 = c - 1;
                     j.c1 = share_owner(begin + nk - 1, T, ge);
-                    j.rows = (int)min64(kLatentRows, (int64_t)q.q_len * a.num_heads - grp * kLatentRows);
+                    j.rows = min(kLatentRows, q.q_len * a.num_heads - grp * kLatentRows);
                 }
             }
             if (c > 0) a.ws_jobs[c - 1] = j;
@@ -216,8 +242,8 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         if (warp == 1) tmem_dealloc(tmem, 512);
         return;
     }
-    SeqWalk<AbsorbedUnits> w;
-    w.start(ms.start);
+    ItemWalk iw(ms.start, hi - lo);
+    SeqWalk<AbsorbedUnits> &w = iw.w;
     if (warp != 0) w.ahead(sb);  // the producer is on the critical path
 
     if (warp == 0) {
@@ -233,9 +259,8 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
         };
         bool ok = true;
-        for (int64_t f = lo; f < hi && ok;) {
-            w.seek(sb, units, f);
-            const AbsorbedSegment g = segment_at(a, w.q, w.pre, f, hi);
+        while (iw.left > 0 && ok) {
+            const AbsorbedSegment g = iw.segment(a.num_heads);
             // A window of 32 boxes (blocks, or 32 tokens of a larger one), one a lane; the block ids of
             // the next window are loaded while the current one is issued.
             const int32_t *table = a.block_tables + (int64_t)w.s * a.max_blocks_per_seq;
@@ -290,7 +315,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 if (++st == NST) { st = 0; ph ^= 1; }
                 w.ahead(sb);
             }
-            f += g.tiles;
+            iw.advance(sb, units, g);
         }
         if (!ok && lane == 0) {
             flag_error(a.err, PKV_DEVERR_TIMEOUT);
@@ -317,9 +342,8 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         uint32_t gq = 0;          // tiles issued
         uint32_t seg_i = 0;
         bool ok = true;
-        for (int64_t f = lo; f < hi && ok;) {
-            w.seek(sb, units, f);
-            const AbsorbedSegment g = segment_at(a, w.q, w.pre, f, hi);
+        while (iw.left > 0 && ok) {
+            const AbsorbedSegment g = iw.segment(a.num_heads);
             const int tiles = __shfl_sync(0xffffffffu, g.tiles, 0);
             ok = wait_all(&ms.q_full, seg_i & 1);
             for (int t = 0; t < tiles && ok; ++t) {
@@ -338,7 +362,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 if (++st == NST) { st = 0; ph ^= 1; }
             }
             umma_commit_warp(&ms.q_empty);
-            f += g.tiles;
+            iw.advance(sb, units, g);
             ++seg_i;
         }
         if (!ok) {
@@ -358,9 +382,8 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         const uint64_t dp = umma_desc_sw128(smem_u32(sP), 16, 1024);
         uint32_t st = 0, gv = 0, seg_i = 0, moves = 0;
         bool ok = true;
-        for (int64_t f = lo; f < hi && ok;) {
-            w.seek(sb, units, f);
-            const AbsorbedSegment g = segment_at(a, w.q, w.pre, f, hi);
+        while (iw.left > 0 && ok) {
+            const AbsorbedSegment g = iw.segment(a.num_heads);
             const int tiles = __shfl_sync(0xffffffffu, g.tiles, 0);
             const int n = __shfl_sync(0xffffffffu, (g.rows + 15) & ~15, 0);
             const uint32_t idesc_pv = umma_idesc_bf16(128, n, 1, 0);
@@ -392,7 +415,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 ++gv;
                 if (++st == NST) st = 0;
             }
-            f += g.tiles;
+            iw.advance(sb, units, g);
             ++seg_i;
         }
         if (!ok) {
@@ -457,9 +480,8 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             if (lane == 0) mbar_arrive(&ms.rescaled);
             return true;
         };
-        for (int64_t f = lo; f < hi && ok;) {
-            w.seek(sb, units, f);
-            const AbsorbedSegment g = segment_at(a, w.q, w.pre, f, hi);
+        while (iw.left > 0 && ok) {
+            const AbsorbedSegment g = iw.segment(a.num_heads);
             const int ctx = w.q.ctx;
             const bool live[2] = {ra < g.rows, ra + 8 < g.rows};
             int lim[2];  // keys the rows may see; rows past the item mask nothing
@@ -607,7 +629,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             if (lane == 0) mbar_arrive(&ms.o_free);
             // inv is written again only behind the next item's tiles, whose weights every warp's
             // arrival is part of
-            f += g.tiles;
+            iw.advance(sb, units, g);
         }
         if (!ok) {
             if (lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
