@@ -300,7 +300,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
         // The warp runs it together on uniform values; one elected lane issues.
-        const uint64_t policy = l2_policy_evict_normal();
+        const uint64_t policy = l2_policy_evict_normal(), once = l2_policy_evict_first();
         const uint32_t pairs0 = smem_u32(sPairs), rope0 = smem_u32(sRope);
         uint32_t n = 0, segs = 0;   // chunks and tiles issued
         uint32_t np = 0, nr = 0;    // pairs and rotary pieces issued
@@ -336,7 +336,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                 for (int h = 0; h < nh; ++h)
                     for (int p = 0; p < 3; ++p)
                         tma_load_4d(sQ + (h * 3 + p) * L::PIECE, &q_map, &ms.q_full, 0, p, g.h,
-                                    (int)(w.q.q0 + g.qt * kExpQTile) + h * 128, policy);
+                                    (int)(w.q.q0 + g.qt * kExpQTile) + h * 128, once);
             }
             __syncwarp();
             ++segs;
