@@ -335,65 +335,74 @@ def paged_attention_decode_kvwrite(out, q, k_new, v_new, k_cache, v_cache, block
         _check(lib().pkv_paged_attention_decode_kvwrite(*args, DTYPE_BF16, *tail), "paged_attention_decode_kvwrite")
 
 
-def _on_current_device(dev: int) -> None:
-    """The library launches on the current device: tensors of another one are refused."""
-    import torch
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensor on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+class _Tensors:
+    """The tensors a call takes, as (name, type, dimensions) each.  The calls below run in a few
+    microseconds on the GPU, so a property of all their tensors is looked at in one pass."""
+    dim = device = dtype = contiguous = ptr = current = stream = None   # torch's own, once it is there
 
+    def __init__(self, *args):
+        self.args, self.dims, self.dtypes = args, tuple(n for _, _, n in args), None
 
-def _bad_tensor(t, dtype, name, ndim, dev):
-    """The complaint about a tensor that _ptrs refused."""
-    _require(t, dtype, name, ndim)
-    raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{dev}")
+    def _bind(self):
+        import torch
+        cls, T = _Tensors, torch.Tensor
+        if cls.ptr is None:
+            cls.dim, cls.device, cls.contiguous = T.dim, T.get_device, T.is_contiguous
+            cls.dtype = T.dtype.__get__
+            cls.current, cls.stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+            cls.ptr = T.data_ptr
+        self.dtypes = tuple(getattr(torch, name) for _, name, _ in self.args)
 
-
-def _ptrs(dev, dtype, *named):
-    """Addresses of tensors given as (tensor, name, ndim), checked to be contiguous, of dtype and
-    on CUDA device dev.  The calls below run in a few microseconds on the GPU, so their checks
-    are kept to one look at each property."""
-    out = []
-    for t, name, ndim in named:
+    def check(self, *ts):
+        """(device, addresses): contiguous CUDA tensors of these types and dimensions on the current
+        device, which is where the library launches."""
+        if self.dtypes is None:
+            self._bind()
+        cls = _Tensors
         try:
-            if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or t.dim() != ndim:
-                _bad_tensor(t, dtype, name, ndim, dev)
-            out.append(t.data_ptr())
-        except AttributeError:
-            raise ValueError(f"{name} must be a CUDA tensor") from None
-    return out
+            dev, *others = set(map(cls.device, ts))
+            if (not others and dev >= 0 and tuple(map(cls.dtype, ts)) == self.dtypes
+                    and tuple(map(cls.dim, ts)) == self.dims and all(map(cls.contiguous, ts))
+                    and dev == cls.current()):
+                return dev, map(cls.ptr, ts)
+        except TypeError:
+            pass
+        self._complain(ts)
 
-
-def _device_of(t, name) -> int:
-    """The CUDA device of a call's first tensor, which has to be the current one."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    dev = t.get_device()
-    if dev != torch._C._cuda_getDevice():
-        _on_current_device(dev)
-    return dev
+    def _complain(self, ts):
+        import torch
+        for t, (name, _, dims), dtype in zip(ts, self.args, self.dtypes):
+            _require(t, dtype, name, dims)
+        for t, (name, _, _) in zip(ts, self.args):
+            if t.get_device() != torch.cuda.current_device():
+                raise ValueError(f"{name} is on {t.device}, but the current device is "
+                                 f"cuda:{torch.cuda.current_device()}")
+        raise ValueError("tensors that do not fit")
 
 
 def _raw_stream(stream, dev):
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _Tensors.stream(dev) if stream is None else stream.cuda_stream
 
 
-def _call_workspace(workspace, nbytes, dev, stream):
-    """(address, bytes, owner) of the caller's workspace (a contiguous CUDA buffer of enough
-    bytes), or of a fresh one that stays alive until `stream` is past the call."""
+def _call_workspace(workspace, dev, stream, size, *sizes):
+    """(address, bytes, owner) of the caller's workspace (a contiguous CUDA buffer; the call checks
+    that it is large enough), or of a fresh one of size(*sizes) bytes that stays alive until `stream`
+    is past the call."""
     import torch
     if workspace is None:
+        nbytes = size(*sizes)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
         if stream is not None:
             ws.record_stream(stream)
         return ws.data_ptr(), nbytes, ws
     if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
-    have = workspace.numel() * workspace.element_size()
-    if have < nbytes:
-        raise PagedKVError(-3, "workspace")
-    return workspace.data_ptr(), have, workspace
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+_STEP = _Tensors(("block_tables", "int32", 2), ("context_lens", "int32", 1), ("query_start_loc", "int32", 1),
+                 ("slot_mapping", "int64", 1), ("free_end", "int32", 1), ("cached_lens", "int32", 1),
+                 ("new_lens", "int32", 1), ("free_blocks", "int32", 1), ("free_begin", "int32", 1))
 
 
 def step_metadata(block_tables, context_lens, query_start_loc, slot_mapping, free_end, cached_lens, new_lens,
@@ -403,36 +412,32 @@ def step_metadata(block_tables, context_lens, query_start_loc, slot_mapping, fre
     query_start_loc [S + 1], free_end [1] int32, slot_mapping [room] int64 (-1 past the last
     token), and the new entries of block_tables [S, MB] int32.  context_lens may be cached_lens
     and free_end may be free_begin: a replayed call then advances its own state."""
-    import torch
-    dev = _device_of(block_tables, "block_tables")
-    bt, cl, qsl, fe, ca, ne, fb, fbeg = _ptrs(
-        dev, torch.int32, (block_tables, "block_tables", 2), (context_lens, "context_lens", 1),
-        (query_start_loc, "query_start_loc", 1), (free_end, "free_end", 1), (cached_lens, "cached_lens", 1),
-        (new_lens, "new_lens", 1), (free_blocks, "free_blocks", 1), (free_begin, "free_begin", 1))
-    sm, = _ptrs(dev, torch.int64, (slot_mapping, "slot_mapping", 1))
+    dev, ptrs = _STEP.check(block_tables, context_lens, query_start_loc, slot_mapping, free_end, cached_lens,
+                            new_lens, free_blocks, free_begin)
     S, MB = block_tables.shape
-    if new_lens.numel() != S or cached_lens.numel() != S or context_lens.numel() != S \
-            or query_start_loc.numel() != S + 1 or free_end.numel() != 1 or free_begin.numel() != 1:
+    if not (new_lens.numel() == cached_lens.numel() == context_lens.numel() == query_start_loc.numel() - 1 == S
+            and free_end.numel() == free_begin.numel() == 1):
         raise ValueError("shape mismatch")
-    st = lib().pkv_step_metadata(bt, cl, qsl, sm, fe, ca, ne, fb, fbeg, S, MB, slot_mapping.numel(),
-                                 free_blocks.numel(), num_blocks, block_size, _raw_stream(stream, dev))
+    st = lib().pkv_step_metadata(*ptrs, S, MB, slot_mapping.numel(), free_blocks.numel(), num_blocks, block_size,
+                                 _raw_stream(stream, dev))
     if st:
         raise PagedKVError(st, "step_metadata")
+
+
+_WRITE = _Tensors(("latent_cache", "bfloat16", 3), ("latent", "bfloat16", 2), ("rope", "bfloat16", 2),
+                  ("slot_mapping", "int64", 1))
 
 
 def latent_cache_write(latent_cache, latent, rope, slot_mapping, stream=None) -> None:
     """latent_cache [NB, bs, R + P] bf16 <- rows [latent ; rope] (latent [T, R], rope [T, P] bf16)
     at int64 slot_mapping [T]; negative slots are skipped."""
-    import torch
-    dev = _device_of(latent_cache, "latent_cache")
-    lc, la, ro = _ptrs(dev, torch.bfloat16, (latent_cache, "latent_cache", 3), (latent, "latent", 2), (rope, "rope", 2))
-    sm, = _ptrs(dev, torch.int64, (slot_mapping, "slot_mapping", 1))
+    dev, ptrs = _WRITE.check(latent_cache, latent, rope, slot_mapping)
     NB, bs, cols = latent_cache.shape
     T, R = latent.shape
     P = cols - R
-    if tuple(rope.shape) != (T, P) or slot_mapping.numel() != T:
+    if rope.shape != (T, P) or slot_mapping.numel() != T:
         raise ValueError("shape mismatch")
-    st = lib().pkv_latent_cache_write(lc, la, ro, sm, T, NB, bs, R, P, DTYPE_BF16, _raw_stream(stream, dev))
+    st = lib().pkv_latent_cache_write(*ptrs, T, NB, bs, R, P, DTYPE_BF16, _raw_stream(stream, dev))
     if st:
         raise PagedKVError(st, "latent_cache_write")
 
@@ -446,20 +451,12 @@ def latent_workspace_size(op: int, num_seqs: int, total_q_tokens: int, num_heads
     return int(n)
 
 
-def _latent_tensors(out, q, latent_cache, block_tables, context_lens, query_start_loc):
-    """(device, sequences, addresses) of the tensors both forms take, checked."""
-    import torch
-    dev = _device_of(q, "q")
-    po, pq, pc = _ptrs(dev, torch.bfloat16, (out, "out", 3), (q, "q", 3), (latent_cache, "latent_cache", 3))
-    pt, pl = _ptrs(dev, torch.int32, (block_tables, "block_tables", 2), (context_lens, "context_lens", 1))
-    S = context_lens.numel()
-    ps = None
-    if query_start_loc is not None:
-        ps, = _ptrs(dev, torch.int32, (query_start_loc, "query_start_loc", 1))
-    if out.shape[:2] != q.shape[:2] or block_tables.shape[0] != S \
-            or (q.shape[0] != S if query_start_loc is None else query_start_loc.numel() != S + 1):
-        raise ValueError("shape mismatch")
-    return dev, S, (po, pq, ps, pc, pt, pl)
+_LATENT_ROWS = (("q", "bfloat16", 3), ("out", "bfloat16", 3))
+_LATENT_CACHE = (("latent_cache", "bfloat16", 3), ("block_tables", "int32", 2), ("context_lens", "int32", 1))
+_QSL = ("query_start_loc", "int32", 1)
+_ABSORBED_DECODE = _Tensors(*_LATENT_ROWS, *_LATENT_CACHE)
+_ABSORBED = _Tensors(*_LATENT_ROWS, _QSL, *_LATENT_CACHE)
+_EXPANDED = _Tensors(*_LATENT_ROWS, _QSL, *_LATENT_CACHE, ("w_k", "bfloat16", 3), ("w_v", "bfloat16", 3))
 
 
 def latent_attention_absorbed(out, q, latent_cache, block_tables, context_lens, scale: float, query_start_loc=None,
@@ -468,17 +465,22 @@ def latent_attention_absorbed(out, q, latent_cache, block_tables, context_lens, 
     rotary part), out [T, H, R] bf16 (to be multiplied by W_v), latent_cache [NB, bs, R + P] bf16,
     block_tables [S, MB] int32, context_lens [S] int32.  Without query_start_loc one row per
     sequence; with it [S + 1] int32 (device), each sequence's last q_len positions."""
-    dev, S, ptrs = _latent_tensors(out, q, latent_cache, block_tables, context_lens, query_start_loc)
+    if query_start_loc is None:
+        dev, (pq, po, *rest) = _ABSORBED_DECODE.check(q, out, latent_cache, block_tables, context_lens)
+        ps = None
+    else:
+        dev, (pq, po, ps, *rest) = _ABSORBED.check(q, out, query_start_loc, latent_cache, block_tables, context_lens)
     T, H, cols = q.shape
+    To, Ho, R = out.shape
     NB, bs, ccols = latent_cache.shape
-    R = out.shape[2]
-    if ccols != cols or cols <= R:
+    S, MB = block_tables.shape
+    if (To, Ho, ccols) != (T, H, cols) or cols <= R or context_lens.numel() != S \
+            or (T != S if ps is None else query_start_loc.numel() != S + 1):
         raise ValueError("shape mismatch")
-    n = latent_workspace_size(OP_LATENT_ABSORBED, S, T, H, R, cols - R)
-    ws, have, keep = _call_workspace(workspace, n, dev, stream)
-    st = lib().pkv_latent_attention_absorbed(
-        *ptrs, S, T, block_tables.shape[1], H, R, cols - R, bs, NB, scale, bool(causal), DTYPE_BF16, ws, have,
-        _raw_stream(stream, dev))
+    ws, have, keep = _call_workspace(workspace, dev, stream, latent_workspace_size, OP_LATENT_ABSORBED, S, T, H, R,
+                                     cols - R)
+    st = lib().pkv_latent_attention_absorbed(po, pq, ps, *rest, S, T, MB, H, R, cols - R, bs, NB, scale,
+                                             bool(causal), DTYPE_BF16, ws, have, _raw_stream(stream, dev))
     if st:
         raise PagedKVError(st, "latent_attention_absorbed")
 
@@ -490,23 +492,22 @@ def latent_attention_expanded(out, q, query_start_loc, latent_cache, block_table
     bf16 (rotary part last), out [T, H, 128] bf16, query_start_loc [S + 1] int32 (device),
     latent_cache [NB, bs, R + P] bf16, w_k and w_v [H, 128, R] bf16; total_context is at least the
     sum of context_lens of the sequences with query rows (host)."""
-    import torch
     if query_start_loc is None:
         raise ValueError("query_start_loc must be a CUDA tensor")
-    dev, S, ptrs = _latent_tensors(out, q, latent_cache, block_tables, context_lens, query_start_loc)
-    pk, pv = _ptrs(dev, torch.bfloat16, (w_k, "w_k", 3), (w_v, "w_v", 3))
+    dev, (pq, po, *rest) = _EXPANDED.check(q, out, query_start_loc, latent_cache, block_tables, context_lens, w_k, w_v)
     T, H, qcols = q.shape
+    To, Ho, vdim = out.shape
     NB, bs, cols = latent_cache.shape
+    S, MB = block_tables.shape
     Hk, nope, R = w_k.shape
     P = cols - R
-    if Hk != H or w_v.shape[0] != H or w_v.shape[2] != R or out.shape[2] != w_v.shape[1] or P <= 0 \
-            or qcols != nope + P:
+    if (To, Ho) != (T, H) or Hk != H or w_v.shape != (H, vdim, R) or P <= 0 or qcols != nope + P \
+            or context_lens.numel() != S or query_start_loc.numel() != S + 1:
         raise ValueError("shape mismatch")
-    n = latent_workspace_size(OP_LATENT_EXPANDED, S, T, H, R, P, total_context)
-    ws, have, keep = _call_workspace(workspace, n, dev, stream)
-    st = lib().pkv_latent_attention_expanded(
-        *ptrs, pk, pv, S, T, total_context, block_tables.shape[1], H, R, P, nope, w_v.shape[1], bs, NB, scale,
-        bool(causal), DTYPE_BF16, ws, have, _raw_stream(stream, dev))
+    ws, have, keep = _call_workspace(workspace, dev, stream, latent_workspace_size, OP_LATENT_EXPANDED, S, T, H, R, P,
+                                     total_context)
+    st = lib().pkv_latent_attention_expanded(po, pq, *rest, S, T, total_context, MB, H, R, P, nope, vdim, bs, NB, scale,
+                                             bool(causal), DTYPE_BF16, ws, have, _raw_stream(stream, dev))
     if st:
         raise PagedKVError(st, "latent_attention_expanded")
 
