@@ -73,10 +73,10 @@ struct AbsorbedSmem {
     static_assert(NST >= 2, "two tiles in flight at least");
 };
 
-// Where a share begins: 64-row group grp of the sequence, tile kb.
+// Where a share begins: 64-row group grp of the sequence, unit `at` of the item.
 struct AbsorbedStart {
     WalkStart seq;
-    int grp, kb;
+    int grp, at;
 };
 
 struct AbsorbedMisc {
@@ -98,12 +98,19 @@ __device__ __forceinline__ uint64_t uniform_desc(uint64_t d) {
     return (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)(d >> 32), 0) << 32 | __shfl_sync(0xffffffffu, (uint32_t)d, 0);
 }
 
-// Units of a sequence: 64-row groups x 64-token tiles.
+// What an item costs besides its tiles, in tiles: its units are kItemCost ones without work, then
+// one a tile, so that a share of many short items has fewer tiles.  (Its output takes 4,000 to 6,000
+// cycles, a tile 3,300 to 4,200.  With shares of equally many tiles the slowest CTA took 1.4 times
+// another's time: 174 us for the rows of 1 to 4 tokens of 32 sequences at 128 heads, 132 with a cost
+// of 4, 135 with 6; one token of 128 sequences 65.9, 62.9, 64.5.)
+constexpr int kItemCost = 4;
+
+// Units of a sequence: 64-row groups x (64-token tiles and the item's cost).
 struct AbsorbedUnits {
     int num_heads;
     __device__ __forceinline__ int64_t operator()(const SeqInfo &q) const {
         const int64_t groups = ((int64_t)q.q_len * num_heads + kLatentRows - 1) / kLatentRows;
-        return groups * ((q.ctx + kLatentTile - 1) / kLatentTile);
+        return groups * ((q.ctx + kLatentTile - 1) / kLatentTile + kItemCost);
     }
 };
 
@@ -121,16 +128,17 @@ struct AbsorbedSegment {
 // runs before its first tile is kept short.)
 struct ItemWalk {
     SeqWalk<AbsorbedUnits> w;
-    int64_t left;  // units of the share from here on
-    int grp, kb;   // 64-row group of the sequence, its tile
-    __device__ __forceinline__ ItemWalk(const AbsorbedStart &st, int64_t units) : left(units), grp(st.grp), kb(st.kb) {
+    int64_t left;  // units of the share from here on; 0 if there is no tile among them
+    int grp, at;   // 64-row group of the sequence, unit of the item
+    __device__ __forceinline__ ItemWalk(const AbsorbedStart &st, int64_t units) : left(units), grp(st.grp), at(st.at) {
         w.start(st.seq);
+        if (at + left <= kItemCost) left = 0;
     }
     __device__ __forceinline__ AbsorbedSegment segment(int num_heads) const {
         AbsorbedSegment g;
         const int nk = (w.q.ctx + kLatentTile - 1) / kLatentTile;
-        g.kb = kb;
-        g.tiles = (int)min64(nk - kb, left);
+        g.kb = max(0, at - kItemCost);
+        g.tiles = (int)min64(nk, at + left - kItemCost) - g.kb;
         g.row_in_seq = grp * kLatentRows;
         g.row0 = (int64_t)w.q.q0 * num_heads + g.row_in_seq;
         g.rows = min(kLatentRows, w.q.q_len * num_heads - g.row_in_seq);
@@ -139,9 +147,10 @@ struct ItemWalk {
     }
     // past the segment
     __device__ __forceinline__ void advance(const SeqBatch &sb, const AbsorbedUnits &u, const AbsorbedSegment &g) {
-        left -= g.tiles;
-        kb = 0;
-        if (++grp * kLatentRows < w.q.q_len * u.num_heads || left <= 0) return;
+        left -= g.kb + g.tiles + kItemCost - at;
+        at = 0;
+        if (left <= kItemCost) left = 0;
+        if (++grp * kLatentRows < w.q.q_len * u.num_heads || left == 0) return;
         grp = 0;
         w.seek(sb, u, w.pre + w.units);
     }
@@ -204,9 +213,10 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
     const bool works = T > 0 && c < ge;
     const int64_t lo = works ? quotient(c * T, ge) : 0, hi = works ? quotient((c + 1) * T, ge) : 0;
     if (works && find_unit(sb, units, sc, 0, lo, &ms.start.seq)) {
-        const int64_t nk = (ms.start.seq.q.ctx + kLatentTile - 1) / kLatentTile, o = lo - ms.start.seq.pre;
-        ms.start.grp = (int)quotient(o, nk);
-        ms.start.kb = (int)(o - ms.start.grp * nk);
+        const int64_t n = (ms.start.seq.q.ctx + kLatentTile - 1) / kLatentTile + kItemCost;
+        const int64_t o = lo - ms.start.seq.pre, grp = quotient(o, n);
+        ms.start.grp = (int)grp;
+        ms.start.at = (int)(o - grp * n);
     }
     tc_fence_before();
     __syncthreads();
@@ -220,8 +230,9 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             if (works && c > 0) {
                 const SeqInfo q = ms.start.seq.q;
                 const int grp = ms.start.grp, nk = (q.ctx + kLatentTile - 1) / kLatentTile;
-                const int64_t begin = lo - ms.start.kb;
-                if (begin != lo && begin >= quotient((c - 1) * T, ge)) {
+                const int kb = ms.start.at - kItemCost;
+                const int64_t begin = lo - kb;  // the item's first tile
+                if (kb > 0 && begin >= quotient((c - 1) * T, ge)) {
                     j.out_off = ((int64_t)q.q0 * a.num_heads + grp * kLatentRows) * R;
                     j.c0 = c - 1;
                     j.c1 = share_owner(begin + nk - 1, T, ge);
