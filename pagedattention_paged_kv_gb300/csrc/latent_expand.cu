@@ -17,8 +17,10 @@
 // columns a CTA, half of TMEM) is double-buffered, so the stores of one head run under the
 // products of the next.  Units are (pair of token tiles, head), cut into equal contiguous
 // shares, so a pair reloads its tokens only when its share crosses tiles.
-// Measured at 16,896 tokens x 64 heads, R = 512 (283 GFLOP): 292 us for single CTAs, 228 with
-// every chunk's halves multicast to both CTAs of a cluster.
+// Measured at 16,896 tokens x 64 heads, R = 512 (283 GFLOP, 554 MB written): 292 us for single
+// CTAs, 228 with every chunk's halves multicast to both CTAs of a cluster, 212 as pairs, some 175 with
+// the epilogue on eight warps that store whole lines (5,700 cycles a unit, 4,100 of them products;
+// the rest is waits for weight chunks, as weights and stores take 34 bytes a cycle of every SM).
 // Waits are bounded in time.  The CTAs of a pair (always resident together) wait for each other;
 // no pair waits for another.
 #include "attn_block.cuh"

@@ -8,7 +8,8 @@
 //
 // Bound: L2, which holds the parts just written.  A thread has 4 columns of kJoinRows rows, and
 // the loads of four parts of each are in flight together: with one row a thread and a (job, row)
-// grid the join of 128 items of 64 x 512 took 15 us behind its kernel, so 11.
+// grid the join of 128 items of 64 x 512 took 15 us behind its kernel, so 11 (12 alone with an
+// empty L2).  Registers for three CTAs an SM without a spill: 16 bytes of it cost 5 to 10 us.
 #pragma once
 
 #include "attn_block.cuh"

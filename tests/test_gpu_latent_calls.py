@@ -125,6 +125,29 @@ def test_graphs_that_share_a_workspace():
     assert pkv.get_device_error() == 0
 
 
+@pytest.mark.parametrize("heads,latent", [(3, 256), (16, 512)])
+def test_what_the_workspace_held_has_no_effect(heads, latent):
+    """NaN everywhere in it, contexts around the sizes of tiles and chunks, room to spare."""
+    ctx = [1, 95, 96, 97, 127, 128, 129, 191, 192, 193, 255, 256, 257, 288, 289, 384, 385, 500, 128]
+    ql = [1, 95, 1, 97, 64, 128, 129, 2, 192, 193, 255, 256, 1, 288, 33, 384, 300, 257, 128]
+    e = Batch(ctx, ql, heads, latent, 128 + ROPE, seed=11)
+    w = weights(heads, latent, 12)
+    n = pkv.latent_workspace_size(pkv.OP_LATENT_EXPANDED, len(ctx), e.q.shape[0], heads, latent, ROPE,
+                                  total_context=sum(ctx) + 1000)
+    for causal in (True, False):
+        ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+        out = torch.full((e.q.shape[0], heads, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+        pkv.latent_attention_expanded(out, e.q, e.qsl, e.cache, e.tables, e.context_lens, *w, SCALE, sum(ctx) + 1000,
+                                      causal=causal, workspace=ws)
+        assert pkv.get_device_error() == 0
+        check(out, *expanded_reference(e, *w, causal=causal), f"causal {causal}")
+    a = Batch(ctx, ql, heads, latent, latent + ROPE, seed=13)
+    ws = workspace(pkv.OP_LATENT_ABSORBED, a).fill_(0xFF)
+    out = absorbed(a, workspace=ws)
+    assert pkv.get_device_error() == 0
+    check(out, *absorbed_reference(a))
+
+
 @pytest.mark.parametrize("form", ["absorbed", "expanded"])
 def test_a_wait_that_runs_out_flags_timeout_and_returns(form):
     cols = 512 if form == "absorbed" else 128
