@@ -36,7 +36,7 @@ __device__ __forceinline__ SeqRaw fetch_seq(const SeqBatch &b, int s) {
     return r;
 }
 
-__device__ __forceinline__ SeqInfo judge_seq(const SeqBatch &b, const SeqRaw &w, bool report) {
+__device__ __forceinline__ SeqInfo vet_seq(const SeqBatch &b, const SeqRaw &w, bool report) {
     SeqInfo r;
     r.q0 = w.q0;
     r.q_len = 0;
@@ -61,7 +61,7 @@ __device__ __forceinline__ SeqInfo judge_seq(const SeqBatch &b, const SeqRaw &w,
 }
 
 __device__ __forceinline__ SeqInfo read_seq(const SeqBatch &b, int s, bool report) {
-    return judge_seq(b, fetch_seq(b, s), report);
+    return vet_seq(b, fetch_seq(b, s), report);
 }
 
 // Units(const SeqInfo &) -> int64_t gives the work units of a live sequence.
@@ -191,7 +191,7 @@ struct SeqWalk {
     __device__ __forceinline__ void look(const SeqBatch &b, const Units &u) {
         if (!fresh) return;
         fresh = false;
-        mine = judge_seq(b, raw, false);
+        mine = vet_seq(b, raw, false);
         my_units = mine.q_len > 0 && !mine.dead ? u(mine) : 0;
     }
     __device__ __forceinline__ void take(int l) {
