@@ -337,47 +337,48 @@ def paged_attention_decode_kvwrite(out, q, k_new, v_new, k_cache, v_cache, block
 
 class _Tensors:
     """The tensors a call takes, as (name, type, dimensions) each.  The calls below run in a few
-    microseconds on the GPU, so a property of all their tensors is looked at in one pass."""
-    dim = device = dtype = contiguous = ptr = current = stream = None   # torch's own, once it is there
+    microseconds on the GPU, so a property of all their tensors is looked at in one pass, and their
+    dimensions where their sizes are."""
+    device = dtype = contiguous = ptr = current = stream = None   # torch's own, once it is there
 
     def __init__(self, *args):
-        self.args, self.dims, self.dtypes = args, tuple(n for _, _, n in args), None
+        self.args, self.dtypes = args, None
 
     def _bind(self):
         import torch
         cls, T = _Tensors, torch.Tensor
         if cls.ptr is None:
-            cls.dim, cls.device, cls.contiguous = T.dim, T.get_device, T.is_contiguous
+            cls.device, cls.contiguous = T.get_device, T.is_contiguous
             cls.dtype = T.dtype.__get__
             cls.current, cls.stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
             cls.ptr = T.data_ptr
         self.dtypes = tuple(getattr(torch, name) for _, name, _ in self.args)
 
     def check(self, *ts):
-        """(device, addresses): contiguous CUDA tensors of these types and dimensions on the current
-        device, which is where the library launches."""
+        """(device, addresses): contiguous CUDA tensors of these types on the current device, which is
+        where the library launches."""
         if self.dtypes is None:
             self._bind()
         cls = _Tensors
         try:
             dev, *others = set(map(cls.device, ts))
             if (not others and dev >= 0 and tuple(map(cls.dtype, ts)) == self.dtypes
-                    and tuple(map(cls.dim, ts)) == self.dims and all(map(cls.contiguous, ts))
-                    and dev == cls.current()):
+                    and all(map(cls.contiguous, ts)) and dev == cls.current()):
                 return dev, map(cls.ptr, ts)
         except TypeError:
             pass
-        self._complain(ts)
+        raise self.complaint(*ts)
 
-    def _complain(self, ts):
+    def complaint(self, *ts):
+        """The error that says what is wrong with tensors that do not fit."""
         import torch
         for t, (name, _, dims), dtype in zip(ts, self.args, self.dtypes):
             _require(t, dtype, name, dims)
         for t, (name, _, _) in zip(ts, self.args):
             if t.get_device() != torch.cuda.current_device():
-                raise ValueError(f"{name} is on {t.device}, but the current device is "
-                                 f"cuda:{torch.cuda.current_device()}")
-        raise ValueError("tensors that do not fit")
+                return ValueError(f"{name} is on {t.device}, but the current device is "
+                                  f"cuda:{torch.cuda.current_device()}")
+        return ValueError("shape mismatch")
 
 
 def _raw_stream(stream, dev):
@@ -412,12 +413,17 @@ def step_metadata(block_tables, context_lens, query_start_loc, slot_mapping, fre
     query_start_loc [S + 1], free_end [1] int32, slot_mapping [room] int64 (-1 past the last
     token), and the new entries of block_tables [S, MB] int32.  context_lens may be cached_lens
     and free_end may be free_begin: a replayed call then advances its own state."""
-    dev, ptrs = _STEP.check(block_tables, context_lens, query_start_loc, slot_mapping, free_end, cached_lens,
-                            new_lens, free_blocks, free_begin)
-    S, MB = block_tables.shape
-    if not (new_lens.numel() == cached_lens.numel() == context_lens.numel() == query_start_loc.numel() - 1 == S
-            and free_end.numel() == free_begin.numel() == 1):
-        raise ValueError("shape mismatch")
+    ts = (block_tables, context_lens, query_start_loc, slot_mapping, free_end, cached_lens, new_lens, free_blocks,
+          free_begin)
+    dev, ptrs = _STEP.check(*ts)
+    try:
+        S, MB = block_tables.shape
+        fits = (new_lens.numel() == cached_lens.numel() == context_lens.numel() == query_start_loc.numel() - 1 == S
+                and free_end.numel() == free_begin.numel() == 1)
+    except ValueError:
+        fits = False
+    if not fits:
+        raise _STEP.complaint(*ts)
     st = lib().pkv_step_metadata(*ptrs, S, MB, slot_mapping.numel(), free_blocks.numel(), num_blocks, block_size,
                                  _raw_stream(stream, dev))
     if st:
@@ -431,12 +437,17 @@ _WRITE = _Tensors(("latent_cache", "bfloat16", 3), ("latent", "bfloat16", 2), ("
 def latent_cache_write(latent_cache, latent, rope, slot_mapping, stream=None) -> None:
     """latent_cache [NB, bs, R + P] bf16 <- rows [latent ; rope] (latent [T, R], rope [T, P] bf16)
     at int64 slot_mapping [T]; negative slots are skipped."""
-    dev, ptrs = _WRITE.check(latent_cache, latent, rope, slot_mapping)
-    NB, bs, cols = latent_cache.shape
-    T, R = latent.shape
-    P = cols - R
-    if rope.shape != (T, P) or slot_mapping.numel() != T:
-        raise ValueError("shape mismatch")
+    ts = (latent_cache, latent, rope, slot_mapping)
+    dev, ptrs = _WRITE.check(*ts)
+    try:
+        NB, bs, cols = latent_cache.shape
+        T, R = latent.shape
+        P = cols - R
+        fits = rope.shape == (T, P) and slot_mapping.numel() == T
+    except ValueError:
+        fits = False
+    if not fits:
+        raise _WRITE.complaint(*ts)
     st = lib().pkv_latent_cache_write(*ptrs, T, NB, bs, R, P, DTYPE_BF16, _raw_stream(stream, dev))
     if st:
         raise PagedKVError(st, "latent_cache_write")
@@ -466,17 +477,22 @@ def latent_attention_absorbed(out, q, latent_cache, block_tables, context_lens, 
     block_tables [S, MB] int32, context_lens [S] int32.  Without query_start_loc one row per
     sequence; with it [S + 1] int32 (device), each sequence's last q_len positions."""
     if query_start_loc is None:
-        dev, (pq, po, *rest) = _ABSORBED_DECODE.check(q, out, latent_cache, block_tables, context_lens)
-        ps = None
+        kinds, ts, ps = _ABSORBED_DECODE, (q, out, latent_cache, block_tables, context_lens), None
+        dev, (pq, po, *rest) = kinds.check(*ts)
     else:
-        dev, (pq, po, ps, *rest) = _ABSORBED.check(q, out, query_start_loc, latent_cache, block_tables, context_lens)
-    T, H, cols = q.shape
-    To, Ho, R = out.shape
-    NB, bs, ccols = latent_cache.shape
-    S, MB = block_tables.shape
-    if (To, Ho, ccols) != (T, H, cols) or cols <= R or context_lens.numel() != S \
-            or (T != S if ps is None else query_start_loc.numel() != S + 1):
-        raise ValueError("shape mismatch")
+        kinds, ts = _ABSORBED, (q, out, query_start_loc, latent_cache, block_tables, context_lens)
+        dev, (pq, po, ps, *rest) = kinds.check(*ts)
+    try:
+        T, H, cols = q.shape
+        To, Ho, R = out.shape
+        NB, bs, ccols = latent_cache.shape
+        S, MB = block_tables.shape
+        fits = ((To, Ho, ccols) == (T, H, cols) and cols > R and context_lens.numel() == S
+                and (T == S if ps is None else query_start_loc.numel() == S + 1))
+    except ValueError:
+        fits = False
+    if not fits:
+        raise kinds.complaint(*ts)
     ws, have, keep = _call_workspace(workspace, dev, stream, latent_workspace_size, OP_LATENT_ABSORBED, S, T, H, R,
                                      cols - R)
     st = lib().pkv_latent_attention_absorbed(po, pq, ps, *rest, S, T, MB, H, R, cols - R, bs, NB, scale,
@@ -494,16 +510,21 @@ def latent_attention_expanded(out, q, query_start_loc, latent_cache, block_table
     sum of context_lens of the sequences with query rows (host)."""
     if query_start_loc is None:
         raise ValueError("query_start_loc must be a CUDA tensor")
-    dev, (pq, po, *rest) = _EXPANDED.check(q, out, query_start_loc, latent_cache, block_tables, context_lens, w_k, w_v)
-    T, H, qcols = q.shape
-    To, Ho, vdim = out.shape
-    NB, bs, cols = latent_cache.shape
-    S, MB = block_tables.shape
-    Hk, nope, R = w_k.shape
-    P = cols - R
-    if (To, Ho) != (T, H) or Hk != H or w_v.shape != (H, vdim, R) or P <= 0 or qcols != nope + P \
-            or context_lens.numel() != S or query_start_loc.numel() != S + 1:
-        raise ValueError("shape mismatch")
+    ts = (q, out, query_start_loc, latent_cache, block_tables, context_lens, w_k, w_v)
+    dev, (pq, po, *rest) = _EXPANDED.check(*ts)
+    try:
+        T, H, qcols = q.shape
+        To, Ho, vdim = out.shape
+        NB, bs, cols = latent_cache.shape
+        S, MB = block_tables.shape
+        Hk, nope, R = w_k.shape
+        P = cols - R
+        fits = ((To, Ho, Hk) == (T, H, H) and w_v.shape == (H, vdim, R) and P > 0 and qcols == nope + P
+                and context_lens.numel() == S and query_start_loc.numel() == S + 1)
+    except ValueError:
+        fits = False
+    if not fits:
+        raise _EXPANDED.complaint(*ts)
     ws, have, keep = _call_workspace(workspace, dev, stream, latent_workspace_size, OP_LATENT_EXPANDED, S, T, H, R, P,
                                      total_context)
     st = lib().pkv_latent_attention_expanded(po, pq, *rest, S, T, total_context, MB, H, R, P, nope, vdim, bs, NB, scale,

@@ -269,3 +269,18 @@ def test_a_prompt_and_the_decode_steps_behind_it():
         assert rms <= 2 * 2.0 ** -8, f"step {i}: {rms}"
     assert pkv.get_device_error() == 0
     assert lens.tolist() == [p + steps for p in prompt]
+
+
+def test_the_complaint_names_the_tensor_and_what_is_wrong():
+    b = Batch([40, 9], [2, 1], 8, 256, 256 + ROPE)
+    out = torch.zeros(3, 8, 256, dtype=torch.bfloat16, device="cuda")
+    for at, value, said in ((0, out.view(24, 256), "out must have 3 dims"), (1, b.q[:, ::2], "q must be contiguous"),
+                            (2, b.cache.float(), "latent_cache must be torch.bfloat16"),
+                            (3, b.tables.view(-1), "block_tables must have 2 dims"),
+                            (3, b.tables.cpu(), "block_tables must be a CUDA tensor"),
+                            (4, b.context_lens[:1], "shape mismatch")):
+        args = [out, b.q, b.cache, b.tables, b.context_lens]
+        args[at] = value
+        with pytest.raises(ValueError, match=said):
+            pkv.latent_attention_absorbed(*args, SCALE, query_start_loc=b.qsl)
+    assert pkv.get_device_error() == 0 and not out.any()
