@@ -6,10 +6,10 @@
 //     out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p,
 // exact, as every part's weights are relative to its own m_p.
 //
-// Bound: L2, which holds the parts just written.  A thread has 4 columns of kJoinRows rows, and
-// the loads of four parts of each are in flight together: with one row a thread and a (job, row)
-// grid the join of 128 items of 64 x 512 took 15 us behind its kernel, so 11 (12 alone with an
-// empty L2).  Registers for three CTAs an SM without a spill: 16 bytes of it cost 5 to 10 us.
+// Bound: latency of the L2, which holds the parts just written.  A thread has 4 columns of one row and
+// the loads of three parts of it in flight, five CTAs an SM: most items have two or three parts, and
+// four parts of two rows a thread (three CTAs an SM) took 1 us more of 11 for 128 items of 64 x 512.
+// One 32k context of 23 parts likes four or six in flight better, by less than that.
 #pragma once
 
 #include "attn_block.cuh"
@@ -23,92 +23,70 @@ struct LatentJob {
     int32_t c0, c1, rows;
 };
 
-constexpr int kJoinRows = 2;
-
 // A CTA has at most one part that begins inside its item, and one that begins with it.
 __device__ __forceinline__ int latent_slot(int c, bool begins) { return 2 * c + begins; }
 
 // Parts lie as [2 * grid][SLOT_ROWS] (m, l) and [2 * grid][SLOT_ROWS][D] o.  BARE: a part that
 // saw nothing of a row (m = -inf) need not have left an output there.
 template <int D, int SLOT_ROWS, bool BARE>
-__global__ void __launch_bounds__(256, 3)
+__global__ void __launch_bounds__(256, 5)
 latent_merge_kernel(const LatentJob *jobs, const float2 *ws_ml, const float *ws_o, __nv_bfloat16 *out,
                     int64_t out_stride) {
     constexpr int CG = D / 4, SETS = 256 / CG;  // threads of a row, rows side by side
-    constexpr int U = 4;                        // parts in flight
+    constexpr int U = 3;                        // parts in flight
     pdl_wait();
     const LatentJob j = jobs[blockIdx.x];
-    if (j.c0 < 0) return;
+    const int cg = threadIdx.x % CG, row = blockIdx.y * SETS + threadIdx.x / CG;
+    if (j.c0 < 0 || row >= j.rows) return;
     const int nparts = j.c1 - j.c0 + 1;
-    const int cg = threadIdx.x % CG, row0 = blockIdx.y * (SETS * kJoinRows) + threadIdx.x / CG;
-    float M[kJoinRows], Ls[kJoinRows];
-    float4 acc[kJoinRows];
-#pragma unroll
-    for (int k = 0; k < kJoinRows; ++k) {
-        M[k] = -INFINITY;
-        Ls[k] = 0.f;
-        acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p0 = 0; p0 < nparts; p0 += U) {
-        float2 ml[U][kJoinRows];
-        float4 o[U][kJoinRows];
+        float2 ml[U];
+        float4 o[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int p = min(p0 + u, nparts - 1);
-            const int64_t slot = latent_slot(j.c0 + p, p == 0);
-#pragma unroll
-            for (int k = 0; k < kJoinRows; ++k) {
-                const int row = row0 + k * SETS;
-                ml[u][k] = make_float2(-INFINITY, 0.f);
-                o[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (p0 + u < nparts && row < j.rows) {
-                    ml[u][k] = __ldcg(ws_ml + slot * SLOT_ROWS + row);
-                    o[u][k] = __ldcg(reinterpret_cast<const float4 *>(ws_o + (slot * SLOT_ROWS + row) * D) + cg);
-                    if (BARE && ml[u][k].x == -INFINITY) o[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                }
+            ml[u] = make_float2(-INFINITY, 0.f);
+            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int p = p0 + u;
+            if (p < nparts) {
+                const int64_t at = (int64_t)latent_slot(j.c0 + p, p == 0) * SLOT_ROWS + row;
+                ml[u] = __ldcg(ws_ml + at);
+                o[u] = __ldcg(reinterpret_cast<const float4 *>(ws_o + at * D) + cg);
+                if (BARE && ml[u].x == -INFINITY) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
+        float mc = M;
 #pragma unroll
-        for (int k = 0; k < kJoinRows; ++k) {
-            float mc = M[k];
+        for (int u = 0; u < U; ++u) mc = fmaxf(mc, ml[u].x);
+        const float base = mc == -INFINITY ? 0.f : mc;  // nothing seen yet
+        const float s = fast_exp2(M - base);
+        M = mc;
+        L *= s;
+        acc.x *= s;
+        acc.y *= s;
+        acc.z *= s;
+        acc.w *= s;
 #pragma unroll
-            for (int u = 0; u < U; ++u) mc = fmaxf(mc, ml[u][k].x);
-            const float base = mc == -INFINITY ? 0.f : mc;  // nothing seen yet
-            const float s = fast_exp2(M[k] - base);
-            M[k] = mc;
-            Ls[k] *= s;
-            acc[k].x *= s;
-            acc[k].y *= s;
-            acc[k].z *= s;
-            acc[k].w *= s;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float w = fast_exp2(ml[u][k].x - base);
-                Ls[k] = fmaf(w, ml[u][k].y, Ls[k]);
-                acc[k].x = fmaf(w, o[u][k].x, acc[k].x);
-                acc[k].y = fmaf(w, o[u][k].y, acc[k].y);
-                acc[k].z = fmaf(w, o[u][k].z, acc[k].z);
-                acc[k].w = fmaf(w, o[u][k].w, acc[k].w);
-            }
+        for (int u = 0; u < U; ++u) {
+            const float w = fast_exp2(ml[u].x - base);
+            L = fmaf(w, ml[u].y, L);
+            acc.x = fmaf(w, o[u].x, acc.x);
+            acc.y = fmaf(w, o[u].y, acc.y);
+            acc.z = fmaf(w, o[u].z, acc.z);
+            acc.w = fmaf(w, o[u].w, acc.w);
         }
     }
-#pragma unroll
-    for (int k = 0; k < kJoinRows; ++k) {
-        const int row = row0 + k * SETS;
-        if (row >= j.rows) continue;
-        const float inv = Ls[k] > 0.f ? 1.f / Ls[k] : 0.f;
-        const uint2 v = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
-                                   pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
-        reinterpret_cast<uint2 *>(out + j.out_off + row * out_stride)[cg] = v;
-    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    reinterpret_cast<uint2 *>(out + j.out_off + row * out_stride)[cg] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 template <int D, int SLOT_ROWS, bool BARE>
 cudaError_t launch_latent_merge(const LatentJob *jobs, const float2 *ws_ml, const float *ws_o, __nv_bfloat16 *out,
                                 int64_t out_stride, int grid, cudaStream_t stream) {
-    constexpr int per = 256 / (D / 4) * kJoinRows;
-    return launch_pdl(latent_merge_kernel<D, SLOT_ROWS, BARE>, dim3(grid, SLOT_ROWS / per), dim3(256), 0, stream, jobs,
-                      ws_ml, ws_o, out, out_stride);
+    return launch_pdl(latent_merge_kernel<D, SLOT_ROWS, BARE>, dim3(grid, SLOT_ROWS * (D / 4) / 256), dim3(256), 0,
+                      stream, jobs, ws_ml, ws_o, out, out_stride);
 }
 
 }  // namespace pkv
