@@ -290,7 +290,7 @@ namespace pkv {
 int current_device(DeviceFacts *out) {
     DeviceInfo *d = nullptr;
     const int st = device_info(&d);
-    if (st == PKV_OK) *out = DeviceFacts{d->sms, d->smem_optin, d->err};
+    if (st == PKV_OK) *out = DeviceFacts{d->sms, d->err};
     return st;
 }
 

@@ -12,7 +12,6 @@ namespace pkv {
 // Facts of the current device and its error word, looked up once per device.
 struct DeviceFacts {
     int sms;
-    int smem_optin;
     int *err;
 };
 int current_device(DeviceFacts *out);  // PKV_OK or PKV_ERR_CUDA
@@ -25,6 +24,5 @@ int encode_tiled(CUtensorMap *map, int rank, const void *base, const uint64_t *d
 uint64_t wait_limit_ns();  // pkv_set_wait_limit_ns
 
 inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-inline size_t round_up_to(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace pkv

@@ -30,7 +30,7 @@
 //    by half.
 //
 // Measured, with the join: one token of 128 sequences of 500 to 2500 tokens, 64 heads, R = 512:
-// 63 us, 3.8 TB/s of what has to be read; 1 to 4 tokens of 32 sequences at 128 heads 132 us.  Two
+// 62 us, 3.9 TB/s of what has to be read; 1 to 4 tokens of 32 sequences at 128 heads 130 us.  Two
 // tiles of 72 KiB are all that fits beside Q, and a stage is loading for about 5,000 of 8,400 cycles
 // at one item a sequence (the rest are its two products and the weights between them): that, the
 // 9,000 cycles before the first tile and the join are what is left to the floor of 36 us.
@@ -98,10 +98,6 @@ struct AbsorbedMisc {
     float inv[kLatentRows];
 };
 static_assert(sizeof(AbsorbedMisc) <= 2048, "fits its place");
-
-__device__ __forceinline__ uint64_t uniform_desc(uint64_t d) {
-    return (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)(d >> 32), 0) << 32 | __shfl_sync(0xffffffffu, (uint32_t)d, 0);
-}
 
 // What an item costs besides its tiles, in tiles: its units are kItemCost ones without work, then
 // one a tile, so that a share of many short items has fewer tiles.  (Its output takes 4,000 to 6,000

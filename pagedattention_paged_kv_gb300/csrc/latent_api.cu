@@ -17,7 +17,6 @@ cudaError_t launch_latent_cache_write(void *cache, const void *latent, const voi
 }
 
 using pkv::aligned_to;
-using pkv::round_up_to;
 
 namespace {
 

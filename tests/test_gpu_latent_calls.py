@@ -225,7 +225,8 @@ def test_a_prompt_and_the_decode_steps_behind_it():
 
     # decode: the queries' latents and the outputs are rounded to bf16 by the projections outside
     slots1 = torch.zeros(S, dtype=torch.int64, device="cuda")
-    lat1, rope1 = torch.zeros(S, R, dtype=torch.bfloat16, device="cuda"), torch.zeros(S, ROPE, dtype=torch.bfloat16, device="cuda")
+    lat1 = torch.zeros(S, R, dtype=torch.bfloat16, device="cuda")
+    rope1 = torch.zeros(S, ROPE, dtype=torch.bfloat16, device="cuda")
     qa = torch.zeros(S, H, R + ROPE, dtype=torch.bfloat16, device="cuda")
     oa = torch.zeros(S, H, R, dtype=torch.bfloat16, device="cuda")
     ws = torch.empty(pkv.latent_workspace_size(pkv.OP_LATENT_ABSORBED, S, S, H, R, ROPE), dtype=torch.uint8,
