@@ -401,6 +401,7 @@ int pkv_latent_attention_absorbed(void *out, const void *q, const int32_t *query
  * (total_context + 127 num_seqs, rounded down to 128) is refused on the device
  * (PKV_DEVERR_CONTEXT_LEN, all rows zero).  The softmax weights are rounded to fp16; a finite
  * value W_v[h] c_j beyond +-65504 is clamped there and flagged PKV_DEVERR_VALUE.
+ * Cache rows that are not finite act as in the absorbed form.
  * Supported: latent_dim, rope_dim, block_size and dtype as for the absorbed form, nope_dim =
  * v_dim = 128, num_heads * (total_context + 127 num_seqs) < 2^29 - 128.
  * Workspace: pkv_latent_workspace_size(PKV_OP_LATENT_EXPANDED, ...): 512 bytes a (head, token)
