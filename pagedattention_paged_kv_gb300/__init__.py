@@ -381,20 +381,28 @@ class _Tensors:
         return ValueError("shape mismatch")
 
 
+def _fresh(nbytes, device, stream):
+    """A buffer for one call on `stream` (None: the current one), taken from that stream's pool: a
+    block that another stream's pool hands out may still be in use by kernels queued there, and one
+    given back on this stream is handed out again behind the call only."""
+    import torch
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _raw_stream(stream, dev):
     return _Tensors.stream(dev) if stream is None else stream.cuda_stream
 
 
 def _call_workspace(workspace, dev, stream, size, *sizes):
     """(address, bytes, owner) of the caller's workspace (a contiguous CUDA buffer; the call checks
-    that it is large enough), or of a fresh one of size(*sizes) bytes that stays alive until `stream`
-    is past the call."""
+    that it is large enough), or of a fresh one of size(*sizes) bytes from `stream`'s own pool."""
     import torch
     if workspace is None:
         nbytes = size(*sizes)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
-        if stream is not None:
-            ws.record_stream(stream)
+        ws = _fresh(nbytes, torch.device("cuda", dev), stream)
         return ws.data_ptr(), nbytes, ws
     if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
