@@ -183,10 +183,20 @@ def workspace_size(op: int, num_seqs: int, total_q_tokens: int, num_heads: int, 
     return int(n)
 
 
-def _workspace(workspace, nbytes, device):
+def _fresh(nbytes, device, stream):
+    """A buffer for one call on `stream` (None: the current one), taken from that stream's pool: a
+    block that another stream's pool hands out may still be in use by kernels queued there, and one
+    given back on this stream is handed out again behind the call only."""
     import torch
-    if workspace is None:
+    if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _workspace(workspace, nbytes, device, stream):
+    if workspace is None:
+        return _fresh(nbytes, device, stream)
     if workspace.numel() * workspace.element_size() < nbytes:
         raise PagedKVError(-3, "workspace")
     return workspace
@@ -209,7 +219,7 @@ def paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens,
             or block_tables.shape[0] != S or context_lens.shape[0] != S:
         raise ValueError("shape mismatch")
     nbytes = workspace_size(OP_DECODE, S, S, Hq, Hkv, d, bs)
-    ws = _workspace(workspace, nbytes, q.device)
+    ws = _workspace(workspace, nbytes, q.device, stream)
     _check(lib().pkv_paged_attention_decode(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
         S, block_tables.shape[1], Hq, Hkv, d, bs, NB, float(scale), DTYPE_BF16, _ptr(ws),
@@ -254,7 +264,7 @@ def paged_attention_decode_fp8(out, q, k_cache, v_cache, block_tables, context_l
             or block_tables.shape[0] != S or context_lens.shape[0] != S:
         raise ValueError("shape mismatch")
     nbytes = workspace_size(OP_DECODE, S, S, Hq, Hkv, d, bs)
-    ws = _workspace(workspace, nbytes, q.device)
+    ws = _workspace(workspace, nbytes, q.device, stream)
     _check(lib().pkv_paged_attention_decode_fp8(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
         S, block_tables.shape[1], Hq, Hkv, d, bs, NB, float(scale), float(k_scale), float(v_scale),
@@ -288,7 +298,7 @@ def paged_attention_varlen(out, q, query_start_loc, k_cache, v_cache, block_tabl
     if max_q_len is None:
         max_q_len = int((query_start_loc[1:] - query_start_loc[:-1]).max().item()) if S else 0
     nbytes = workspace_size(OP_VARLEN, S, total_q, Hq, Hkv, d, bs)
-    ws = _workspace(workspace, nbytes, q.device)
+    ws = _workspace(workspace, nbytes, q.device, stream)
     args = [_ptr(out), _ptr(q), _ptr(query_start_loc), _ptr(k_cache), _ptr(v_cache),
             _ptr(block_tables), _ptr(context_lens), S, total_q, int(max_q_len), block_tables.shape[1],
             Hq, Hkv, d, bs, NB, float(scale), int(bool(causal))]
@@ -324,7 +334,7 @@ def paged_attention_decode_kvwrite(out, q, k_new, v_new, k_cache, v_cache, block
     if fp8 and (k_scale is None or v_scale is None):
         raise ValueError("an FP8 cache needs k_scale and v_scale")
     nbytes = workspace_size(OP_DECODE, S, S, Hq, Hkv, d, bs)
-    ws = _workspace(workspace, nbytes, q.device)
+    ws = _workspace(workspace, nbytes, q.device, stream)
     args = [_ptr(out), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
             _ptr(context_lens), S, block_tables.shape[1], Hq, Hkv, d, bs, NB, float(scale)]
     tail = [_ptr(ws), ws.numel() * ws.element_size(), _stream_ptr(stream)]
@@ -379,17 +389,6 @@ class _Tensors:
                 return ValueError(f"{name} is on {t.device}, but the current device is "
                                   f"cuda:{torch.cuda.current_device()}")
         return ValueError("shape mismatch")
-
-
-def _fresh(nbytes, device, stream):
-    """A buffer for one call on `stream` (None: the current one), taken from that stream's pool: a
-    block that another stream's pool hands out may still be in use by kernels queued there, and one
-    given back on this stream is handed out again behind the call only."""
-    import torch
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _raw_stream(stream, dev):

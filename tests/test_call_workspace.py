@@ -43,3 +43,37 @@ def test_a_latent_call_s_fresh_workspace_belongs_to_its_stream(made, stream):
     at, have, keep = pkv._call_workspace(None, 0, stream, lambda a, b: a + b, 100, 28)
     assert (at, have) == (4096, 128) and isinstance(keep, Buffer)
     assert made == [(128, "the current stream" if stream is None else stream)]
+
+
+class Tensor:
+    """What a paged call reads of a tensor before it launches."""
+    dtype, device = torch.bfloat16, "cuda:0"
+
+    def __init__(self, *shape):
+        self.shape = torch.Size(shape)
+
+    def __getitem__(self, i):
+        return self
+
+    def data_ptr(self):
+        return 4096
+
+
+@pytest.mark.parametrize("stream", [types.SimpleNamespace(cuda_stream=7)])
+@pytest.mark.parametrize("call", ["decode", "decode_fp8", "varlen", "decode_kvwrite"])
+def test_a_paged_call_s_fresh_workspace_belongs_to_its_stream(made, monkeypatch, call, stream):
+    monkeypatch.setattr(pkv, "_require", lambda *a, **kw: None)
+    monkeypatch.setattr(pkv, "workspace_size", lambda *a: 512)
+    monkeypatch.setattr(Buffer, "numel", lambda self: 512, raising=False)
+    monkeypatch.setattr(Buffer, "element_size", lambda self: 1, raising=False)
+    launched = []
+    monkeypatch.setattr(pkv, "lib", lambda: type("L", (), {"__getattr__": lambda s, n: lambda *a: launched.append(n) or 0})())
+    q, cache, tables, lens = Tensor(4, 8, 128), Tensor(9, 16, 2, 128), Tensor(4, 3), Tensor(4)
+    rows = Tensor(4, 2, 128)
+    {"decode": lambda: pkv.paged_attention_decode(q, q, cache, cache, tables, lens, 0.1, stream=stream),
+     "decode_fp8": lambda: pkv.paged_attention_decode_fp8(q, q, cache, cache, tables, lens, 0.1, 1.0, 1.0, stream=stream),
+     "varlen": lambda: pkv.paged_attention_varlen(q, q, Tensor(5), cache, cache, tables, lens, 0.1, max_q_len=1,
+                                                  stream=stream),
+     "decode_kvwrite": lambda: pkv.paged_attention_decode_kvwrite(q, q, rows, rows, cache, cache, tables, lens, 0.1,
+                                                                  stream=stream)}[call]()
+    assert len(launched) == 1 and made == [(512, stream)]

@@ -48,3 +48,16 @@ def test_expanded():
     check_side_stream(lambda o, s: pkv.latent_attention_expanded(o, b.q, b.qsl, b.cache, b.tables, b.context_lens, *w,
                                                                  SCALE, 1000, stream=s),
                       out, pkv.latent_workspace_size(pkv.OP_LATENT_EXPANDED, 2, 600, 16, 512, ROPE, total_context=1000))
+
+
+def test_paged_decode():
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    S, blocks = 4, 60
+    kc, vc = (torch.randn(S * blocks, 16, 2, 128, device="cuda", generator=g).bfloat16() for _ in range(2))
+    q = torch.randn(S, 16, 128, device="cuda", generator=g).bfloat16()
+    tables = torch.randperm(S * blocks, device="cuda", generator=g).int().view(S, blocks)
+    lens = torch.tensor([900, 77, 960, 1], dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(q)
+    check_side_stream(lambda o, s: pkv.paged_attention_decode(o, q, kc, vc, tables, lens, 0.09, stream=s), out,
+                      pkv.workspace_size(pkv.OP_DECODE, S, S, 16, 2, 128))
