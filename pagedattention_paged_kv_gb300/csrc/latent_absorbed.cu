@@ -333,14 +333,18 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             }
             iw.advance(sb, units, g);
         }
-        if (!ok && lane == 0) {
-            flag_error(a.err, PKV_DEVERR_TIMEOUT);
-            *abort_flag = 1;
-            // copies in flight land before the shared memory is given back
+        if (lane == 0) {
+            if (!ok) {
+                flag_error(a.err, PKV_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+                // a stage of which only one half was asked for: its phase ends with that half
+                if (fill & 1) mbar_arrive(&ms.kv_full[fill / 2 % NST]);
+            }
+            // The copies land before this CTA ends, whoever else has given up waiting for them.
             const uint32_t issued = (fill + 1) / 2, pending = minu32(issued, NST);  // fill counts halves
             for (uint32_t k = issued - pending; k < issued; ++k)
-                mbar_wait(&ms.kv_full[k % NST], (k / NST) & 1, nullptr, kCopyLandsNs);
-            if (qloads > 0) mbar_wait(&ms.q_full, (qloads - 1) & 1, nullptr, kCopyLandsNs);
+                mbar_wait(&ms.kv_full[k % NST], (k / NST) & 1, nullptr);
+            if (qloads > 0) mbar_wait(&ms.q_full, (qloads - 1) & 1, nullptr);
         }
     } else if (warp == 1) {
         // ------------------------------ QK issuer ------------------------------

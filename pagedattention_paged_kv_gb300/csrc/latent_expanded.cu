@@ -369,15 +369,15 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             tw.advance(sb, units, g);
         }
         if (!waited) pdl_wait();
-        if (!ok && lane == 0) {
-            flag_error(a.err, PKV_DEVERR_TIMEOUT);
-            *abort_flag = 1;
-            // copies in flight land first
-            for (uint32_t i = np > 3 ? np - 3 : 0; i < np; ++i)
-                mbar_wait(&ms.full[i % 3], (i / 3) & 1, nullptr, kCopyLandsNs);
-            for (uint32_t i = nr > 2 ? nr - 2 : 0; i < nr; ++i)
-                mbar_wait(&ms.rope_full[i & 1], (i >> 1) & 1, nullptr, kCopyLandsNs);
-            if (segs > 0) mbar_wait(&ms.q_full, (segs - 1) & 1, nullptr, kCopyLandsNs);
+        if (lane == 0) {
+            if (!ok) {
+                flag_error(a.err, PKV_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // The copies land before this CTA ends, whoever else has given up waiting for them.
+            for (uint32_t i = np > 3 ? np - 3 : 0; i < np; ++i) mbar_wait(&ms.full[i % 3], (i / 3) & 1, nullptr);
+            for (uint32_t i = nr > 2 ? nr - 2 : 0; i < nr; ++i) mbar_wait(&ms.rope_full[i & 1], (i >> 1) & 1, nullptr);
+            if (segs > 0) mbar_wait(&ms.q_full, (segs - 1) & 1, nullptr);
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------

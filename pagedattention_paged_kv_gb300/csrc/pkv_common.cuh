@@ -22,7 +22,9 @@ constexpr int kBS = 16;
 // forever.  A wait for the CTA's own copies or MMAs already in flight -- they always
 // complete -- keeps the long limit, so a CTA never exits with them outstanding.
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;  // 2 s
-// A copy under way lands in microseconds: a CTA that gives up waits this long for its own.
+// Where the CTAs of a pair fill one barrier between them, its phase never ends if one of them has
+// given up before its share of the copies: there a CTA waits this long for its own, which land in
+// microseconds.
 constexpr uint64_t kCopyLandsNs = 5000000ull;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
