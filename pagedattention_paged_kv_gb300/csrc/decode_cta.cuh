@@ -351,10 +351,13 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap &k_map, const CUten
                 if (!ok) break;
             }
         }
-        if (!ok && lane == 0) {
-            flag_error(a.err, PKV_DEVERR_TIMEOUT);
-            *abort_flag = 1;
-            // Let the copies already issued land before the CTA's shared memory goes away.
+        if (lane == 0) {
+            if (!ok) {
+                flag_error(a.err, PKV_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // The copies land before the CTA's shared memory goes away, whoever else has given
+            // up waiting for them.
             const uint32_t pending = minu32(issued, (uint32_t)NST);
             uint32_t st = stage, ph = phase;
             for (uint32_t i = 0; i < pending; ++i) {

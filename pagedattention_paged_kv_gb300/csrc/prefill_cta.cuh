@@ -347,15 +347,16 @@ __device__ __forceinline__ void prefill_cta(const CUtensorMap &q_map, const CUte
         // ------------------------------ TMA producer ------------------------------
         const uint64_t policy = l2_policy_evict_normal();
         uint32_t fill = 0, pst = 0, pph = 0;  // copies issued; ring slot of the next one
-        int seg_i = 0;
+        uint32_t qloads = 0;
         bool ok = true;
         for (int64_t f = lo; f < hi && ok;) {
             Segment sg;
             segment_at<L::BPC>(a, pre, f, hi, sg);
             const UnitPos &u = sg.u;
             if (lane == 0) {
-                if (seg_i > 0) ok = mbar_wait(q_empty, (seg_i - 1) & 1, abort_flag, a.wait_ns);
+                if (qloads > 0) ok = mbar_wait(q_empty, (qloads - 1) & 1, abort_flag, a.wait_ns);
                 if (ok) {
+                    ++qloads;
                     mbar_arrive_expect_tx(q_full, 2 * DCH * half_rows * 128);
                     const int tok0 = (int)(u.t.q_row0 + u.qt * TPT);
                     for (int h = 0; h < 2; ++h)
@@ -419,17 +420,19 @@ __device__ __forceinline__ void prefill_cta(const CUtensorMap &q_map, const CUte
                 }
             }
             f = sg.end;
-            ++seg_i;
         }
-        if (!ok && lane == 0) {
-            flag_error(a.err, PKV_DEVERR_TIMEOUT);
-            *abort_flag = 1;
-            // let issued copies land before shared memory is released
+        if (lane == 0) {
+            if (!ok) {
+                flag_error(a.err, PKV_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // issued copies land before shared memory is released, whoever else has given up
+            // waiting for them
             const uint32_t nring = FP8 ? NST8 : NST;
             const uint32_t pending = minu32(fill, nring);
             for (uint32_t k = fill - pending; k < fill; ++k)
                 mbar_wait(FP8 ? &f8_full[k % nring] : &kv_full[k % nring], (k / nring) & 1, nullptr);
-            if (seg_i > 0) mbar_wait(q_full, (seg_i - 1) & 1, nullptr);
+            if (qloads > 0) mbar_wait(q_full, (qloads - 1) & 1, nullptr);
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
