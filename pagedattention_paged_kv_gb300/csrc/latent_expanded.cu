@@ -25,7 +25,9 @@
 //    of the result and the error was 1.6 times the result's own rounding.  The weights stay
 //    below 2^8 by the rescale rule; values past fp16's range are clamped and flagged where
 //    they are made (latent_expand.cu).  Keys stay bf16, the type of the queries they meet.
-//  * Waits are bounded in time; no CTA waits on another CTA.
+//  * The kernel starts under the expansion's tail.  Every role waits for the expansion's end before its
+//    first limited wait (the producer behind its first query load), so a limit counts this kernel's
+//    own steps.  Waits are bounded in time; no CTA of the kernel waits on another.
 //
 // Measured with the expansion and the join, R = 512, 64 heads: a chunk of 512 queries behind 16,384
 // tokens 450 us alone and 470 back to back (331 at the matrix products' peak rate), eight prompts of 500
@@ -233,8 +235,8 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         tma_prefetch_desc(&rope_map);
     }
     // The expansion's CTAs let this kernel start once everything before them is complete, so all
-    // inputs of the call may be read here; only what the expansion writes has to be waited for, and
-    // only by the producer (CTAs without work wait too, so that this grid ends behind the last).
+    // inputs of the call may be read here; only what the expansion writes has to be waited for (CTAs
+    // without work wait too, so that this grid ends behind the last).
     pdl_trigger();
     // A CTA of this kernel has the SM's shared memory, so no other holder of TMEM is there.
     if (warp == 1) tmem_alloc(&ms.tmem_slot, 512);
@@ -299,7 +301,10 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
 
     TileWalk tw(sb, units, ms.start[0], hi);
     SeqWalk<ExpandedUnits> &w = tw.w;
-    if (warp != 0) w.ahead(sb);  // the producer is on the critical path
+    if (warp != 0) {  // the producer is on the critical path
+        w.ahead(sb);
+        pdl_wait();
+    }
     auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.wait_ns));
     };

@@ -53,3 +53,31 @@ def test_expanded_shares_of_one_or_two_chunks(ctx, ql, heads, latent):
         return out
 
     run_out_then_healthy(lambda: go(outs[0]), lambda: go(outs[1]), expanded_reference(b, *w))
+
+
+def test_the_limit_does_not_count_the_expansion():
+    """A limit of 200 us: the longest wait inside either kernel takes microseconds, the expansion of
+    65,536 tokens for 64 heads (1.1 TFLOP of products, 2.1 GB written) far longer than the limit."""
+    ctx, heads = 65536, 64
+    b = Batch([ctx], [16], heads, 512, 128 + ROPE, seed=4, fill=0.0, block_size=64)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    w = [(torch.randn(heads, 128, 512, device="cuda", generator=g) * 512 ** -0.5).bfloat16() for _ in range(2)]
+    n = pkv.latent_workspace_size(pkv.OP_LATENT_EXPANDED, 1, 16, heads, 512, ROPE, total_context=ctx)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def go():
+        out = torch.full((16, heads, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+        pkv.latent_attention_expanded(out, b.q, b.qsl, b.cache, b.tables, b.context_lens, *w, SCALE, ctx, workspace=ws)
+        return out
+
+    want = go()
+    assert pkv.get_device_error() == 0
+    try:
+        pkv.set_wait_limit_ns(200_000)
+        for _ in range(5):
+            got = go()
+            assert pkv.get_device_error() == 0
+            assert torch.equal(got, want)
+    finally:
+        pkv.set_wait_limit_ns(0)
