@@ -607,7 +607,7 @@ latent_absorbed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             for (int k = 0; k < 2; ++k) {  // the four threads of a row hold its sum in parts
                 l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
                 l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
-                if ((lane & 3) == 0) ms.inv[ra + 8 * k] = l[k] > 0.f ? 1.f / l[k] : 0.f;
+                if ((lane & 3) == 0) ms.inv[ra + 8 * k] = 1.f / l[k];
             }
             if (!meet()) { ok = false; break; }
             const int slot = g.whole ? 0 : latent_slot(c, g.kb == 0);

@@ -27,7 +27,8 @@ struct LatentJob {
 __device__ __forceinline__ int latent_slot(int c, bool begins) { return 2 * c + begins; }
 
 // Parts lie as [2 * grid][SLOT_ROWS] (m, l) and [2 * grid][SLOT_ROWS][D] o.  BARE: a part that
-// saw nothing of a row (m = -inf) need not have left an output there.
+// saw nothing of a row (l = 0) need not have left an output there.  (m = -inf does not tell: it is
+// that of a part with scores of NaN alone too, whose l and o are NaN.)
 template <int D, int SLOT_ROWS, bool BARE>
 __global__ void __launch_bounds__(256, 5)
 latent_merge_kernel(const LatentJob *jobs, const float2 *ws_ml, const float *ws_o, __nv_bfloat16 *out,
@@ -53,7 +54,7 @@ latent_merge_kernel(const LatentJob *jobs, const float2 *ws_ml, const float *ws_
                 const int64_t at = (int64_t)latent_slot(j.c0 + p, p == 0) * SLOT_ROWS + row;
                 ml[u] = __ldcg(ws_ml + at);
                 o[u] = __ldcg(reinterpret_cast<const float4 *>(ws_o + at * D) + cg);
-                if (BARE && ml[u].x == -INFINITY) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (BARE && ml[u].y == 0.f) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
         float mc = M;
@@ -77,7 +78,7 @@ latent_merge_kernel(const LatentJob *jobs, const float2 *ws_ml, const float *ws_
             acc.w = fmaf(w, o[u].w, acc.w);
         }
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = 1.f / L;  // L = 0: every score is -inf, the row NaN by definition
     reinterpret_cast<uint2 *>(out + j.out_off + row * out_stride)[cg] =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
