@@ -22,9 +22,11 @@
 //    thread a row) computes its weights, as in the paged prefill.
 //  * Values and weights are fp16 (11 bits against bf16's 8; kind::f16 takes both operands of
 //    one type, so they go together): with bf16 the rounding of each weighed as much as that
-//    of the result and the error was 1.6 times the result's own rounding.  The weights stay
-//    below 2^8 by the rescale rule; values past fp16's range are clamped and flagged where
-//    they are made (latent_expand.cu).  Keys stay bf16, the type of the queries they meet.
+//    of the result and the error was 1.6 times the result's own rounding.  The weights are held
+//    2^kWeightShift times larger, up to 2^15 by the rescale rule: each is off by 2^-11 of itself or
+//    2^-32 of the largest, so that many small ones keep their part of the sum.  Values past fp16's
+//    range are clamped and flagged where they are made (latent_expand.cu).  Keys stay bf16, the type
+//    of the queries they meet.
 //  * The kernel starts under the expansion's tail.  Every role waits for the expansion's end before its
 //    first limited wait (the producer behind its first query load), so a limit counts this kernel's
 //    own steps.  Waits are bounded in time; no CTA of the kernel waits on another.
@@ -48,6 +50,11 @@ namespace pkv {
 namespace {
 
 constexpr int kSnap = 1;
+
+// exp2(s - m + kWeightShift) <= 2^(kRescaleSlack + kWeightShift) = 2^15, half of fp16's range.  Sums and
+// outputs of a row, and its parts', are all this much larger.
+constexpr float kWeightShift = 7.0f;
+static_assert(kRescaleSlack + kWeightShift <= 15.0f, "weights fit fp16");
 
 constexpr int kExpandedThreads = 384;  // loads, MMAs, two idle warps, two softmax warpgroups
 
@@ -563,7 +570,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                         }
                         if (up) m_ref = mx;
                     }
-                    const float base = m_ref == -INFINITY ? 0.f : m_ref;
+                    const float base = m_ref == -INFINITY ? 0.f : m_ref - kWeightShift;
                     const uint64_t nb2 = f2_pack(-base, -base);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
