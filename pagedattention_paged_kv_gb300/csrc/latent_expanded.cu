@@ -24,7 +24,7 @@
 //    one type, so they go together): with bf16 the rounding of each weighed as much as that
 //    of the result and the error was 1.6 times the result's own rounding.  The weights are held
 //    2^kWeightShift times larger, up to 2^15 by the rescale rule: each is off by 2^-11 of itself or
-//    2^-32 of the largest, so that many small ones keep their part of the sum.  Values past fp16's
+//    2^-32 of the largest, so that small ones count where the large one's value is near zero.  Values past fp16's
 //    range are clamped and flagged where they are made (latent_expand.cu).  Keys stay bf16, the type
 //    of the queries they meet.
 //  * The kernel starts under the expansion's tail.  Every role waits for the expansion's end before its
