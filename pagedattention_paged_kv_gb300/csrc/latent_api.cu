@@ -232,6 +232,7 @@ extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int
     pkv::ExpandedBuffers buf;
     buf.rope = reinterpret_cast<__nv_bfloat16 *>(ws + p.off_rope);
     buf.kv = reinterpret_cast<uint16_t *>(ws + p.off_kv);
+    buf.value_exp = reinterpret_cast<int8_t *>(ws + p.off_exp);
     buf.padded = p.padded;
 
     CUtensorMap latmap, wkmap, wvmap, qmap, kvmap, ropemap;

@@ -4,8 +4,11 @@
 // for every cached token j of the sequences with query rows: a matrix product of the gathered
 // latent rows [tokens, R] with the stacked weights [256 rows a head, R], written as rows of
 // 256 16-bit columns a (head, token), and the rotary parts copied beside them.  Keys are
-// rounded to bf16, values to fp16 (see latent_expanded.cu); a finite value past fp16's range
-// is clamped to it and flagged PKV_DEVERR_VALUE.
+// rounded to bf16, values to fp16 (see latent_expanded.cu).  fp16 reaches from 2^16 down to 2^-14 with
+// all its bits, and values may be of any size: those of 32 tokens of a head are stored 2^-x times as
+// large, their largest between 2^14 and 2^15, and x beside them (x >= -64, reached by a largest of
+// 2^-50).  A value is so off by 2^-11 of itself, by 2^-39 of that largest or by 2^-89.  x stays at 0
+// from 2^14 on; a finite value past fp16's range is clamped to it and flagged PKV_DEVERR_VALUE.
 //
 // Bound: tensor.  2 * 256 * R operations against 512 bytes written a (token, head): 512
 // operations a byte at R = 512.  What feeds the tensor pipe is the question: a CTA keeps 128
@@ -326,25 +329,46 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_co
             tc_fence_after();
             if (g < NT) {
                 uint16_t *dst = a.buf.kv + ((int64_t)(h * 4 + 2 * is_v) * a.buf.padded + row0) * 64 + part * 16;
-#pragma unroll 1
-                for (int i = 0; i < 4; ++i) {  // a 64-column piece, 16 of the warp's rows
-                    const int q = i >> 1, r0 = row + (i & 1) * 16;
-                    uint32_t r[32];
+                // a 64-column piece, 16 of the warp's rows; past the context the product saw whatever the
+                // slots held
+                auto load = [&](int i, uint32_t(&r)[32]) {
                     tmem_ld_16x64(tmem + ((uint32_t)(quarter * 32 + (i & 1) * 16) << 16) + (n & 1) * 256 + is_v * 128 +
-                                      q * 64, r);
+                                      (i >> 1) * 64, r);
                     tmem_wait_ld();
                     reg_order32(r);
-                    if (valid < kExpTile) {  // past the context the product saw whatever the slots held
+                    if (valid < kExpTile) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (r0 + (j & 2) * 4 >= valid) r[j] = 0u;
+                            if (row + (i & 1) * 16 + (j & 2) * 4 >= valid) r[j] = 0u;
                     }
-                    if (is_v) {
-                        float top = 0.f;
+                };
+                float grow = 1.f;   // 2^-x
+                bool past = false;  // a value is past fp16's range
+                if (is_v) {
+                    float top = 0.f;  // of the warp's 32 tokens (NaN does not take part)
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t r[32];
+                        load(i, r);
 #pragma unroll
                         for (int j = 0; j < 32; j += 2)
                             top = fmax3(top, fabsf(__uint_as_float(r[j])), fabsf(__uint_as_float(r[j + 1])));
-                        if (__any_sync(0xffffffffu, top > 65504.f)) {
+                    }
+                    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+                    const int x = max(kValueExpMin, min(0, (int)(bits >> 23) - 127 - 14));
+                    grow = __uint_as_float((uint32_t)(127 - x) << 23);
+                    past = __uint_as_float(bits) > 65504.f;
+                    if (lane == 0) a.buf.value_exp[(int64_t)h * (a.buf.padded / 32) + row0 / 32 + quarter] = (int8_t)x;
+                }
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    const int q = i >> 1, r0 = row + (i & 1) * 16;
+                    uint32_t r[32];
+                    load(i, r);
+                    if (is_v) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * grow);
+                        if (past) {
                             bool over = false;
 #pragma unroll
                             for (int j = 0; j < 32; ++j) over |= clamp_f16(r[j]);

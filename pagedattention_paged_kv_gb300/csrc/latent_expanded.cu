@@ -24,9 +24,13 @@
 //    one type, so they go together): with bf16 the rounding of each weighed as much as that
 //    of the result and the error was 1.6 times the result's own rounding.  The weights are held
 //    2^kWeightShift times larger, up to 2^15 by the rescale rule: each is off by 2^-11 of itself or
-//    2^-32 of the largest, so that small ones count where the large one's value is near zero.  Values past fp16's
-//    range are clamped and flagged where they are made (latent_expand.cu).  Keys stay bf16, the type
-//    of the queries they meet.
+//    2^-32 of the largest, so that small ones count where the large one's value is near zero.
+//  * The values of 32 keys are stored 2^-x times as large, so that small ones keep their bits
+//    (latent_expand.cu): with s' = s + x,
+//        out = sum_j 2^(s'_j - m) (2^-x v_j) / sum_j 2^-x 2^(s'_j - m)
+//    where m is the running maximum of the s', so weights stay below 2^15 whatever the x.  Values past
+//    fp16's range are clamped and flagged where they are made.  Keys stay bf16, the type of the
+//    queries they meet.
 //  * The kernel starts under the expansion's tail.  Every role waits for the expansion's end before its
 //    first limited wait (the producer behind its first query load), so a limit counts this kernel's
 //    own steps.  Waits are bounded in time; no CTA of the kernel waits on another.
@@ -147,13 +151,14 @@ __device__ __forceinline__ void snap_start(ExpandedStart *st, bool causal, int64
 struct TileWalk {
     SeqWalk<ExpandedUnits> w;
     ExpandedTiles t;
-    int64_t left;  // units of the share from here on
+    int64_t left;   // units of the share from here on
+    int64_t tiles;  // expansion tiles before the sequence
     int h, qt, kb;
     bool causal;
     int heads;
     __device__ __forceinline__ TileWalk(const SeqBatch &sb, const ExpandedUnits &u, const ExpandedStart &st, int64_t hi)
-        : t(st.seq.q, u.causal), left(hi - st.unit), h(st.h), qt(st.qt), kb(st.kb), causal(u.causal),
-          heads(u.num_heads) {
+        : t(st.seq.q, u.causal), left(hi - st.unit), tiles(st.tiles), h(st.h), qt(st.qt), kb(st.kb),
+          causal(u.causal), heads(u.num_heads) {
         w.start(st.seq);
         if (left > 0 && kb == t.chunks(qt)) next(sb, u);
     }
@@ -163,6 +168,7 @@ struct TileWalk {
         qt = 0;
         if (++h < heads) return;
         h = 0;
+        tiles += t.nk;
         w.seek(sb, u, w.pre + w.units);
         t = ExpandedTiles(w.q, causal);
     }
@@ -335,17 +341,10 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             ++np;
             return true;
         };
-        int64_t tiles = ms.start[0].tiles;
-        int seq = ms.start[0].seq.s, ctx = ms.start[0].seq.q.ctx;
         bool waited = false;
         while (tw.left > 0 && ok) {
             const ExpandedSegment g = tw.segment();
-            if (w.s != seq) {  // the next live sequence
-                tiles += (ctx + kExpTile - 1) / kExpTile;
-                seq = w.s;
-                ctx = w.q.ctx;
-            }
-            int key = __shfl_sync(0xffffffffu, (int)(tiles + g.kb) * kExpTile, 0);
+            int key = __shfl_sync(0xffffffffu, (int)(tw.tiles + g.kb) * kExpTile, 0);
             int row = __shfl_sync(0xffffffffu, (int)(4 * g.h * a.buf.padded) + key, 0);
             const int chunks = __shfl_sync(0xffffffffu, g.chunks, 0);
             if (segs > 0) ok = wait_all(&ms.q_empty, (segs - 1) & 1);
@@ -522,7 +521,13 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
             const int64_t pos = (int64_t)(ctx - w.q.q_len) + g.qt * kExpQTile + min(tok, g.tokens - 1);
             const int64_t lim = a.causal ? pos + 1 : ctx;
             float m_ref = -INFINITY, l = 0.f;
+            // the exponents of the values of a chunk's four times 32 keys, a byte each, a chunk ahead
+            const int32_t *exps = reinterpret_cast<const int32_t *>(a.buf.value_exp) +
+                                  (int64_t)g.h * (a.buf.padded / kExpTile) + tw.tiles + g.kb;
+            int32_t next_exps = __ldcg(exps);
             for (int ch = 0; ch < mine; ++ch, ++gh) {
+                const int32_t chunk_exps = next_exps;
+                if (ch + 1 < mine) next_exps = __ldcg(exps + ch + 1);
                 if (!wait_all(&ms.s_full[h], gh & 1)) { ok = false; break; }
                 tc_fence_after();
                 const int vis = (int)max64(0, min64(lim - (int64_t)(g.kb + ch) * kExpTile, kExpTile));
@@ -542,20 +547,24 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                     tmem_wait_ld();
                     reg_order32(reinterpret_cast<uint32_t(&)[32]>(v[0]));
                     reg_order32(reinterpret_cast<uint32_t(&)[32]>(v[32]));
-                    float rm = fmaxf(red0, red1);
                     if (!full) {
                         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int j = 0; j < 64; ++j)
                             if (r * 64 + j >= vis) v[j] = __float_as_uint(-INFINITY);
 #pragma unroll
-                        for (int j = 0; j < 64; j += 8)
+                        for (int j = 0; j < 64; j += 4)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                m4[k] = fmax3(m4[k], __uint_as_float(v[j + 2 * k]), __uint_as_float(v[j + 2 * k + 1]));
-                        rm = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                            for (int k = 0; k < 2; ++k) {
+                                float &m = m4[2 * (j / 32) + k];
+                                m = fmax3(m, __uint_as_float(v[j + 2 * k]), __uint_as_float(v[j + 2 * k + 1]));
+                            }
+                        red0 = fmaxf(m4[0], m4[1]);
+                        red1 = fmaxf(m4[2], m4[3]);
                     }
-                    const float mx = rm * sl2;
+                    const int xs[2] = {(int8_t)(chunk_exps >> (16 * r)), (int8_t)(chunk_exps >> (16 * r + 8))};
+                    const float x0 = (float)xs[0], x1 = (float)xs[1];
+                    const float mx = fmaxf(fmaf(red0, sl2, x0), fmaf(red1, sl2, x1));
                     const bool up = mx > m_ref + kRescaleSlack;
                     if (__any_sync(0xffffffffu, up)) {
                         const float alpha = up ? fast_exp2(m_ref - mx) : 1.f;
@@ -571,21 +580,25 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
                         if (up) m_ref = mx;
                     }
                     const float base = m_ref == -INFINITY ? 0.f : m_ref - kWeightShift;
-                    const uint64_t nb2 = f2_pack(-base, -base);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
+                        const float b = (q ? x1 : x0) - base, grow = __int_as_float((127 - xs[q]) << 23);  // 2^-x
+                        const uint64_t nb2 = f2_pack(b, b);
+                        uint64_t gs2[2] = {0, 0};  // the 32 keys' weights
                         uint32_t pk[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(v[q * 32 + 2 * j]),
+                            const uint64_t y2 = f2_fma(f2_pack(__uint_as_float(v[q * 32 + 2 * j]),
                                                                __uint_as_float(v[q * 32 + 2 * j + 1])),
                                                        sc2, nb2);
-                            float x0, x1;
-                            f2_unpack(x2, x0, x1);
-                            const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+                            float y0, y1;
+                            f2_unpack(y2, y0, y1);
+                            const float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
                             pk[j] = pack_f16x2(e0, e1);
-                            ps2[j & 1] = f2_add(ps2[j & 1], f2_pack(e0, e1));
+                            gs2[j & 1] = f2_add(gs2[j & 1], f2_pack(e0, e1));
                         }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) ps2[k] = f2_fma(gs2[k], f2_pack(grow, grow), ps2[k]);
                         tmem_st16(tS + (2 * r + q) * 16, pk);
                     }
                 }
@@ -697,7 +710,8 @@ void plan_expanded(int num_seqs, int64_t total_context, int num_heads, int sms, 
     p->padded = (total_context + (int64_t)num_seqs * (kExpTile - 1)) / kExpTile * kExpTile;
     p->off_rope = 0;
     p->off_kv = p->off_rope + up((size_t)p->padded * kExpRope * 2);
-    p->off_jobs = p->off_kv + up((size_t)num_heads * p->padded * 2 * kExpHeadDim * 2);
+    p->off_exp = p->off_kv + up((size_t)num_heads * p->padded * 2 * kExpHeadDim * 2);
+    p->off_jobs = p->off_exp + up((size_t)num_heads * p->padded / 32);
     p->off_ml = p->off_jobs + up(sizeof(LatentJob) * (size_t)p->grid);
     p->off_o = p->off_ml + up(2 * (size_t)p->grid * kExpQTile * sizeof(float2));
     p->ws_bytes = p->off_o + up(2 * (size_t)p->grid * kExpQTile * kExpHeadDim * sizeof(float));

@@ -17,12 +17,15 @@ constexpr int kExpQTile = 256;    // query tokens of an attention tile (two MMA 
 // rows starts on the next multiple of 128): piece p (64 key columns, the next 64, 64 value columns,
 // the next 64) is row (4 h + p) * padded + i of kv, so the 128 rows of a box are contiguous; rope
 // row i is the token's rotary key part.  Rows past a context are zero.  Value column 16 j + 2 i + e of
-// 64 (e < 2, i < 8) is stored as column 8 i + 2 j + e.
+// 64 (e < 2, i < 8) is stored as column 8 i + 2 j + e.  The values of each 32 padded tokens of a head
+// have an exponent x in common: what is stored is 2^-x v.
 struct ExpandedBuffers {
     __nv_bfloat16 *rope;  // [padded][64]
     uint16_t *kv;         // [num_heads][4][padded][64]: bf16 keys, fp16 values
+    int8_t *value_exp;    // [num_heads][padded / 32]
     int64_t padded;       // tokens, a multiple of 128
 };
+constexpr int kValueExpMin = -64;  // value_exp is between this and 0
 
 struct ExpandArgs {
     const int32_t *query_start_loc;
@@ -56,7 +59,7 @@ struct ExpandedArgs {
 struct ExpandedPlan {
     int grid;
     int64_t padded;
-    size_t off_rope, off_kv, off_jobs, off_ml, off_o, ws_bytes;
+    size_t off_rope, off_kv, off_exp, off_jobs, off_ml, off_o, ws_bytes;
 };
 
 void plan_expanded(int num_seqs, int64_t total_context, int num_heads, int sms, ExpandedPlan *p);
