@@ -370,11 +370,15 @@ int pkv_latent_cache_write(void *latent_cache, const void *latent, const void *r
  * query_start_loc NULL: one query row per sequence (total_q_tokens = num_seqs), context_lens
  * 0 gives a zero row.  Otherwise sequence s owns rows query_start_loc[s] ..
  * query_start_loc[s + 1] - 1, its last q_len positions (verification of drafted tokens, short
- * chunks), masked as in pkv_paged_attention_varlen; a sequence whose metadata is bad gets zero
- * rows, and rows behind query_start_loc[num_seqs] are left as they were.  What the cache holds
- * at or past a context has no effect; a row inside the context that is not finite makes every
- * row of that sequence not finite, also those the causal mask hides it from.  The softmax weights are rounded to bf16 for the product
- * with the latents; sums are fp32.
+ * chunks), masked as in pkv_paged_attention_varlen; a sequence whose context length is bad gets
+ * zero rows, one whose query_start_loc entries are bad has none, and rows behind
+ * query_start_loc[num_seqs] are left as they were.  A block id outside the pool is flagged and its
+ * tokens count as rows of zeros (score 0, value 0).  The softmax weights are rounded to bf16 for the
+ * product with the latents; sums are fp32.
+ * What the cache holds at or past a context has no effect.  Inside it, a latent part that is not
+ * finite makes every query row of its sequence not finite, also those the causal mask hides it from
+ * (their weight of zero is multiplied with it); a rotary part that is not finite enters the scores of
+ * the rows that see it alone, where a score of -infinity has no weight.
  * Supported: dtype PKV_DTYPE_BF16, latent_dim 256 or 512, rope_dim 64, block_size 8, 16, 32 or
  * 64, any num_heads with total_q_tokens * num_heads < 2^31 - 128, 0 < scale < infinity.
  * Workspace: pkv_latent_workspace_size(PKV_OP_LATENT_ABSORBED, ...), 256-byte aligned.
@@ -399,9 +403,14 @@ int pkv_latent_attention_absorbed(void *out, const void *q, const int32_t *query
  * the sum of context_lens over the sequences with query rows, as the caller knows it on the
  * host; a batch whose sum of contexts, each rounded up to 128, exceeds the room this gives
  * (total_context + 127 num_seqs, rounded down to 128) is refused on the device
- * (PKV_DEVERR_CONTEXT_LEN, all rows zero).  The softmax weights are rounded to fp16; a finite
- * value W_v[h] c_j beyond +-65504 is clamped there and flagged PKV_DEVERR_VALUE.
- * Cache rows that are not finite act as in the absorbed form.
+ * (PKV_DEVERR_CONTEXT_LEN, all rows zero).  The softmax weights are rounded to fp16 (each off by
+ * 2^-11 of itself or 2^-32 of the row's largest), the values to fp16 relative to the largest of 32
+ * tokens (positions 32 i .. 32 i + 31) of a head: each off by 2^-11 of itself, 2^-39 of that largest
+ * or 2^-89.  A finite value W_v[h] c_j beyond +-65504 is clamped there and flagged PKV_DEVERR_VALUE.
+ * Bad metadata and block ids act as in the absorbed form, and so do cache rows that are not finite,
+ * but that of the query rows which the mask hides such a latent part from only some are reached: rows
+ * are worked on in tiles of 256 from a sequence's first one on, and those of a tile that ends before
+ * the token's 128-token chunk (counted from position 0) stay finite.
  * Supported: latent_dim, rope_dim, block_size and dtype as for the absorbed form, nope_dim =
  * v_dim = 128, num_heads * (total_context + 127 num_seqs) < 2^29 - 128.
  * Workspace: pkv_latent_workspace_size(PKV_OP_LATENT_EXPANDED, ...): 512 bytes a (head, token)
