@@ -380,7 +380,8 @@ int pkv_latent_cache_write(void *latent_cache, const void *latent, const void *r
  * (their weight of zero is multiplied with it); a rotary part that is not finite enters the scores of
  * the rows that see it alone, where a score of -infinity has no weight.
  * Supported: dtype PKV_DTYPE_BF16, latent_dim 256 or 512, rope_dim 64, block_size 8, 16, 32 or
- * 64, any num_heads with total_q_tokens * num_heads < 2^31 - 128, 0 < scale < infinity.
+ * 64, any num_heads with total_q_tokens * num_heads < 2^31 - 128, scale > 0 with scale * log2(e)
+ * below infinity in fp32.
  * Workspace: pkv_latent_workspace_size(PKV_OP_LATENT_ABSORBED, ...), 256-byte aligned.
  */
 int pkv_latent_attention_absorbed(void *out, const void *q, const int32_t *query_start_loc,
@@ -411,7 +412,7 @@ int pkv_latent_attention_absorbed(void *out, const void *q, const int32_t *query
  * but that of the query rows which the mask hides such a latent part from only some are reached: rows
  * are worked on in tiles of 256 from a sequence's first one on, and those of a tile that ends before
  * the token's 128-token chunk (counted from position 0) stay finite.
- * Supported: latent_dim, rope_dim, block_size and dtype as for the absorbed form, nope_dim =
+ * Supported: latent_dim, rope_dim, block_size, scale and dtype as for the absorbed form, nope_dim =
  * v_dim = 128, num_heads * (total_context + 127 num_seqs) < 2^29 - 128.
  * Workspace: pkv_latent_workspace_size(PKV_OP_LATENT_EXPANDED, ...): 512 bytes a (head, token)
  * and about 40 MB.

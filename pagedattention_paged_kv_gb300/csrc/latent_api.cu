@@ -25,6 +25,12 @@ int block_shift(int block_size) {
     return block_size == 8 ? 3 : block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : -1;
 }
 
+// scale x log2(e), which the kernels take, or 0 for a scale that is not supported.
+float log2_scale(float scale) {
+    const float s = scale * 1.4426950408889634f;
+    return scale > 0.f && s < INFINITY ? s : 0.f;
+}
+
 int check_latent(int num_seqs, int total_q, int max_blocks_per_seq, int num_heads, int latent_dim, int rope_dim,
                  int block_size, int64_t num_blocks, int dtype) {
     if (num_seqs < 0 || total_q < 0 || max_blocks_per_seq < 0 || num_heads <= 0 || latent_dim <= 0 ||
@@ -151,7 +157,8 @@ extern "C" int pkv_latent_attention_absorbed(void *out, const void *q, const int
     int st = check_latent(num_seqs, total_q_tokens, max_blocks_per_seq, num_heads, latent_dim, rope_dim, block_size,
                           num_blocks, dtype);
     if (st != PKV_OK) return st;
-    if (!(scale > 0.f) || scale == INFINITY) return PKV_ERR_INVALID_ARG;
+    const float scale_log2 = log2_scale(scale);
+    if (scale_log2 == 0.f) return PKV_ERR_INVALID_ARG;
     if (!query_start_loc && total_q_tokens != num_seqs) return PKV_ERR_INVALID_ARG;
     if (num_seqs == 0 || total_q_tokens == 0) return PKV_OK;
     if (!out || !q || !latent_cache || !block_tables || !context_lens) return PKV_ERR_INVALID_ARG;
@@ -187,7 +194,7 @@ extern "C" int pkv_latent_attention_absorbed(void *out, const void *q, const int
     a.grid = p.grid;
     a.causal = causal != 0;
     a.num_blocks = num_blocks;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale_log2;
     a.ws_jobs = reinterpret_cast<pkv::LatentJob *>(ws + p.off_jobs);
     a.ws_ml = reinterpret_cast<float2 *>(ws + p.off_ml);
     a.ws_o = reinterpret_cast<float *>(ws + p.off_o);
@@ -209,8 +216,8 @@ extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int
     int st = check_latent(num_seqs, total_q_tokens, max_blocks_per_seq, num_heads, latent_dim, rope_dim, block_size,
                           num_blocks, dtype);
     if (st != PKV_OK) return st;
-    if (total_context < 0 || nope_dim <= 0 || v_dim <= 0 || !(scale > 0.f) || scale == INFINITY)
-        return PKV_ERR_INVALID_ARG;
+    const float scale_log2 = log2_scale(scale);
+    if (total_context < 0 || nope_dim <= 0 || v_dim <= 0 || scale_log2 == 0.f) return PKV_ERR_INVALID_ARG;
     if (nope_dim != pkv::kExpHeadDim || v_dim != pkv::kExpHeadDim ||
         !expanded_fits(num_seqs, total_context, num_heads))
         return PKV_ERR_UNSUPPORTED;
@@ -293,7 +300,7 @@ extern "C" int pkv_latent_attention_expanded(void *out, const void *q, const int
     a.grid = p.grid;
     a.max_context = (int64_t)max_blocks_per_seq * block_size;
     a.causal = causal != 0;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale_log2;
     a.buf = buf;
     a.ws_jobs = reinterpret_cast<pkv::LatentJob *>(ws + p.off_jobs);
     a.ws_ml = reinterpret_cast<float2 *>(ws + p.off_ml);
