@@ -4,6 +4,7 @@
 #pragma once
 
 #include <atomic>
+#include <mutex>
 
 #include <cuda_fp16.h>
 
@@ -35,6 +36,7 @@ __device__ __forceinline__ void pdl_trigger() {
 // kernel, kept by its launcher).
 struct SmemAllowance {
     std::atomic<int> bytes[64];
+    std::mutex raising;
 };
 
 // Raises `kernel`'s dynamic shared-memory limit to `smem` on the current device unless an
@@ -47,12 +49,12 @@ cudaError_t allow_dynamic_smem(void (*kernel)(Params...), size_t smem, SmemAllow
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (rec.bytes[dev].load(std::memory_order_acquire) >= (int)smem) return cudaSuccess;
+    // one thread at a time: the smaller of two sizes must not be set behind the larger
+    std::lock_guard<std::mutex> lock(rec.raising);
+    if (rec.bytes[dev].load(std::memory_order_relaxed) >= (int)smem) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    int cur = rec.bytes[dev].load(std::memory_order_relaxed);
-    while (cur < (int)smem && !rec.bytes[dev].compare_exchange_weak(cur, (int)smem)) {
-    }
-    return cudaSuccess;
+    if (e == cudaSuccess) rec.bytes[dev].store((int)smem, std::memory_order_release);
+    return e;
 }
 
 // launch_pdl (below) with the grid in clusters of `cluster` CTAs.
