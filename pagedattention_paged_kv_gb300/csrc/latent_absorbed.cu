@@ -10,7 +10,10 @@
 // Bound.  A cached token costs 2 (R + 64) bytes once per 64 query rows, and 2 * 64 * (2R + 64)
 // multiply-adds: at R = 512, 1152 bytes against 69,632 MACs, i.e. 49 cycles of one SM's
 // share of the HBM bandwidth against 17 cycles of its tensor pipe at the full rate.  Up to
-// 64 rows a token is HBM-bound if the MMAs stay near half rate and loads never pause.
+// 64 rows a token is HBM-bound if the MMAs stay near half rate and loads never pause.  (That counts
+// operations.  Both operands come from shared memory: a 16-deep step of QK, M = N = 64, has 4 KB of them
+// for 16 cycles of products, one of PV, M = 128, N = 64, 6 KB for 32.  Were they read at 128 bytes a
+// cycle, which is not measured here, a tile's 36 and 16 steps would take 1,900 cycles, not 1,100.)
 //
 // Layout
 //  * A work item is 64 query rows (row = token * heads + head) of one sequence; its units
@@ -102,8 +105,12 @@ static_assert(sizeof(AbsorbedMisc) <= 2048, "fits its place");
 // What an item costs besides its tiles, in tiles: its units are kItemCost ones without work, then
 // one a tile, so that a share of many short items has fewer tiles.  (Its output takes 4,000 to 6,000
 // cycles, a tile 3,300 to 4,200.  With shares of equally many tiles the slowest CTA took 1.4 times
-// another's time: 174 us for the rows of 1 to 4 tokens of 32 sequences at 128 heads, 132 with a cost
-// of 4, 135 with 6; one token of 128 sequences 65.9, 62.9, 64.5.)
+// another's time.)  Measured, us:
+//                                                        R = 512              R = 256
+//   cost                                             0    2    4    6     0    2    4    6
+//   1 to 4 tokens of 32 sequences, 128 heads       172  143  130  134    98   80   74   68
+//   one token of 128 sequences, 64 heads          65.3 61.3 62.1 63.6  38.1 35.6 35.2 35.4
+//   one of 64, four of them long, 16 heads        56.9 51.1 50.9 52.4  36.4 31.3 30.4 30.9
 constexpr int kItemCost = 4;
 
 // Units of a sequence: 64-row groups x (64-token tiles and the item's cost).

@@ -22,9 +22,11 @@
 // shares, so a pair reloads its tokens only when its share crosses tiles.
 // Measured at 16,896 tokens x 64 heads, R = 512 (283 GFLOP, 554 MB written): 292 us for single
 // CTAs, 228 with every chunk's halves multicast to both CTAs of a cluster, 212 as pairs, some 175 with
-// the epilogue on eight warps that store whole lines.  What is left is the writes: a plain fill of the
-// 554 MB takes 140 us (3.9 TB/s; the products alone are 148 us at the peak rate), and without its
-// stores the call is 45 us shorter.
+// the epilogue on eight warps that store whole lines.  The value warps' first pass over a unit, for its
+// largest values, is not in these: with it eight prompts' 311 MB take 138 us, without it 130, both under
+// the counters.  What is left is the writes: a plain fill of the 554 MB takes
+// 140 us (3.9 TB/s; the products alone are 148 us at the peak rate), and without its stores the call is
+// 45 us shorter.
 // Waits are bounded in time.  The CTAs of a pair (always resident together) wait for each other;
 // no pair waits for another.
 #include "attn_block.cuh"

@@ -35,9 +35,10 @@
 //    first limited wait (the producer behind its first query load), so a limit counts this kernel's
 //    own steps.  Waits are bounded in time; no CTA of the kernel waits on another.
 //
-// Measured with the expansion and the join, R = 512, 64 heads: a chunk of 512 queries behind 16,384
-// tokens 450 us alone and 470 back to back (331 at the matrix products' peak rate), eight prompts of 500
-// to 2500 tokens 480 to 495 (270).  Back to back the chunk runs at the board's power limit (1370 W, SM
+// Measured with the expansion and the join, R = 512, 64 heads, in a graph of calls: a chunk of 512 queries
+// behind 16,384 tokens 447 to 485 us (331 at the matrix products' peak rate), eight prompts of 500 to 2500
+// tokens 475 to 499 (270).  With plain fp16 values, whose small ones were lost, these were 443 to 478 and
+// 466 to 488.  Back to back the chunk runs at the board's power limit (1370 W, SM
 // clock 1.65 GHz of 2.07): chunks of 96 keys in two whole stages with an issuer a half took 2,770 cycles
 // for 96 keys against 4,500 for 128, and no less time.  At full clocks a chunk's 4,500 cycles are
 // 2,550 of products, the issuer's steps between them, and waits for keys, which are asked for
@@ -53,6 +54,8 @@ namespace pkv {
 
 namespace {
 
+// A share that would begin this close to a tile's begin or end, in chunks, begins there instead
+// (snap_start): a cut one chunk from an end would cost a part and its join for next to no balance.
 constexpr int kSnap = 1;
 
 // exp2(s - m + kWeightShift) <= 2^(kRescaleSlack + kWeightShift) = 2^15, half of fp16's range.  Sums and
