@@ -264,12 +264,13 @@ __global__ void __launch_bounds__(1024, 1) free_pages_kernel(const FreeArgs a, c
 
     const int id0 = blockIdx.x * words_per_cta * 32;  // below 2^23
     const int wl = tid & 31, nw = nt >> 5;
+    const int64_t gathered = refused ? 0 : a.num_blocks;  // refused: no page was freed, whatever the counts are
     for (int w0 = tid >> 5; w0 < words_per_cta; w0 += nw * kInFlight) {
         int32_t held[kInFlight];
 #pragma unroll
         for (int k = 0; k < kInFlight; ++k) {
             const int id = id0 + 32 * (w0 + nw * k) + wl;
-            held[k] = w0 + nw * k < words_per_cta && id < a.num_blocks ? __ldcg(a.new_ref_counts + id) : 0;
+            held[k] = w0 + nw * k < words_per_cta && id < gathered ? __ldcg(a.new_ref_counts + id) : 0;
         }
 #pragma unroll
         for (int k = 0; k < kInFlight; ++k) {
