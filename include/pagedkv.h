@@ -424,9 +424,10 @@ int pkv_step_metadata(int32_t *block_tables, int32_t *context_lens, int32_t *que
  * and the pages left without a holder go in front of the free list: in ascending order, the last of
  * them at index free_begin[0] - 1, and free_end[0] is the index of the first.  A row outside the
  * tables is flagged PKV_DEVERR_SEQ.  An entry outside the pool, or of a page without holders, is
- * flagged PKV_DEVERR_BLOCK_ID and changes nothing.  More freed pages than free_begin[0], or
- * free_begin[0] outside the list, are flagged PKV_DEVERR_FREE_BLOCKS: then the lowest ids find no
- * place, or (outside) nothing is freed.
+ * flagged PKV_DEVERR_BLOCK_ID and changes nothing.  A negative count is flagged PKV_DEVERR_BLOCK_ID and
+ * becomes 0.  More freed pages than free_begin[0], or free_begin[0] outside the list, are flagged
+ * PKV_DEVERR_FREE_BLOCKS: then the lowest ids find no place, or (outside) nothing is freed and the
+ * counts stay as they are.
  *
  * pkv_compact_pages: moves the live pages (ref_counts > 0) of a pool towards its lowest ids.  Move k
  * takes the k-th highest live id into the k-th lowest free one, for as long as that is a lower id

@@ -226,8 +226,19 @@ __global__ void __launch_bounds__(1024, 1) free_pages_kernel(const FreeArgs a, c
         else if (report) flag_error(a.err, PKV_DEVERR_SEQ);
     }
     const int64_t g = (int64_t)blockIdx.x * nt + tid, gn = (int64_t)gridDim.x * nt;
-    if (a.new_ref_counts != a.ref_counts)
-        for (int64_t b = g; b < a.num_blocks; b += gn) a.new_ref_counts[b] = a.ref_counts[b];
+    // A negative count is a damaged one: 0 from here on, so that only freed pages have one below.
+    for (int64_t b0 = g; b0 < a.num_blocks; b0 += gn * kInFlight) {
+        int32_t held[kInFlight];
+#pragma unroll
+        for (int k = 0; k < kInFlight; ++k) held[k] = b0 + gn * k < a.num_blocks ? a.ref_counts[b0 + gn * k] : 0;
+#pragma unroll
+        for (int k = 0; k < kInFlight; ++k) {
+            if (b0 + gn * k >= a.num_blocks) break;
+            const bool bad = held[k] < 0 && !refused;
+            if (bad) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+            if (bad || a.new_ref_counts != a.ref_counts) a.new_ref_counts[b0 + gn * k] = bad ? 0 : held[k];
+        }
+    }
     sync_all();  // the counts are in place, the rows known, free_begin read
 
     // A page that loses its last holder is marked by a count far below zero; nothing but a damaged table
@@ -274,7 +285,7 @@ __global__ void __launch_bounds__(1024, 1) free_pages_kernel(const FreeArgs a, c
         }
 #pragma unroll
         for (int k = 0; k < kInFlight; ++k) {
-            const bool freed = held[k] < kFreed / 2;
+            const bool freed = held[k] < 0;
             const uint32_t word = __ballot_sync(0xffffffffu, freed);
             if (w0 + nw * k >= words_per_cta) continue;
             if (freed) a.new_ref_counts[id0 + 32 * (w0 + nw * k) + wl] = 0;
