@@ -20,6 +20,7 @@
 #include "decode_cta.cuh"
 #include "paged_shared.cuh"
 #include "prefix_cta.cuh"
+#include "tcgen05.cuh"
 
 namespace pkv {
 
@@ -200,7 +201,7 @@ paged_shared_kernel(const __grid_constant__ CUtensorMap dk_map, const __grid_con
         }
         as.prefix_parts[i] = parts;
     }
-    __syncthreads();  // the scratch is free for the roles
+    hand_over_smem();  // the scratch is free for the roles
     if ((int)blockIdx.x < k) decode_cta<D, FP8, NTH, true>(dk_map, dv_map, ad, (int)blockIdx.x, k, false, skip);
     else prefix_cta<D, FP8>(pq_map, pk_map, pv_map, ap, pre, skip, (int)blockIdx.x - k, grid - k);
 }

@@ -156,6 +156,13 @@ __device__ __forceinline__ void fence_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Barrier of the CTA behind which asynchronous copies may write shared memory that its threads have read and
+// written: a barrier alone orders accesses of one proxy, not these with TMA's.
+__device__ __forceinline__ void hand_over_smem() {
+    fence_async_smem();
+    __syncthreads();
+}
+
 // 32 consecutive fp32 columns of the warp's 32 TMEM lanes (one row per thread).
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
