@@ -24,6 +24,7 @@
 #include "decode_cta.cuh"
 #include "prefill_cta.cuh"
 #include "paged_varlen.cuh"
+#include "tcgen05.cuh"
 
 namespace pkv {
 
@@ -55,7 +56,7 @@ __device__ __forceinline__ int64_t cta_sum(int64_t x, int64_t *red) {
     __syncthreads();
     int64_t t = 0;
     for (int w = 0; w < (int)(blockDim.x >> 5); ++w) t += red[w];
-    __syncthreads();
+    hand_over_smem();
     return t;
 }
 
@@ -76,7 +77,7 @@ paged_varlen_kernel(const __grid_constant__ CUtensorMap dk_map, const __grid_con
     for (int v = threadIdx.x; v < V; v += blockDim.x) td += item_blocks(ad, v, false);
     for (int s = threadIdx.x; s < ap.num_seqs; s += blockDim.x) tp += seq_units(ap, s, false);
     td = cta_sum(td, red);
-    tp = cta_sum(tp, red);  // ends with __syncthreads: the bodies may now reuse the memory
+    tp = cta_sum(tp, red);  // ends with hand_over_smem: the bodies' copies may now reuse the memory
     const int G = (int)gridDim.x;
     const int k = decode_ctas(td, tp, G, sp);
     if ((int)blockIdx.x < k) decode_cta<D, FP8, 1>(dk_map, dv_map, ad, (int)blockIdx.x, k, false);

@@ -19,10 +19,10 @@ def test_the_barrier_has_the_fence():
     assert re.sub(r"\s", "", body) == "fence_async_smem();__syncthreads();"
 
 
-@pytest.mark.parametrize("name,kernel", [("paged_shared.cu", "paged_shared_kernel")])
+@pytest.mark.parametrize("name,kernel", [("paged_shared.cu", "paged_shared_kernel"), ("paged_varlen.cu", "cta_sum")])
 def test_scratch_goes_over_to_the_copies(name, kernel):
     src = text(name)
     plan = src[src.index(kernel + "("):]
-    plan = plan[:re.search(r"\bdecode_cta<", plan).start()]
+    plan = plan[:re.search(r"\bdecode_cta<|\n\}", plan).start()]
     barriers = re.findall(r"__syncthreads\w*|hand_over_smem", plan)
     assert barriers[-1] == "hand_over_smem"
