@@ -265,7 +265,7 @@ struct JoinArgs {
 template <int D>
 __global__ void __launch_bounds__(256, 3) join_kernel(const JoinArgs a) {
     constexpr int CG = D / 8;
-    const int cg = threadIdx.x % CG, s = blockIdx.x, h = blockIdx.y * (256 / CG) + threadIdx.x / CG;
+    const int cg = threadIdx.x % CG, s = blockIdx.y, h = blockIdx.x * (256 / CG) + threadIdx.x / CG;
     // Exact: kvh * group <= 2^20 (8192 items of up to 8 heads, 128 rows), so a quotient is off by at most
     // 2^-23 * 2^20 / group = 1 / (8 group), and the half added leaves 1 / (2 group)
     const int kvh = (int)(((float)h + 0.5f) * a.inv_group), hg = h - kvh * a.group;
@@ -426,7 +426,8 @@ static cudaError_t launch_shared_d(const CUtensorMap &dk, const CUtensorMap &dv,
     j.head_tiles = ad.head_tiles;
     j.room = (int64_t)ad.max_blocks_per_seq * ad.block_size;
     constexpr int per = 256 / (D / 8);  // rows of a CTA
-    return launch_pdl(join_kernel<D>, dim3(ad.num_seqs, (ad.num_heads + per - 1) / per), dim3(256), 0, stream, j);
+    // y has 16 bits: the sequences (8192 at most), not the heads (2^20)
+    return launch_pdl(join_kernel<D>, dim3((ad.num_heads + per - 1) / per, ad.num_seqs), dim3(256), 0, stream, j);
 }
 
 cudaError_t launch_paged_shared(int head_dim, bool fp8, const CUtensorMap &dk, const CUtensorMap &dv,
