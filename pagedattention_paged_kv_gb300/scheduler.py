@@ -114,10 +114,41 @@ class IterationBatch:
         return max((it.q_len for it in self.items), default=0)
 
 
+def _runs_of(common: np.ndarray):
+    """A run of n rows as neighbouring groups that save the most reads of blocks, (members - 1) * prefix in
+    all, fewest groups where that is equal.  common [n - 1]: leading blocks of neighbours in common; a
+    group's prefix is the least inside it.  Returns [(begin, end, prefix)]."""
+    n = len(common) + 1
+    edge = np.concatenate([[-1], common, [-1]])
+    # A cut pays only where the rows beside it have less in common than one of them has with its other
+    # neighbour: anywhere else a row goes over to the other side, or the two sides join, without loss.
+    at = [0, *(1 + np.flatnonzero((common < edge[:-2]) | (common < edge[2:]))).tolist(), n]
+    at = np.array(at)
+    m = len(at) - 1
+    least = np.full(2 * m - 1, 1 << 40)   # of what neighbours have in common: inside the parts, at the cuts between
+    least[1::2] = common[at[1:-1] - 1]
+    for i, (a, b) in enumerate(zip(at[:-1], at[1:])):
+        if b - a > 1:
+            least[2 * i] = common[a:b - 1].min()
+    best, begin, prefix = (np.zeros(m + 1, np.int64) for _ in range(3))   # for the rows before at[j]: saved, last group
+    for j in range(1, m + 1):
+        shared = np.minimum.accumulate(least[2 * j - 2::-1])[::-2]   # of rows at[i] .. at[j] - 1
+        saved = best[:j] + (at[j] - at[:j] - 1) * shared
+        begin[j] = i = int(saved.argmax())
+        best[j], prefix[j] = saved[i], shared[i] if at[j] - at[i] > 1 else 0
+    groups, j = [], m
+    while j > 0:
+        groups.append((int(at[begin[j]]), int(at[j]), int(prefix[j])))
+        j = begin[j]
+    return groups[::-1]
+
+
 def shared_prefixes(block_tables: np.ndarray, context_lens: np.ndarray, block_size: int = BLOCK_SIZE):
     """Which neighbouring rows of a batch share a prefix, as paged_attention_decode_shared takes it:
-    (group_start [G + 1], prefix_lens [G]) int32.  A group is a run of rows with the same first block; its
-    prefix is the leading blocks that all its rows have in common, within every row's context."""
+    (group_start [G + 1], prefix_lens [G]) int32.  A group's prefix is the leading blocks that all its rows
+    have in common, within every row's context.  Rows with the same first block are one group unless
+    splitting them saves more reads: families on documents behind one system prompt, or a short request
+    beside long ones."""
     tables, ctx = np.asarray(block_tables), np.asarray(context_lens)
     S = tables.shape[0]
     if S == 0 or tables.shape[1] == 0:
@@ -125,14 +156,22 @@ def shared_prefixes(block_tables: np.ndarray, context_lens: np.ndarray, block_si
     first = np.where(ctx > 0, tables[:, 0], -1)
     new = np.ones(S, bool)
     new[1:] = (first[1:] != first[:-1]) | (first[1:] < 0)
-    start = np.flatnonzero(np.append(new, True)).astype(np.int32)
-    lens = np.zeros(len(start) - 1, np.int32)
-    for g, (a, b) in enumerate(zip(start[:-1], start[1:])):
-        if b - a > 1:
-            n = int(ctx[a:b].min()) // block_size
-            same = (tables[a:b, :n] == tables[a, :n]).all(axis=0)
-            lens[g] = (n if same.all() else int(np.argmin(same))) * block_size
-    return start, lens
+    runs = np.flatnonzero(np.append(new, True))
+    start, lens = [0], []
+    for a, b in zip(runs[:-1].tolist(), runs[1:].tolist()):
+        if b - a == 1:
+            groups = [(0, 1, 0)]
+        else:
+            full = ctx[a:b].astype(np.int64) // block_size
+            limit = np.minimum(np.minimum(full[1:], full[:-1]), tables.shape[1])
+            n = int(limit.max())
+            differs = np.ones((b - a - 1, n + 1), bool)   # column n: the end of every row
+            differs[:, :n] = tables[a + 1:b, :n] != tables[a:b - 1, :n]
+            groups = _runs_of(np.minimum(differs.argmax(axis=1), limit))
+        for _, end, prefix in groups:
+            start.append(a + end)
+            lens.append(prefix * block_size)
+    return np.array(start, np.int32), np.array(lens, np.int32)
 
 
 class PrefixCache:
@@ -222,7 +261,7 @@ class Scheduler:
                              "gets its token before any prefill chunk)")
         self.bm = block_manager
         self.cache = PrefixCache(block_manager, block_size) if prefix_cache else None
-        # iterations of decodes alone: sequences with the same first block next to each other in the batch
+        # iterations of decodes alone: sequences next to each other in the batch that have leading blocks in common
         self.group_shared = bool(group_shared)
         self._copies: list = []
         self.max_num_seqs = int(max_num_seqs)
@@ -369,7 +408,7 @@ class Scheduler:
                 take[id(s)] = 1
         items = [ScheduledItem(s, s.computed, take[id(s)]) for s in self.running if id(s) in take]
         if self.group_shared and all(it.q_len == 1 for it in items):
-            items.sort(key=lambda it: it.seq.block_table[:1])
+            items.sort(key=lambda it: it.seq.block_table)
         self.iteration += 1
         batch = self._pack(items, admitted, finished, preempted)
         if self._copies:
