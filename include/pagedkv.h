@@ -276,6 +276,10 @@ int pkv_paged_attention_varlen_fp8(void *out, const void *q, const int32_t *quer
  * group_start that is not ascending within the batch is flagged PKV_DEVERR_SEQ and prefix_lens outside
  * [0, max_blocks_per_seq * block_size] PKV_DEVERR_CONTEXT_LEN; the sequences concerned attend alone.
  * Of a row whose scores are all -infinity, or include NaN or +infinity, the output is NaN.
+ * Over the shared rows of an FP8 cache a query row is held in two e4m3 numbers an element: exactly where
+ * the element is at least 2^-9 of its row's largest, else to within 2^-16 of that largest (one element
+ * moves a score by at most that much times |k| * scale).  Over own rows it is held as in
+ * pkv_paged_attention_decode_fp8, in fp16: exactly for magnitudes in [2^-14, 65504].
  * pkv_set_decode_split has no effect here.
  * Supported: the head counts, head_dim and block sizes of pkv_paged_attention_decode (of
  * pkv_paged_attention_decode_fp8: head_dim 128), num_groups <= num_seqs, scale > 0 with scale *
@@ -284,7 +288,8 @@ int pkv_paged_attention_varlen_fp8(void *out, const void *q, const int32_t *quer
  * kernel's stages do not fit in shared memory together: with an FP8 cache above num_seqs + num_groups
  * of about 8,300.
  * Workspace: pkv_workspace_size(PKV_OP_DECODE_SHARED, num_seqs, num_seqs, ...), 256-byte aligned: about
- * 8 bytes a query element and, on 152 SMs, 50 MB.
+ * 10.2 bytes a query element (the parts of both sides in fp32, an FP8 cache's queries) and, on 152 SMs and
+ * for head_dim 128, 50 MB.
  */
 int pkv_paged_attention_decode_shared(void *out, const void *q, const void *k_cache, const void *v_cache,
                                       const int32_t *block_tables, const int32_t *context_lens,
@@ -584,9 +589,11 @@ void pkv_set_decode_split(int enabled);
 
 /*
  * Which groups of pkv_paged_attention_decode_shared share their prefix, for launches from now on
- * (process-wide): 1 (the default) those for which it is expected to be faster, by the number of their
- * sequences, the prefix and the head counts; 2 all with two sequences or more; 0 none (the sharing's
- * ablation).  Results agree within rounding.  Not from the pages.
+ * (process-wide): 1 (the default) those whose shared rows take less SM time together than in each
+ * sequence alone, by the number of their sequences, the prefix and the head counts; 2 all with two
+ * sequences or more; 0 none (the sharing's ablation).  HBM is not weighed: with 64 query heads over 8 and a
+ * bf16 cache, pairs attend alone behind any prefix by default (32 of them behind 8192 tokens: 315 us,
+ * with 2 190 us).  Results agree within rounding, of an FP8 cache's queries too.  Not from the pages.
  */
 void pkv_set_shared_prefix(int mode);
 

@@ -766,7 +766,8 @@ def set_decode_split(enabled: bool) -> None:
 
 def set_shared_prefix(mode: int) -> None:
     """Which groups of paged_attention_decode_shared share their prefix, for launches from now on: 1 (the
-    default) those for which it is expected to be faster, 2 all, 0 none: the sharing's ablation."""
+    default) those whose shared rows take less SM time together than in each sequence alone (HBM is not
+    weighed: pairs over a bf16 cache of 8 KV heads attend alone), 2 all, 0 none: the sharing's ablation."""
     lib().pkv_set_shared_prefix(int(mode))
 
 

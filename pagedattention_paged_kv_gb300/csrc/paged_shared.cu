@@ -12,11 +12,10 @@
 // two amounts of work, and takes a role as in paged_varlen.cu.
 //
 // Measured (64 query heads over 8, d 128; the kernels of a call, L2 as they leave it): 128 sequences with
-// up to 512 own tokens behind 8192 shared ones 57 us (193 MB of DRAM, which a copy would move in 28; 3.5 us
+// up to 512 own tokens behind 8192 shared ones 56 us (193 MB of DRAM, which a copy would move in 28; 3.5 us
 // until the roles begin, 4.5 until the first scores, the sides done at 47 to 50, the join 8), 64 sequences
-// on two prefixes of 32,768 100 us (578 MB, 5.8 TB/s), 96 sequences on 12 documents over an FP8 cache 70 us
-// (263 MB).  Each sequence alone (pkv_paged_attention_decode) the same batches take
-// 277, 773 and 183 us.
+// on two prefixes of 32,768 102 us (578 MB, 5.7 TB/s), 96 sequences on 12 documents over an FP8 cache 72 us
+// (263 MB).  Each sequence alone (pkv_paged_attention_decode) the same batches take 277, 790 and 182 us.
 #include "decode_cta.cuh"
 #include "paged_shared.cuh"
 #include "prefix_cta.cuh"
@@ -61,6 +60,8 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
 // another sequence of the group does too, and the group is worth a tile; the others attend to all their
 // tokens alone, as all do when group_start is not ascending within the batch.  So the result does not depend on
 // the grouping, as long as the tables of a group agree.
+// 384 threads leave 168 registers.  <128, FP8, two n-tiles> spills 44 bytes and loads 60 (the decode kernel of
+// that form 72 and 104); the others spill nothing.
 template <int D, bool FP8, int NTH>
 __global__ void __launch_bounds__(kSharedThreads, 1)
 paged_shared_kernel(const __grid_constant__ CUtensorMap dk_map, const __grid_constant__ CUtensorMap dv_map,
@@ -118,6 +119,8 @@ paged_shared_kernel(const __grid_constant__ CUtensorMap dk_map, const __grid_con
     }
     __syncthreads();
     // A group whose sequences would read the prefix in less SM time than its tiles take does not share it.
+    // HBM is left out, so groups of two that it bounds do not share (32 behind 8192 tokens, 64 heads over 8: 315
+    // us alone, 190 shared; groups of three share: 191, alone 462).
     for (int g = tid; g < G; g += nt) {
         if (count[g] < 2 || costs.mode == 2) continue;
         const int seqs = gs[g + 1] - gs[g], tiles = prefix_tiles(seqs, ap.group);

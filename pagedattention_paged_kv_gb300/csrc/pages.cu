@@ -11,10 +11,10 @@
 //            down; tables, counts and free list follow
 //
 // Bound: latency.  The arrays are a few MB at most, and each call is a chain of dependent steps
-// (lengths, table entries, counts, sums over the whole pool): two branches of two requests take 3.9 us, 1024
-// branches of 128 requests 9.8, one request freed 3.8, 900 of 1024 freed 20, 64 pages moved 7.3, a pool of
-// 105,000 pages for 1024 requests squeezed 17.7.  One cluster of CTAs runs the chain
-// in one launch: the hardware's cluster barrier stands between the steps, so no step costs a launch
+// (lengths, table entries, counts, sums over the whole pool): four branches of two requests take 3.9 us (in
+// place as well), 1024 branches of 128 requests 9.8, one request of four freed 3.7 (in place 4.2), 900 of 1024
+// freed 19.5 (19.8), 64 pages moved 7.4, a pool of 105,000 pages for 1024 requests squeezed 17.7.  One cluster of
+// CTAs runs the chain in one launch: the hardware's cluster barrier stands between the steps, so no step costs a launch
 // and no workspace is needed, and what the CTAs tell each other goes through their shared memory.
 // The set of pages a call frees, or finds live, is a bitmap there: CTA c holds the bits of the c-th
 // part of the pool, and ranks in ascending order come from counting bits.  Everything waits for
@@ -459,9 +459,16 @@ namespace {
 
 // CTAs for a pool of `blocks` pages and `rows` rows to walk through: one for what 1024 threads take in one
 // or two rounds (a barrier of a cluster costs as much as a round), else a cluster of 4 or of 16, the most
-// there may be (more than 8 have to be allowed).  Moving 64 of 2,000 pages: 7.3 us with one CTA, 10.4 with
-// 16; freeing 900 rows of 140 pages each: 28 us with 16 CTAs of 1024, 42 with 8 of 512 (before the freed
-// pages were gathered by whole warps: 20 now).
+// there may be (more than 8 have to be allowed).  us with 1 / 4 / 8 / 16 CTAs, the rows' pages of their own:
+//     rows x pages   free                      compact, a quarter free   fork into `rows`, in place
+//     16 x 16        4.7 / 6.8 / 6.7 / 7.5     4.8 / 7.4 / 7.3 / 8.6     4.0 / 5.0 / 5.0 / 4.8
+//     64 x 64        9.7 / 11.1 / 11.1 / 12.1  10.0 / 11.2 / 10.8 / 12.4 6.4 / 7.0 / 7.1 / 6.9
+//     64 x 120       14.9 / 15.2 / 15.1 / 16.0 15.2 / 13.6 / 13.4 / 14.8 8.1 / 8.5 / 8.6 / 9.1
+//     128 x 120      26.2 / 15.9 / 15.8 / 16.5 27.0 / 14.7 / 14.2 / 15.8 12.6 / 8.9 / 9.1 / 9.1
+//     512 x 60       48.1 / 18.0 / 12.5 / 13.3 50.3 / 19.4 / 12.8 / 14.1 22.5 / 13.0 / 9.0 / 8.9
+//     1024 x 100     148 / 44.7 / 25.8 / 18.0  160 / 47.3 / 27.1 / 19.5  64.7 / 22.0 / 13.7 / 11.1
+// The rule is within 1.4 us of the best of them, here and at seven sizes between.  (A fork that is not in
+// place copies the pool's counts: 1.1 us more at most.)
 int ctas_for(int64_t blocks, int64_t rows, int max_blocks_per_seq) {
     const int64_t rounds = rows * ((max_blocks_per_seq + kRowLanes * kInFlight - 1) / (kRowLanes * kInFlight));
     if (blocks <= 8192 && rounds <= 64) return 1;

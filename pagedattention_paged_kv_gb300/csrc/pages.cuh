@@ -7,7 +7,7 @@
 namespace pkv {
 
 constexpr int kPageMaxSeqs = 16384;       // rows of a block table, forks or listed rows of a call
-constexpr int64_t kPageMaxBlocks = 1 << 22;  // pages of a pool: a bit (compact: two words in 32) of shared memory each
+constexpr int64_t kPageMaxBlocks = 1 << 22;  // pages of a pool: free and compact keep two words for 32 of them in shared memory
 
 // What the three kernels share: rows of block tables, their lengths, the counts of holders.  An
 // array and the one that replaces it (cached_lens / context_lens, ref_counts / new_ref_counts,
