@@ -2,6 +2,7 @@
 the arrays."""
 import numpy as np
 import pytest
+import torch
 
 import page_helpers as H
 import pagedattention_paged_kv_gb300 as pkv
@@ -45,3 +46,49 @@ def test_negative_counts_are_no_freed_pages(count, lens, in_place):
     got = call_free(p, rows, in_place)
     assert pkv.get_device_error() == pkv.DEVERR_BLOCK_ID
     same(got, (w_lens, w_refs, w_free, np.array([p.begin - len(gone)])))
+
+
+class Guarded:
+    """int32 tensors on the GPU with untouched words before and behind each."""
+
+    def __init__(self):
+        self.whole = []
+
+    def __call__(self, a):
+        a = np.asarray(a, np.int64).astype(np.int32)
+        x = torch.full((a.size + 128,), 77, dtype=torch.int32, device="cuda")
+        self.whole.append(x)
+        x[64:64 + a.size] = torch.from_numpy(a.reshape(-1)).cuda()
+        return x[64:64 + a.size].view(a.shape)
+
+    def intact(self):
+        return all((x[:64] == 77).all() and (x[-64:] == 77).all() for x in self.whole)
+
+
+@pytest.mark.parametrize("rows,pages", [(5, 40), (300, 9000), (40, 40000)])   # one CTA, a cluster of 4, of 16
+@pytest.mark.parametrize("seed", range(12))
+def test_any_contents_stay_inside_the_arrays(seed, rows, pages):
+    """Every array holds whatever memory may hold: small and huge numbers of both signs."""
+    r = np.random.Generator(np.random.PCG64([seed, rows]))
+    width, forks, bs = 30, 50, int(r.choice([8, 16, 64]))
+
+    def any_of(top, *shape):
+        x = r.integers(-3, top + 4, shape)
+        huge = r.integers(-2 ** 31, 2 ** 31, shape)
+        return np.where(r.random(shape) < (0.3 if seed % 2 else 0.02), huge, x)
+    g = Guarded()
+    t, lens, refs = g(any_of(pages, rows, width)), g(any_of(width * bs, rows)), g(any_of(3, pages))
+    lst, begin = g(any_of(pages, pages + 20)), g(any_of(pages, 1))
+    src, dst, some = g(any_of(rows, forks)), g(any_of(rows, forks)), g(any_of(rows, forks))
+    lens[::3] = 0
+    pairs, moves, count, end = g(np.zeros((forks, 2))), g(np.zeros((37, 2))), g([0]), g([0])
+    new_t, new_lens, new_refs = g(np.zeros((rows, width))), g(np.zeros(rows)), g(np.zeros(pages))
+    known = pkv.DEVERR_SEQ | pkv.DEVERR_CONTEXT_LEN | pkv.DEVERR_BLOCK_ID | pkv.DEVERR_FREE_BLOCKS
+    for _ in range(2):
+        pkv.fork_pages(t, new_lens, new_refs, pairs, end, lens, refs, lst, begin, src, dst, bs)
+        pkv.fork_pages(t, lens, refs, pairs, begin, lens, refs, lst, begin, src, dst, bs)
+        pkv.compact_pages(new_t, new_refs, moves, count, lst, end, t, lens, refs, bs)
+        pkv.free_pages(new_lens, new_refs, lst, end, t, lens, refs, begin, some, bs)
+        pkv.free_pages(lens, refs, lst, begin, t, lens, refs, begin, some, bs)
+        pkv.compact_pages(t, refs, moves, count, lst, end, t, lens, refs, bs)
+        assert pkv.get_device_error() & ~known == 0 and g.intact()
